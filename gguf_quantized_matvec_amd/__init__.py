@@ -23,7 +23,8 @@ EXPORTS = ("qmv_act_bytes", "quantize_act_q8_0", "qmv_launch", "qmv_launch_group
            "qmv_partials_launch", "qmm_partials_launch", "qmv_launch_noalloc", "qmv_gateup_act_bytes",
            "qmv_launch_gateup_swiglu", "qmv_launch_gateup_swiglu_q8", "qmv_act_bytes_q8k", "quantize_act_q8_k", "qmv_launch_q8k",
            "qmv_launch_gateup_swiglu_q8k", "qmv_launch_group_q8k", "qmm_launch_q8k", "qmv_partials_q8k_launch", "qmv_prepared_bytes", "qmv_prepare",
-           "qmm_launch_q8k_prepared", "qmm_partials_q8k_prepared_launch", "qmv_strerror")
+           "qmm_launch_q8k_prepared", "qmm_partials_q8k_prepared_launch", "qmv_add_rmsnorm_q8_0", "qmv_add_rmsnorm_q8_k",
+           "qmv_kv_bytes", "qmv_kv_append", "qmv_kv_read", "qmv_kv_attention_bytes", "qmv_kv_attention", "qmv_strerror")
 MAX_BATCH = 16
 MAX_GROUP = 8
 
@@ -32,6 +33,20 @@ class Gemv(ctypes.Structure):
     """struct qmv_gemv: one GEMV of qmv_launch_group (pointers as integers)."""
     _fields_ = [("w", ctypes.c_void_p), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("x", ctypes.c_void_p), ("xq", ctypes.c_void_p), ("y", ctypes.c_void_p)]
+
+
+class KvStruct(ctypes.Structure):
+    """struct qmv_kv: a layer's paged 4-bit cache (pointer as integer)."""
+    _fields_ = [("pages", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("page_tokens", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32)]
+
+
+class KvBatchStruct(ctypes.Structure):
+    """struct qmv_kv_batch: the sequences of one call (pointers as integers)."""
+    _fields_ = [("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("lens", ctypes.c_void_p), ("q_start", ctypes.c_void_p), ("B", ctypes.c_int64),
+                ("T", ctypes.c_int64), ("max_len", ctypes.c_int64)]
 
 
 class QmvError(RuntimeError):
@@ -77,11 +92,22 @@ def lib() -> ctypes.CDLL:
         L.qmv_launch_gateup_swiglu_q8.argtypes = [I, P, P, I64, I64, P, I64, P, P, P, P]
         L.qmv_launch_gateup_swiglu_q8k.argtypes = [I, P, P, I64, I64, P, I64, P, P, P]
         L.qmv_launch_group_q8k.argtypes = [I, I64, ctypes.POINTER(Gemv), I, P]
+        F, KV, KB = ctypes.c_float, ctypes.POINTER(KvStruct), ctypes.POINTER(KvBatchStruct)
+        for f in ("qmv_add_rmsnorm_q8_0", "qmv_add_rmsnorm_q8_k"):
+            getattr(L, f).argtypes = [P, P, P, F, I64, I64, P, P, P, P]
+        L.qmv_kv_bytes.argtypes = [I64, I, I, I]
+        L.qmv_kv_bytes.restype = ctypes.c_size_t
+        L.qmv_kv_append.argtypes = [KV, KB, P, I64, I, P, I64, P, I64, P, I, I, P, P]
+        L.qmv_kv_read.argtypes = [KV, KB, P, P, P]
+        L.qmv_kv_attention_bytes.argtypes = [I64, I64, I, I, I, I64]
+        L.qmv_kv_attention_bytes.restype = ctypes.c_size_t
+        L.qmv_kv_attention.argtypes = [KV, KB, P, I64, I, F, I64, P, P, P]
         for f in ("quantize_act_q8_0", "qmv_launch", "qmv_launch_group", "qmm_launch",
                   "qmv_partials_launch", "qmm_partials_launch", "qmv_launch_noalloc",
                   "qmv_launch_gateup_swiglu", "qmv_launch_gateup_swiglu_q8", "quantize_act_q8_k", "qmv_launch_q8k",
                   "qmv_launch_gateup_swiglu_q8k", "qmv_launch_group_q8k", "qmm_launch_q8k", "qmv_partials_q8k_launch", "qmv_prepare",
-                  "qmm_launch_q8k_prepared", "qmm_partials_q8k_prepared_launch"):
+                  "qmm_launch_q8k_prepared", "qmm_partials_q8k_prepared_launch", "qmv_add_rmsnorm_q8_0",
+                  "qmv_add_rmsnorm_q8_k", "qmv_kv_append", "qmv_kv_read", "qmv_kv_attention"):
             getattr(L, f).restype = I
         L.qmv_strerror.argtypes = [I]
         L.qmv_strerror.restype = ctypes.c_char_p
@@ -209,6 +235,44 @@ def qmm_partials_q8k_prepared_launch(type: int, wp: int, N: int, K: int, xq: int
                                      P: int, stream: int = 0) -> None:
     _check(lib().qmm_partials_q8k_prepared_launch(type, wp, N, K, xq, M, P, stream),
            "qmm_partials_q8k_prepared_launch")
+
+
+def qmv_add_rmsnorm_q8_0(x: int, res, w: int, eps: float, rows: int, K: int, h, y, xq: int,
+                         stream: int = 0) -> None:
+    _check(lib().qmv_add_rmsnorm_q8_0(x, res, w, eps, rows, K, h, y, xq, stream),
+           "qmv_add_rmsnorm_q8_0")
+
+
+def qmv_add_rmsnorm_q8_k(x: int, res, w: int, eps: float, rows: int, K: int, h, y, xq: int,
+                         stream: int = 0) -> None:
+    _check(lib().qmv_add_rmsnorm_q8_k(x, res, w, eps, rows, K, h, y, xq, stream),
+           "qmv_add_rmsnorm_q8_k")
+
+
+def qmv_kv_bytes(n_pages: int, page_tokens: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib().qmv_kv_bytes(n_pages, page_tokens, kv_heads, head_dim))
+
+
+def qmv_kv_append(kv: KvStruct, seqs: KvBatchStruct, q: int, q_stride: int, q_heads: int, k: int,
+                  k_stride: int, v: int, v_stride: int, freq, rot: int, halves: int, q_out: int,
+                  stream: int = 0) -> None:
+    _check(lib().qmv_kv_append(kv, seqs, q, q_stride, q_heads, k, k_stride, v, v_stride, freq, rot,
+                               halves, q_out, stream), "qmv_kv_append")
+
+
+def qmv_kv_read(kv: KvStruct, seqs: KvBatchStruct, k: int, v: int, stream: int = 0) -> None:
+    _check(lib().qmv_kv_read(kv, seqs, k, v, stream), "qmv_kv_read")
+
+
+def qmv_kv_attention_bytes(T: int, B: int, q_heads: int, kv_heads: int, head_dim: int,
+                           max_len: int) -> int:
+    return int(lib().qmv_kv_attention_bytes(T, B, q_heads, kv_heads, head_dim, max_len))
+
+
+def qmv_kv_attention(kv: KvStruct, seqs: KvBatchStruct, q: int, q_stride: int, q_heads: int,
+                     scale: float, window: int, out: int, work: int, stream: int = 0) -> None:
+    _check(lib().qmv_kv_attention(kv, seqs, q, q_stride, q_heads, scale, window, out, work, stream),
+           "qmv_kv_attention")
 
 
 def qmv_strerror(code: int) -> str:
@@ -477,3 +541,228 @@ def partials_q8k_prepared(type: int, wp, N: int, K: int, xq, M: int, P=None, str
                                      _dev(xq, torch.uint8, "xq"), M, _dev(P, torch.int32, "P"),
                                      _stream(stream))
     return P
+
+
+# ------------------------------- norm into 8 bits, the paged 4-bit cache --
+
+class _On:
+    """The device and stream of a call on tensors of `device`: makes that
+    device current for the launch, allocates on the call's stream, and gives
+    the stream's handle.  stream: None (the device's current one), a torch
+    stream, or a handle."""
+
+    def __init__(self, device, stream):
+        import torch
+        self._guards = []
+        if torch.cuda.current_device() != device.index:
+            self._guards.append(torch.cuda.device(device))
+        if stream is None:
+            self.handle = torch.cuda.current_stream(device).cuda_stream
+        else:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=device)
+            self.handle = stream.cuda_stream
+            self._guards.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for g in self._guards:
+            g.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        for g in reversed(self._guards):
+            g.__exit__(*exc)
+        return False
+
+
+def _on(t, dtype, what, device):
+    """The address of a contiguous tensor of a type on a device."""
+    if t.device != device:
+        raise ValueError(f"{what} must be on {device}, got {t.device}")
+    return _dev(t, dtype, what)
+
+
+def _add_rmsnorm(q8k, x, w, eps, res, h, y, xq, stream):
+    import torch
+    f32 = torch.float32
+    if x.dim() != 2 or w.shape != x.shape[1:]:
+        raise ValueError(f"x must be [rows, K] and w [K], got {tuple(x.shape)} and {tuple(w.shape)}")
+    for t, what in ((res, "res"), (h, "h"), (y, "y")):
+        if t is not None and t.shape != x.shape:
+            raise ValueError(f"{what} must have x's shape {tuple(x.shape)}, got {tuple(t.shape)}")
+    if h is not None and res is None:
+        raise ValueError("h receives x + res: it goes with res")
+    rows, K = x.shape
+    xp = _dev(x, f32, "x")
+    dev = x.device
+    n = qmv_act_bytes_q8k(rows, K) if q8k else qmv_act_bytes(rows, K)
+    if n == 0:
+        raise ValueError(f"bad shape rows={rows} K={K}")
+    if xq is not None and xq.numel() < n:
+        raise ValueError(f"xq must hold {n} bytes, got {xq.numel()}")
+    with _On(dev, stream) as s:
+        if xq is None:
+            xq = torch.empty(n, dtype=torch.uint8, device=dev)
+        if h is None and res is not None:
+            h = torch.empty_like(x)
+        fn = qmv_add_rmsnorm_q8_k if q8k else qmv_add_rmsnorm_q8_0
+        fn(xp, None if res is None else _on(res, f32, "res", dev), _on(w, f32, "w", dev), eps, rows,
+           K, None if h is None else _on(h, f32, "h", dev),
+           None if y is None else _on(y, f32, "y", dev), _on(xq, torch.uint8, "xq", dev), s)
+    return h, xq
+
+
+def add_rmsnorm(x, w, eps, res=None, h=None, y=None, xq=None, stream=None):
+    """(h, xq): h = x + res (None without res; h may be x or res), and the
+    Q8_0 scratch of RMS norm(h) * w for matvec / matmul with x None.  x, res
+    f32 [rows, K], w f32 [K]; y, if given, receives the norm's f32 values."""
+    return _add_rmsnorm(False, x, w, eps, res, h, y, xq, stream)
+
+
+def add_rmsnorm_q8k(x, w, eps, res=None, h=None, y=None, xq=None, stream=None):
+    """add_rmsnorm with the Q8_K scratch (K % 256 == 0), for the Q8_K path."""
+    return _add_rmsnorm(True, x, w, eps, res, h, y, xq, stream)
+
+
+class KVCache:
+    """A layer's keys and values in 4 bits: pages, a uint8 device tensor of
+    whole pages (None: n_pages new ones), as qmv_kv describes them."""
+
+    def __init__(self, pages, page_tokens: int, kv_heads: int, head_dim: int, n_pages=None,
+                 device="cuda"):
+        import torch
+        one = qmv_kv_bytes(1, page_tokens, kv_heads, head_dim)
+        if one == 0:
+            raise ValueError(f"bad cache shape page_tokens={page_tokens} kv_heads={kv_heads} "
+                             f"head_dim={head_dim}")
+        if pages is None:
+            pages = torch.empty(one * n_pages, dtype=torch.uint8, device=device)
+        ptr = _dev(pages, torch.uint8, "pages")
+        if pages.numel() == 0 or pages.numel() % one:
+            raise ValueError(f"pages must be whole pages of {one} bytes, got {pages.numel()} bytes")
+        self.pages, self.kv_heads, self.head_dim = pages, kv_heads, head_dim
+        self.page_tokens = page_tokens
+        self.c = KvStruct(ptr, pages.numel() // one, page_tokens, kv_heads, head_dim)
+
+
+class KVBatch:
+    """The sequences of a call: table int32 [B, pages], lens int32 [B] (with the
+    call's own tokens), q_start int32 [B + 1] or None (one row a sequence), T
+    rows in all, max_len a bound of the lengths (None: what the table holds,
+    for a cache of page_tokens)."""
+
+    def __init__(self, table, lens, q_start=None, T=None, max_len=None, page_tokens=None):
+        import torch
+        i32 = torch.int32
+        if table.dim() != 2 or lens.shape != table.shape[:1]:
+            raise ValueError(f"table must be [B, pages] and lens [B], got {tuple(table.shape)} and "
+                             f"{tuple(lens.shape)}")
+        B, stride = table.shape
+        if q_start is not None and q_start.shape != (B + 1,):
+            raise ValueError(f"q_start must be [{B + 1}], got {tuple(q_start.shape)}")
+        if T is None:
+            if q_start is not None:
+                raise ValueError("T, the number of rows, goes with q_start")
+            T = B
+        if max_len is None:
+            if page_tokens is None:
+                raise ValueError("give max_len, or page_tokens for all that the table can name")
+            max_len = stride * page_tokens
+        dev = table.device
+        self.c = KvBatchStruct(_dev(table, i32, "table"), stride, _on(lens, i32, "lens", dev),
+                               None if q_start is None else _on(q_start, i32, "q_start", dev),
+                               B, T, max_len)
+        self.table, self.lens, self.q_start = table, lens, q_start
+        self.B, self.T, self.max_len = B, T, max_len
+
+
+def _rows(t, T, width, what, device):
+    """(address, row stride) of T rows of `width` f32 with adjacent elements."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
+        raise ValueError(f"{what} must be a tensor on {device}")
+    if t.dtype != torch.float32:
+        raise TypeError(f"{what} must be torch.float32, got {t.dtype}")
+    if t.dim() != 2 or t.shape != (T, width) or t.stride(1) != 1:
+        raise ValueError(f"{what} must be [{T}, {width}] with adjacent elements, got "
+                         f"{tuple(t.shape)} with strides {t.stride()}")
+    return t.data_ptr(), t.stride(0) if T > 1 else max(width, t.stride(0))
+
+
+def _heads(q, cache, what="q"):
+    if q.dim() != 2 or q.shape[1] % cache.head_dim:
+        raise ValueError(f"{what} must be [T, heads * {cache.head_dim}], got {tuple(q.shape)}")
+    return q.shape[1] // cache.head_dim
+
+
+def _here(cache, batch):
+    dev = cache.pages.device
+    if batch.table.device != dev:
+        raise ValueError(f"table must be on {dev}, got {batch.table.device}")
+    return dev
+
+
+def kv_append(cache: KVCache, batch: KVBatch, q, k, v, freq=None, halves: bool = False, q_out=None,
+              stream=None):
+    """Rotates q [T, q_heads * D] and k [T, kv_heads * D] by their positions
+    (freq f64 [rot / 2], None: no rotation) and appends k and v to the cache.
+    Returns the rotated q (q_out, or a new tensor, whose skipped rows are
+    not written)."""
+    import torch
+    dev, T = _here(cache, batch), batch.T
+    heads, width = _heads(q, cache), cache.kv_heads * cache.head_dim
+    qp, qs = _rows(q, T, q.shape[1], "q", dev)
+    kp, ks = _rows(k, T, width, "k", dev)
+    vp, vs = _rows(v, T, width, "v", dev)
+    if q_out is not None and q_out.shape != q.shape:
+        raise ValueError(f"q_out must have q's shape {tuple(q.shape)}, got {tuple(q_out.shape)}")
+    rot, fp = 0, None
+    if freq is not None:
+        rot, fp = 2 * freq.numel(), _on(freq, torch.float64, "freq", dev)
+    with _On(dev, stream) as s:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.float32, device=dev)
+        qmv_kv_append(cache.c, batch.c, qp, qs, heads, kp, ks, vp, vs, fp, rot, int(halves),
+                      _on(q_out, torch.float32, "q_out", dev), s)
+    return q_out
+
+
+def kv_read(cache: KVCache, batch: KVBatch, k=None, v=None, stream=None):
+    """(k, v) [T, kv_heads * D] f32: the values held for the rows' tokens."""
+    import torch
+    dev = _here(cache, batch)
+    shape = (batch.T, cache.kv_heads * cache.head_dim)
+    for t, what in ((k, "k"), (v, "v")):
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{what} must be {shape}, got {tuple(t.shape)}")
+    with _On(dev, stream) as s:
+        if k is None:
+            k = torch.empty(shape, dtype=torch.float32, device=dev)
+        if v is None:
+            v = torch.empty(shape, dtype=torch.float32, device=dev)
+        qmv_kv_read(cache.c, batch.c, _on(k, torch.float32, "k", dev),
+                    _on(v, torch.float32, "v", dev), s)
+    return k, v
+
+
+def kv_attention(cache: KVCache, batch: KVBatch, q, scale: float, window: int = 0, out=None,
+                 work=None, stream=None):
+    """out [T, q_heads * D] f32: causal attention of the rows q over the cache
+    (window: only the last `window` positions; 0: all)."""
+    import torch
+    dev, T = _here(cache, batch), batch.T
+    heads = _heads(q, cache)
+    qp, qs = _rows(q, T, q.shape[1], "q", dev)
+    if out is not None and out.shape != q.shape:
+        raise ValueError(f"out must have q's shape {tuple(q.shape)}, got {tuple(out.shape)}")
+    n = qmv_kv_attention_bytes(T, batch.B, heads, cache.kv_heads, cache.head_dim, batch.max_len)
+    if work is not None and work.numel() < n:
+        raise ValueError(f"work must hold {n} bytes, got {work.numel()}")
+    with _On(dev, stream) as s:
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.float32, device=dev)
+        if work is None:
+            work = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
+        qmv_kv_attention(cache.c, batch.c, qp, qs, heads, scale, window,
+                         _on(out, torch.float32, "out", dev), _on(work, torch.uint8, "work", dev), s)
+    return out

@@ -20,6 +20,9 @@ SOURCES = [(os.path.join(CSRC, "qmv_kernels.hip"), ["-mllvm", "-amdgpu-mfma-vgpr
            (os.path.join(CSRC, "qmm_kernels.hip"), []),
            (os.path.join(CSRC, "qmm8k_kernels.hip"), []),
            (os.path.join(CSRC, "qmv_noalloc.hip"), []),
+           (os.path.join(CSRC, "qmv_norm.hip"), []),
+           (os.path.join(CSRC, "qmv_kv.hip"), []),
+           (os.path.join(CSRC, "qmv_step_api.cpp"), []),
            (os.path.join(CSRC, "qmv_api.cpp"), [])]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

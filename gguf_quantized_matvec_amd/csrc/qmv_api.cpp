@@ -4,11 +4,9 @@
 // call has no effect at all.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
-#include <string.h>
-
-#include <atomic>
 
 #include "../../include/qmv.h"
+#include "qmv_device.h"
 #include "qmv_internal.h"
 
 namespace {
@@ -27,7 +25,9 @@ int elems_per_block(int type) {
     return 0;
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+using qmv::aligned;
+using qmv::check_device;
+using qmv::launched;
 
 int check_weights(int type, const void* w, int64_t N, int64_t K) {
     const int qk = elems_per_block(type);
@@ -36,25 +36,6 @@ int check_weights(int type, const void* w, int64_t N, int64_t K) {
     if (!w || !aligned(w, 16)) return QMV_EINVAL_PTR;
     return QMV_OK;
 }
-
-// Cached per device: 1 = gfx950, 2 = something else.
-std::atomic<int> g_dev_ok[64];
-
-int check_device() {
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0) return QMV_EUNSUPPORTED_DEVICE;
-    if (dev < 64) {
-        const int v = g_dev_ok[dev].load(std::memory_order_relaxed);
-        if (v) return v == 1 ? QMV_OK : QMV_EUNSUPPORTED_DEVICE;
-    }
-    hipDeviceProp_t prop;
-    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return QMV_EUNSUPPORTED_DEVICE;
-    const bool ok = strncmp(prop.gcnArchName, "gfx950", 6) == 0;
-    if (dev < 64) g_dev_ok[dev].store(ok ? 1 : 2, std::memory_order_relaxed);
-    return ok ? QMV_OK : QMV_EUNSUPPORTED_DEVICE;
-}
-
-int launched(int hip_rc) { return hip_rc == 0 ? QMV_OK : QMV_ELAUNCH; }
 
 // Shared front half of qmv_launch / qmm_launch.
 int matmul_common(int type, const void* w, int64_t N, int64_t K, const float* x, int64_t rows,

@@ -363,6 +363,121 @@ int qmm_partials_q8k_prepared_launch(int type, const void* wp, int64_t N, int64_
 int qmv_launch_noalloc(int type, const void* w, int64_t N, int64_t K, const float* x,
                        int64_t B, float* y, void* stream);
 
+/* ---- The operators around the products of a decode or prefill step ----
+ * A block of the llama family ("Models and formats", architectures table)
+ * runs, around the products above: the residual addition with RMS norm, whose
+ * result the next products take as 8-bit activations; the rotation of q and k
+ * by position with the append of k and v to the cache; and the attention over
+ * the cache.  The same rules hold: the caller owns every buffer, nothing is
+ * allocated or synchronised, every check of the arguments comes before
+ * anything is enqueued. */
+
+/* Residual addition, RMS norm and quantisation in one launch:
+ *   h = x + res            (f32; without res, h below stands for x)
+ *   y_i = (float)(h_i r w_i),  r = 1/sqrt(sum h^2 / K + eps)   (in f64)
+ * and y quantised into xq exactly as quantize_act_q8_0 (rows, K; xq
+ * qmv_act_bytes(rows, K) bytes) or quantize_act_q8_k (K % 256 == 0; xq
+ * qmv_act_bytes_q8k(rows, K) bytes) would, staging included, so that the
+ * products of that path for these rows take it with x = NULL.  x, res
+ * [rows][K], w [K] f32, 4-byte aligned (16-byte aligned is faster); 1 <= rows
+ * <= 2^24, 0 <= eps <= 1.  res and h are given together or both NULL; h
+ * [rows][K] receives the sum and may be x or res itself.  y [rows][K], if not
+ * NULL, receives y before its quantisation; it, xq and w overlap nothing
+ * else.  The order of every sum depends on K alone: a row's bits do not
+ * depend on the rows beside it. */
+int qmv_add_rmsnorm_q8_0(const float* x, const float* res, const float* w, float eps,
+                         int64_t rows, int64_t K, float* h, float* y, void* xq, void* stream);
+int qmv_add_rmsnorm_q8_k(const float* x, const float* res, const float* w, float eps,
+                         int64_t rows, int64_t K, float* h, float* y, void* xq, void* stream);
+
+/* A layer's keys and values held in 4 bits, in pages of page_tokens tokens (a
+ * power of two, 16..1024).  Each key or value head is held as Q4_0 values:
+ * per 32 elements m = the value of the largest magnitude (the first of
+ * equals), d = m / -8, id = 1/d (0 when not finite), code = min(15,
+ * trunc((x id) + 8.5)) with both operations in f32, stored fp16(d); value
+ * d * (code - 8).  A block with a NaN or an infinity gets d = NaN.  head_dim:
+ * a multiple of 32, 32..256 (nb = head_dim / 32); 1 <= kv_heads <=
+ * QMV_KV_MAX_HEADS.  pages: qmv_kv_bytes(...) bytes, 16-byte aligned; need
+ * not be cleared.  Head h of page p is the page_tokens * 36 nb bytes at (p *
+ * kv_heads + h) * page_tokens * 36 nb:
+ *   K codes  [token][g = 0..3][b][4 bytes]: the eight nibbles (low first) hold
+ *            elements 0, 2, 4, 6, 1, 3, 5, 7 of 32b + 8g ...
+ *   V codes  [token / 4][m = 0..15][b][token % 4]: low nibble element 32b +
+ *            2m, high nibble element 32b + 2m + 1
+ *   K scales [token][b] fp16, V scales [token][b] fp16. */
+#define QMV_KV_MAX_HEADS 1024
+#define QMV_KV_MAX_ROWS (1 << 20)
+#define QMV_KV_MAX_LEN (1 << 30)
+typedef struct qmv_kv {
+    void* pages;
+    int64_t n_pages;
+    int32_t page_tokens, kv_heads, head_dim;
+} qmv_kv;
+
+/* The sequences of a call, in device memory (read when the work runs, so a
+ * captured launch follows their contents): sequence b holds lens[b] tokens,
+ * the call's own among them, position p in page table[b * table_stride + p /
+ * page_tokens]; its rows are q_start[b] .. q_start[b + 1] - 1 of the T rows
+ * of the call (q_start [B + 1], ascending from 0) and stand at its last
+ * positions.  q_start NULL: one row a sequence, T == B.  Rows from
+ * q_start[B] on belong to no sequence and are left alone, outputs included.
+ * A length of 0 is a sequence without tokens.  max_len (1..2^30, at most
+ * table_stride * page_tokens) bounds the lengths, and sizes the launch and the
+ * workspace.  1 <= B, T <= QMV_KV_MAX_ROWS.
+ * These contents are not checked on the host.  Whatever they hold, nothing
+ * outside the described buffers is touched: a length is cut to max_len, a
+ * page number out of range holds no token (an append drops it, attention does
+ * not see it), a run of rows outside the T rows is empty. */
+typedef struct qmv_kv_batch {
+    const int32_t* table;
+    int64_t table_stride;
+    const int32_t* lens;
+    const int32_t* q_start;
+    int64_t B, T, max_len;
+} qmv_kv_batch;
+
+/* Bytes of the pages of a cache; 0 for an invalid shape. */
+size_t qmv_kv_bytes(int64_t n_pages, int page_tokens, int kv_heads, int head_dim);
+
+/* Rotates q and k by their positions and appends k and v to the cache, in one
+ * launch.  q: T rows of q_heads * head_dim f32, q_stride floats apart; k, v:
+ * T rows of kv_heads * head_dim, k_stride / v_stride apart (so the three may
+ * be parts of one buffer); q_heads a multiple of kv_heads, at most
+ * QMV_KV_MAX_HEADS.  The first rot elements (even, 0..head_dim) of each head
+ * turn in pairs, (2i, 2i + 1), or with halves != 0 (i, i + rot / 2), by the
+ * angle position * freq[i] (freq [rot / 2] f64 radians, 8-byte aligned, NULL
+ * when rot is 0): angle, sine, cosine and products in f64, rounded once to
+ * f32.  q_out [T][q_heads * head_dim] receives the rotated q (it may be q
+ * itself when q_stride is that row); the rotated k and v are quantised into
+ * the pages.  A row whose position is negative is skipped, q_out included;
+ * one whose page is out of range writes only its q_out.  Every position
+ * written must lie in a page that no other sequence of the call writes.
+ * Other tokens of the pages keep their bytes. */
+int qmv_kv_append(const qmv_kv* kv, const qmv_kv_batch* seqs, const float* q, int64_t q_stride,
+                  int q_heads, const float* k, int64_t k_stride, const float* v, int64_t v_stride,
+                  const double* freq, int rot, int halves, float* q_out, void* stream);
+
+/* The values held for each row's token: k, v [T][kv_heads * head_dim] f32.
+ * Rows without a token or a page are left alone. */
+int qmv_kv_read(const qmv_kv* kv, const qmv_kv_batch* seqs, float* k, float* v, void* stream);
+
+/* Bytes of workspace of qmv_kv_attention; 0 for an invalid shape.  It does
+ * not shrink as T, B or max_len grow. */
+size_t qmv_kv_attention_bytes(int64_t T, int64_t B, int q_heads, int kv_heads, int head_dim,
+                              int64_t max_len);
+
+/* Causal attention over the cache: for each row (at position p) and query
+ * head, out = sum_t softmax_t(scale * q . k[t]) v[t] over the sequence's
+ * positions t with p - window < t <= p (window 0: all t <= p); 0 for a row
+ * that sees no position.  Query heads j * (q_heads / kv_heads) ... read
+ * key/value head j.  q: T rows of q_heads * head_dim f32, q_stride floats
+ * apart (a multiple of 4), 16-byte aligned; out [T][q_heads * head_dim],
+ * 16-byte aligned, not q; work: qmv_kv_attention_bytes(T, B, ...) bytes,
+ * 16-byte aligned, used by one call at a time; 0 < scale <= 1e6. */
+int qmv_kv_attention(const qmv_kv* kv, const qmv_kv_batch* seqs, const float* q, int64_t q_stride,
+                     int q_heads, float scale, int64_t window, float* out, void* work,
+                     void* stream);
+
 /* Static text for a status code. */
 const char* qmv_strerror(int code);
 

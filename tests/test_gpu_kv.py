@@ -1,0 +1,445 @@
+"""The paged 4-bit cache on the GPU: append with rotation, read back,
+attention, against the definitions in 64 bits."""
+import numpy as np
+import pytest
+
+from step_ref import attention, decode_page, encode_page, q4_0, q4_value, rotate
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def g():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import gguf_quantized_matvec_amd as g
+    g.lib()
+    return g
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+class Case:
+    """A cache with pages in no order, sequences of `lens` tokens whose last `ns` are a call's rows."""
+
+    def __init__(self, lens, ns, page, hkv, d, seed, spare_rows=0, spare_pages=2, spare_table=1):
+        self.rng = np.random.default_rng(seed)
+        self.lens, self.ns, self.page, self.hkv, self.d, self.nb = lens, ns, page, hkv, d, d // 32
+        self.B = len(lens)
+        need = [-(-n // page) for n in lens]
+        self.n_pages = sum(need) + spare_pages
+        order = self.rng.permutation(self.n_pages)
+        self.table = np.full((self.B, max(need + [1]) + spare_table), -7, np.int32)
+        at = 0
+        for b, m in enumerate(need):
+            self.table[b, :m] = order[at:at + m]
+            at += m
+        self.spare = order[at:]
+        self.starts = np.concatenate([[0], np.cumsum(ns)]).astype(np.int32)
+        self.rows = int(self.starts[-1])
+        self.T = self.rows + spare_rows
+        self.pos = np.concatenate([np.arange(n - m, n) for n, m in zip(lens, ns)] or [[]]).astype(np.int64)
+        self.seq = np.repeat(np.arange(self.B), ns)
+        self.head_bytes = page * 36 * self.nb
+
+    def batch(self, g, max_len=None, starts=True):
+        return g.KVBatch(dev(self.table), dev(np.array(self.lens, np.int32)),
+                         dev(self.starts) if starts else None, self.T if starts else None,
+                         max_len or max(self.lens + [1]))
+
+    def cells(self, raw):
+        return raw.reshape(self.n_pages, self.hkv, self.head_bytes)
+
+    def token(self, raw, b, p):
+        """(K codes, K d, V codes, V d) of a token, [hkv, ...]."""
+        page = self.cells(raw)[self.table[b, p // self.page]]
+        parts = [decode_page(page[h], self.page, self.nb) for h in range(self.hkv)]
+        return [np.stack([x[i][p % self.page] for x in parts]) for i in range(4)]
+
+
+def nasty(rng, shape):
+    """Keys and values with zero blocks, ties of the largest magnitude and very small ones."""
+    x = rng.standard_normal(shape).astype(np.float32)
+    f = x.reshape(-1, 32)
+    kind = rng.integers(0, 9, len(f))
+    f[kind == 0] = 0
+    f[kind == 1] *= np.float32(1e-6)
+    tie = kind == 2
+    f[tie, 5], f[tie, 21] = 4.0, -4.0
+    f[kind == 3, 31] = 300.0
+    f[kind == 4] *= np.float32(1e-40)  # 1/d is not finite: codes 8, d 0
+    return x
+
+
+APPENDS = [
+    # lens, rows of each, page, q heads, kv heads, d, rot, halves
+    ([1], [1], 16, 1, 1, 32, 32, False),
+    ([777], [1], 64, 32, 8, 128, 128, False),
+    ([5, 40, 16, 17], [1, 1, 1, 1], 16, 14, 2, 64, 64, True),
+    ([33, 5, 100], [33, 3, 70], 32, 6, 3, 96, 48, True),
+    ([50, 30, 0, 20], [20, 0, 0, 20], 16, 5, 1, 160, 160, False),
+    ([130], [130], 64, 4, 4, 256, 128, False),
+    ([9, 31], [9, 17], 16, 2, 1, 224, 0, False),
+    ([20], [20], 16, 3, 1, 192, 192, True),
+]
+
+
+@pytest.mark.parametrize("lens,ns,page,hq,hkv,d,rot,halves", APPENDS)
+def test_append(g, lens, ns, page, hq, hkv, d, rot, halves):
+    print("append", lens, ns, page, hq, hkv, d, rot, halves, flush=True)
+    c = Case(lens, ns, page, hkv, d, 3, spare_rows=3)
+    rng = c.rng
+    q = rng.standard_normal((c.T, hq * d)).astype(np.float32)
+    k, v = nasty(rng, (c.T, hkv * d)), nasty(rng, (c.T, hkv * d))
+    freq = 10000.0 ** (-np.arange(0, rot, 2) / max(rot, 1))
+    before = rng.integers(0, 256, c.n_pages * hkv * c.head_bytes, dtype=np.uint8)
+    pages = dev(before)
+    cache, batch = g.KVCache(pages, page, hkv, d), c.batch(g)
+    # the three as parts of one buffer, with its row stride
+    width = (hq + 2 * hkv) * d + 4
+    both = torch.zeros(c.T, width, device="cuda")
+    qd, kd, vd = both[:, :hq * d], both[:, hq * d:(hq + hkv) * d], both[:, (hq + hkv) * d:(hq + 2 * hkv) * d]
+    qd.copy_(dev(q)); kd.copy_(dev(k)); vd.copy_(dev(v))
+    out = torch.full((c.T, hq * d), 7.0, device="cuda")
+    g.kv_append(cache, batch, qd, kd, vd, dev(freq) if rot else None, halves=halves, q_out=out)
+    torch.cuda.synchronize()
+    got, raw = out.cpu().numpy(), pages.cpu().numpy()
+    n = c.rows
+    # the rotated q: one rounding of what f64 holds to far below an f32 step (a few of its own
+    # roundings of the two products)
+    want = rotate(q[:n].reshape(n, hq, d), c.pos, freq, halves).reshape(n, -1)
+    assert np.all(np.abs(got[:n] - want) <= 2.0 ** -24 * np.abs(want) + 2.0 ** -45)
+    assert np.all(got[n:] == 7.0)  # rows of no sequence
+    kr = rotate(k[:n].reshape(n, hkv, d), c.pos, freq, halves).astype(np.float32)
+    kc, ks = q4_0(kr)
+    vc, vs = q4_0(v[:n].reshape(n, hkv, d))
+    touched = np.zeros(c.cells(raw).shape, bool)
+    for i in range(n):
+        a = c.token(raw, c.seq[i], c.pos[i])
+        for x, y in zip(a, (kc[i], ks[i], vc[i], vs[i])):
+            assert np.array_equal(x, y), (i, x, y)
+        p = int(c.pos[i]) % page
+        cell = touched[c.table[c.seq[i], c.pos[i] // page]]
+        kcode = np.zeros((page, c.nb, 32), int)
+        kcode[p] = 15
+        half = np.zeros((page, c.nb), np.float16)
+        half.view(np.uint16)[p] = 0xFFFF
+        cell |= encode_page(kcode, half, kcode, half, page, c.nb) != 0
+    now, was = c.cells(raw), c.cells(before)
+    assert np.array_equal(now[~touched], was[~touched])  # every other token's bytes
+    # what a reader sees
+    rk = torch.full((c.T, hkv * d), 5.0, device="cuda")
+    rv = rk.clone()
+    g.kv_read(cache, batch, rk, rv)
+    assert np.array_equal(rk.cpu().numpy()[:n], q4_value(kc, ks).reshape(n, -1).astype(np.float32))
+    assert np.array_equal(rv.cpu().numpy()[:n], q4_value(vc, vs).reshape(n, -1).astype(np.float32))
+    assert torch.all(rk[n:] == 5.0) and torch.all(rv[n:] == 5.0)
+    # q in place
+    q2 = dev(q)
+    g.kv_append(cache, batch, q2, dev(k), dev(v), dev(freq) if rot else None, halves=halves, q_out=q2)
+    assert torch.equal(q2[:n], out[:n]) and torch.equal(q2[n:], dev(q)[n:])
+    assert np.array_equal(pages.cpu().numpy(), raw)
+
+
+def test_append_is_the_sum_of_its_parts(g):
+    """A prompt appended at once, in two calls, and token by token: the same bytes."""
+    hq, hkv, d, page, n = 4, 2, 64, 16, 37
+    rng = np.random.default_rng(1)
+    q, k, v = (dev(rng.standard_normal((n, h * d)).astype(np.float32)) for h in (hq, hkv, hkv))
+    freq = dev(10000.0 ** (-np.arange(0, d, 2) / d))
+    table = dev(np.array([[2, 0, 1]], np.int32))
+    got = []
+    for cuts in ([n], [20, 17], [1] * n):
+        cache = g.KVCache(torch.zeros(3 * hkv * page * 72, dtype=torch.uint8, device="cuda"), page, hkv, d)
+        out, at = [], 0
+        for m in cuts:
+            batch = g.KVBatch(table, dev(np.array([at + m], np.int32)), dev(np.array([0, m], np.int32)), m, 48)
+            out.append(g.kv_append(cache, batch, q[at:at + m], k[at:at + m], v[at:at + m], freq))
+            at += m
+        got.append((torch.cat(out), cache.pages))
+    for o, p in got[1:]:
+        assert torch.equal(o, got[0][0]) and torch.equal(p, got[0][1])
+
+
+def test_append_far_position_and_bad_values(g):
+    """Position 10^6: the angle keeps its low bits.  A block with a NaN or an infinity reads as NaN,
+    its neighbours do not."""
+    d, page = 64, 1024
+    pos = 10 ** 6
+    table = np.full((1, pos // page + 1), -1, np.int32)
+    table[0, pos // page] = 0
+    freq = 10000.0 ** (-np.arange(0, d, 2) / d)
+    rng = np.random.default_rng(2)
+    q, k, v = (rng.standard_normal((1, d)).astype(np.float32) for _ in range(3))
+    v[0, 3], v[0, 40] = np.nan, -np.inf
+    cache = g.KVCache(None, page, 1, d, n_pages=1)
+    batch = g.KVBatch(dev(table), dev(np.array([pos + 1], np.int32)), max_len=pos + 1)
+    out = g.kv_append(cache, batch, dev(q), dev(k), dev(v), dev(freq)).cpu().numpy()
+    want = rotate(q.reshape(1, 1, d), np.array([pos]), freq, False).reshape(1, d)
+    # the angle, about 10^6, is held to 2^-33 at worst (its f64 rounding): 2^-32 on values of about 1
+    assert np.all(np.abs(out - want) <= 2.0 ** -24 * np.abs(want) + 2.0 ** -31)
+    _, rv = g.kv_read(cache, batch)
+    rv = rv.cpu().numpy()
+    assert np.all(np.isnan(rv))  # one block holds the NaN, the other the infinity
+    v2 = v.copy()
+    v2[0, 40] = 1.0
+    g.kv_append(cache, batch, dev(q), dev(k), dev(v2), dev(freq))
+    rk, rv = (x.cpu().numpy() for x in g.kv_read(cache, batch))
+    assert np.all(np.isnan(rv[0, :32])) and np.all(np.isfinite(rv[0, 32:])) and np.all(np.isfinite(rk))
+
+
+def test_untrusted_tables(g):
+    """Pages out of range, lengths of zero, below zero and beyond the table, runs of rows outside the
+    call: nothing else is touched, and what is named is right."""
+    hq, hkv, d, page = 2, 1, 64, 16
+    rng = np.random.default_rng(4)
+    size = 2 * page * 72
+    pages = torch.full((size,), 9, dtype=torch.uint8, device="cuda")
+    cache = g.KVCache(pages, page, hkv, d)
+    table = np.array([[0, 1], [2, -1], [1 << 30, 5], [-(1 << 31), 1]], np.int32)
+    q, k, v = (dev(rng.standard_normal((4, h * d)).astype(np.float32)) for h in (hq, hkv, hkv))
+    freq = dev(10000.0 ** (-np.arange(0, d, 2) / d))
+    out = torch.full((4, hq * d), 3.0, device="cuda")
+    for lens in ([0, 5, 5, 5], [-3, 17, 30, 2], [-(1 << 31), 1, 16, 16]):
+        batch = g.KVBatch(dev(table), dev(np.array(lens, np.int32)), max_len=32)
+        g.kv_append(cache, batch, q, k, v, freq, q_out=out)
+        assert torch.all(pages == 9)
+        assert torch.all(out[0] == 3.0)  # no position
+        rk = torch.full((4, hkv * d), 4.0, device="cuda")
+        g.kv_read(cache, batch, rk, rk.clone())
+        assert torch.all(rk == 4.0)
+        o = g.kv_attention(cache, batch, q, 0.125)
+        assert torch.all(o == 0.0)  # rows that see no position
+    # lengths beyond max_len are cut to it: the row stands at position 31, in page 1
+    batch = g.KVBatch(dev(table), dev(np.array([2 ** 31 - 1, 0, 0, 0], np.int32)), max_len=32)
+    g.kv_append(cache, batch, q, k, v, freq, q_out=out)
+    assert torch.all(pages[:page * 72] == 9) and not torch.all(pages == 9)
+    # runs of rows outside the call, and not in order
+    for starts in ([0, 5, 6, 7, 8], [-1, 2, 3, 4, 4], [4, 3, 2, 1, 0], [0, 2 ** 31 - 1, -(2 ** 31), 0, 0],
+                   [9, 9, 9, 9, 9]):
+        batch = g.KVBatch(dev(table), dev(np.array([9, 9, 9, 9], np.int32)), dev(np.array(starts, np.int32)), 4, 32)
+        g.kv_append(cache, batch, q, k, v, freq, q_out=out)
+        g.kv_read(cache, batch, rk, rk.clone())
+        g.kv_attention(cache, batch, q, 0.125, out=out)
+    torch.cuda.synchronize()
+
+
+def test_streams_and_capture(g):
+    """append + attention captured once; lengths, tables and inputs change between the replays."""
+    B, hq, hkv, d, page = 3, 4, 2, 64, 16
+    rng = np.random.default_rng(6)
+    freq = dev(10000.0 ** (-np.arange(0, d, 2) / d))
+    table = dev(rng.permutation(B * 40).reshape(B, 40).astype(np.int32))
+    lens = dev(np.ones(B, np.int32))
+    q, k, v = (torch.zeros(B, h * d, device="cuda") for h in (hq, hkv, hkv))
+    cache = g.KVCache(torch.zeros(B * 40 * hkv * page * 72, dtype=torch.uint8, device="cuda"), page, hkv, d)
+    other = g.KVCache(torch.zeros_like(cache.pages), page, hkv, d)
+    batch = g.KVBatch(table, lens, max_len=640)
+    qr, out = torch.empty_like(q), torch.empty_like(q)
+    work = torch.empty(max(16, g.qmv_kv_attention_bytes(B, B, hq, hkv, d, 640)), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        g.kv_append(cache, batch, q, k, v, freq, q_out=qr)
+        g.kv_attention(cache, batch, qr, 0.125, out=out, work=work)
+    cache.pages.zero_()
+    side = torch.cuda.Stream()
+    for step in range(30):
+        lens.copy_(dev(np.array([step + 1, 600 + step, 0 if step % 3 else 20 + step], np.int32)))
+        for t in (q, k, v):
+            t.copy_(dev(rng.standard_normal(tuple(t.shape)).astype(np.float32)))
+        work.fill_(255)
+        graph.replay()
+        if step % 5 == 0:
+            torch.cuda.synchronize()
+        side.wait_stream(torch.cuda.current_stream())
+        qs = g.kv_append(other, batch, q, k, v, freq, stream=side)
+        o = g.kv_attention(other, batch, qs, 0.125, stream=side.cuda_stream)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(cache.pages, other.pages)
+        assert torch.equal(out, o), step
+
+
+# ------------------------------------------------------------- attention --
+
+def filled(c, hq, dscale=1.0):
+    """Random pages in both forms: raw bytes, and per sequence K, V f64 [L, hkv, d]."""
+    rng = c.rng
+    cells = np.empty((c.n_pages, c.hkv, c.head_bytes), np.uint8)
+    ks, vs = (np.empty((c.n_pages, c.hkv, c.page, c.d)) for _ in range(2))
+    for i in range(c.n_pages):
+        for h in range(c.hkv):
+            kc, kd = q4_0(rng.standard_normal((c.page, c.d)).astype(np.float32))
+            vc, vd = q4_0((dscale * rng.standard_normal((c.page, c.d))).astype(np.float32))
+            cells[i, h] = encode_page(kc, kd, vc, vd, c.page, c.nb)
+            ks[i, h], vs[i, h] = q4_value(kc, kd), q4_value(vc, vd)
+
+    def of(x, b):
+        m = -(-c.lens[b] // c.page)
+        t = x[c.table[b, :m]].transpose(0, 2, 1, 3).reshape(m * c.page, c.hkv, c.d)
+        return t[:c.lens[b]]
+
+    return cells.reshape(-1), [of(ks, b) for b in range(c.B)], [of(vs, b) for b in range(c.B)]
+
+
+def bound(d, length, out, amax, pv):
+    """How far an f32 computation may be off.  A score is a sum of d products: each product and each
+    of at most d + 8 roundings (scaling and splitting q, the block scales, the sums) is off by half a
+    step of a magnitude below sum |q k| scale (amax, natural units), and exp adds 2^-22; both enter
+    every weight and their sum.  The weighted sums run over partial sums of at most 64 terms and
+    the runs of 512 keys; each is off by half a step of sum p |v|."""
+    delta = (d + 8) * 2.0 ** -24 * amax[..., None] + 2.0 ** -21
+    return (2 * delta + (80 + length / 512) * 2.0 ** -24) * pv + 1e-30
+
+
+ATTNS = [
+    # lens, rows of each, page, q heads, kv heads, d, window
+    ([1], [1], 16, 1, 1, 32, 0),
+    ([500], [1], 64, 14, 2, 64, 0),
+    ([129, 1, 128, 0, 511, 513, 1030], [1] * 7, 16, 8, 2, 128, 0),
+    ([700, 30], [1, 1], 32, 16, 1, 96, 100),
+    ([300], [1], 256, 20, 1, 128, 0),           # more query heads than one tile of rows
+    ([600], [1], 16, 33, 1, 64, 0),
+    ([130, 260], [1, 1], 64, 4, 2, 256, 0),
+    ([100], [1], 16, 3, 3, 160, 7),
+    ([70, 140], [1, 1], 16, 2, 1, 224, 0),
+    ([530], [1], 32, 7, 1, 192, 0),
+    ([65], [65], 16, 2, 2, 64, 0),              # a whole prompt
+    ([200, 17, 5, 600], [37, 0, 5, 100], 16, 6, 2, 64, 0),
+    ([540], [530], 64, 5, 1, 128, 60),
+    ([40, 33], [33, 33], 16, 3, 1, 32, 1),      # a window of the row's own position
+    ([3], [7], 16, 4, 2, 64, 0),                # more rows than tokens: the first see nothing
+    ([90], [50], 32, 1, 1, 256, 40),
+]
+
+
+@pytest.mark.parametrize("lens,ns,page,hq,hkv,d,window", ATTNS)
+def test_attention(g, lens, ns, page, hq, hkv, d, window):
+    print("attention", lens, ns, page, hq, hkv, d, window, flush=True)
+    c = Case(lens, ns, page, hkv, d, 11, spare_rows=0 if ns == [1] * len(ns) else 2)
+    raw, ks, vs = filled(c, hq)
+    q = (1.5 * c.rng.standard_normal((c.T, hq * d))).astype(np.float32)
+    scale = 1 / np.sqrt(d)
+    cache = g.KVCache(dev(raw), page, hkv, d)
+    one = ns == [1] * len(ns)
+    out = torch.full((c.T, hq * d), 7.0, device="cuda")
+    g.kv_attention(cache, c.batch(g, starts=not one), dev(q), scale, window=window, out=out)
+    got = out.cpu().numpy()
+    assert np.all(got[c.rows:] == 7.0)
+    check(c, got, q, ks, vs, hq, float(np.float32(scale)), window)
+    if one:  # the same rows named by starts
+        assert torch.equal(g.kv_attention(cache, c.batch(g), dev(q), scale, window=window), out)
+
+
+def check(c, got, q, ks, vs, hq, scale, window, seen=None):
+    for b in range(c.B):
+        lo, hi = c.starts[b], c.starts[b + 1]
+        if lo == hi:
+            continue
+        pos = np.arange(c.lens[b] - c.ns[b], c.lens[b])
+        want, amax, pv = attention(q[lo:hi].reshape(hi - lo, hq, c.d), ks[b], vs[b], pos, scale, window,
+                                   None if seen is None else seen[b])
+        x = got[lo:hi].reshape(hi - lo, hq, c.d)
+        assert np.all(x[pos < 0] == 0)
+        lim = bound(c.d, c.lens[b], want, amax, pv)
+        worst = np.max(np.abs(x - want) / lim)
+        assert np.all(np.abs(x - want) <= lim), (b, worst)
+
+
+@pytest.mark.parametrize("dscale", [1e-6, 1e-3, 1.0, 1e3, 6e4])
+def test_value_scales(g, dscale):
+    """Values of any size that fp16 scales hold keep their relative accuracy."""
+    c = Case([300, 40], [1, 1], 16, 2, 64, 12)
+    raw, ks, vs = filled(c, 4, dscale)
+    # and tokens with much larger or smaller values than their neighbours
+    q = (3 * c.rng.standard_normal((c.T, 4 * 64))).astype(np.float32)
+    got = g.kv_attention(g.KVCache(dev(raw), 16, 2, 64), c.batch(g), dev(q), 0.125).cpu().numpy()
+    check(c, got, q, ks, vs, 4, 0.125, 0)
+
+
+def test_masked_places_may_hold_anything(g):
+    """NaN and infinite scales behind the last token, in tokens a row does not see, and in pages that
+    the table does not name; a page out of range is not seen."""
+    hq, hkv, d, page = 4, 2, 64, 16
+    c = Case([150, 40], [30, 40], page, hkv, d, 13)
+    raw, ks, vs = filled(c, hq)
+    q = c.rng.standard_normal((c.T, hq * d)).astype(np.float32)
+    cells = c.cells(raw.copy())
+    half = page * 32 * c.nb
+
+    def spoil(b, p, bits):
+        cell = cells[c.table[b, p // page]]
+        for part in range(2):
+            at = half + part * page * 2 * c.nb + (p % page) * 2 * c.nb
+            cell[:, at:at + 2 * c.nb] = np.array([bits] * c.nb, np.uint16).view(np.uint8)
+
+    for p in range(150, 160):
+        spoil(0, p, 0x7E00)
+    for p in range(40, 48):
+        spoil(1, p, 0x7C00)
+    cells[c.spare] = 0xFF
+    cache = g.KVCache(dev(cells.reshape(-1)), page, hkv, d)
+    got = g.kv_attention(cache, c.batch(g), dev(q), 0.125).cpu().numpy()
+    check(c, got, q, ks, vs, hq, 0.125, 0)
+    # a NaN token spoils the rows that see it and no other
+    spoil(1, 20, 0x7E00)
+    cache = g.KVCache(dev(cells.reshape(-1)), page, hkv, d)
+    o = g.kv_attention(cache, c.batch(g), dev(q), 0.125).cpu().numpy()
+    assert np.array_equal(o[:50], got[:50]) and np.all(np.isnan(o[50:]))
+    o = g.kv_attention(cache, c.batch(g), dev(q), 0.125, window=5).cpu().numpy()
+    assert np.all(np.isfinite(o[:50])) and np.all(np.isnan(o[50:55])) and np.all(np.isfinite(o[55:]))
+    # a hole in the table
+    c.table[0, 3] = 1 << 20
+    c.table[1, 1] = -1
+    got = g.kv_attention(cache, c.batch(g), dev(q), 0.125).cpu().numpy()
+    seen = [np.ones(150, bool), np.ones(40, bool)]
+    seen[0][48:64] = False
+    seen[1][16:32] = False
+    check(c, got, q, ks, vs, hq, 0.125, 0, seen)
+
+
+def test_extreme_scores(g):
+    """Scores of hundreds, one key that takes all the weight, and rows of zeros (every weight equal)."""
+    c = Case([200], [4], 16, 1, 64, 14)
+    raw, ks, vs = filled(c, 2)
+    q = c.rng.standard_normal((c.T, 128)).astype(np.float32)
+    q[0] *= 300
+    q[1] = 0
+    q[2] *= np.float32(1e-20)
+    q[3, :64] *= np.float32(1e4)
+    got = g.kv_attention(g.KVCache(dev(raw), 16, 1, 64), c.batch(g), dev(q), 1.0).cpu().numpy()
+    check(c, got, q, ks, vs, 2, 1.0, 0)
+
+
+def test_shared_pages_and_offsets(g):
+    """Two sequences that share their first pages, and pages whose bytes lie beyond 2^32."""
+    hkv, d, page, hq = 8, 256, 1024, 8
+    one = hkv * page * 36 * 8
+    n_pages = (1 << 32) // one + 3
+    pages = torch.zeros(n_pages * one, dtype=torch.uint8, device="cuda")
+    c = Case([1100, 1030], [1, 1], page, hkv, d, 15, spare_pages=0)
+    raw, ks, vs = filled(c, hq)
+    last = n_pages - 1
+    cells = c.cells(raw)
+    table = np.zeros((2, 2), np.int32)
+    for i, (b, j) in enumerate([(0, 0), (0, 1), (1, 1)]):
+        to = last - i
+        pages[to * one:(to + 1) * one] = dev(cells[c.table[b, j]].reshape(-1))
+        table[b, j] = to
+    table[1, 0] = table[0, 0]
+    ks[1][:1024], vs[1][:1024] = ks[0][:1024], vs[0][:1024]
+    q = c.rng.standard_normal((2, hq * d)).astype(np.float32)
+    cache = g.KVCache(pages, page, hkv, d)
+    batch = g.KVBatch(dev(table), dev(np.array(c.lens, np.int32)), max_len=1100)
+    got = g.kv_attention(cache, batch, dev(q), 0.0625).cpu().numpy()
+    check(c, got, q, ks, vs, hq, 0.0625, 0)
+    # an append there
+    k, v = (c.rng.standard_normal((2, hkv * d)).astype(np.float32) for _ in range(2))
+    g.kv_append(cache, batch, dev(q), dev(k), dev(v))
+    rk, rv = g.kv_read(cache, batch)
+    assert np.array_equal(rk.cpu().numpy(), q4_value(*q4_0(k)).astype(np.float32))
+    assert np.array_equal(rv.cpu().numpy(), q4_value(*q4_0(v)).astype(np.float32))
