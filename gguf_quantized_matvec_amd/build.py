@@ -22,6 +22,7 @@ SOURCES = [(os.path.join(CSRC, "qmv_kernels.hip"), ["-mllvm", "-amdgpu-mfma-vgpr
            (os.path.join(CSRC, "qmv_noalloc.hip"), []),
            (os.path.join(CSRC, "qmv_norm.hip"), []),
            (os.path.join(CSRC, "qmv_kv.hip"), []),
+           (os.path.join(CSRC, "qmv_kv_attention.hip"), ["-mllvm", "-amdgpu-mfma-vgpr-form"]),
            (os.path.join(CSRC, "qmv_step_api.cpp"), []),
            (os.path.join(CSRC, "qmv_api.cpp"), [])]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

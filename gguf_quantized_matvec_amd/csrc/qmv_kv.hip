@@ -1,9 +1,9 @@
 // The paged 4-bit key/value cache on gfx950: appending rotated keys and
-// values, reading stored values back, and attention over the cache.
+// values, and reading stored values back.
 //
 // A key or value head is held as Q4_0 values: per 32 elements an fp16 scale d
 // and 4-bit codes, value d * (code - 8).  The bytes of a page are laid out for
-// the loads of the attention kernel rather than as 18-byte GGUF blocks
+// the loads of the attention kernel (qmv_kv_attention.hip) rather than as 18-byte GGUF blocks
 // (nb = head_dim / 32 blocks a head; per page and head, in this order):
 //   K codes  [token][g = 0..3][b][4]   nibble j of the 4 bytes is element
 //                                      NIB(j) of 32b + 8g ..., so that a masked
@@ -17,68 +17,10 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "qmv_internal.h"
-#include "qmv_step.h"
+#include "qmv_kv_device.h"
 
 namespace qmv {
 namespace {
-
-constexpr float NO_KEY = -1e30f;  // running reference of a row that has seen no key
-
-__device__ __forceinline__ float half_value(uint16_t h) {
-    _Float16 f;
-    __builtin_memcpy(&f, &h, 2);
-    return (float)f;
-}
-
-// Element e (0..7) of a K word sits in nibble K_NIB(e): 0, 4, 1, 5, 2, 6, 3, 7.
-__device__ __forceinline__ int k_nibble(int e) { return (e >> 1) | ((e & 1) << 2); }
-
-// A sequence as a call sees it: rows [q0, q0 + n) at positions len - n ... .
-struct Seq {
-    int q0, n, len;
-};
-
-// Lengths and starts come from device memory and are not trusted: a length is
-// cut to what the table can name and to max_len, a run of rows to the T rows
-// of the call.
-__device__ __forceinline__ Seq seq_of(const KvArgs& kv, int b) {
-    Seq s;
-    s.q0 = kv.q_start ? kv.q_start[b] : b;
-    s.n = kv.q_start ? kv.q_start[b + 1] - s.q0 : 1;
-    if (s.q0 < 0 || s.n < 0 || s.n > kv.T - s.q0) s.q0 = s.n = 0;
-    const int64_t most = kv.table_stride << kv.log2p;
-    int len = kv.lens[b];
-    if (len > kv.max_len) len = kv.max_len;
-    if ((int64_t)len > most) len = (int)most;
-    s.len = len < 0 ? 0 : len;
-    return s;
-}
-
-// The sequence of row t: the last b with start[b] <= t, by the whole wave 64
-// starts at a time.  Uniform over the wave; -1 if there is none.
-__device__ __forceinline__ int seq_of_row(const KvArgs& kv, int t) {
-    if (!kv.q_start) return t < kv.B ? t : -1;
-    const int lane = threadIdx.x & 63;
-    int below = 0;
-    for (int b0 = 0; b0 <= kv.B; b0 += 64) {
-        const int b = b0 + lane;
-        const unsigned long long m = __ballot(b <= kv.B && kv.q_start[b] <= t);
-        below += __popcll(m);
-        if (m != ~0ull) break;
-    }
-    return below >= 1 && below <= kv.B ? below - 1 : -1;
-}
-
-// The page that holds position p of sequence b, or -1 if the table names none.
-__device__ __forceinline__ int page_of(const KvArgs& kv, int b, int p) {
-    const int pg = kv.table[(int64_t)b * kv.table_stride + (p >> kv.log2p)];
-    return pg >= 0 && (int64_t)pg < kv.n_pages ? pg : -1;
-}
-
-__device__ __forceinline__ uint8_t* head_of(const KvArgs& kv, int page, int head) {
-    return kv.pages + ((int64_t)page * kv.Hkv + head) * kv.head_bytes;
-}
 
 // --------------------------------------------------------------- append ----
 constexpr int HEADS = 8;  // heads (of q, k and v together) per workgroup
@@ -232,80 +174,6 @@ __global__ __launch_bounds__(256) void k_kv_read(KvArgs kv, float* __restrict__ 
     }
 }
 
-// ------------------------------------------------------------ attention ----
-// One workgroup per row and query head, 256 keys at a time: scores (one key a
-// thread), the running maximum and sum, then the weighted values (one element
-// a thread).
-__global__ __launch_bounds__(256) void k_kv_attention(AttnArgs a) {
-    const KvArgs& kv = a.kv;
-    __shared__ float qs[256], ps[256], red[4];
-    const int t = blockIdx.x, hq = blockIdx.y, tid = threadIdx.x;
-    const int D = 32 * kv.nb, head = hq / (a.Hq / kv.Hkv);
-    const int b = seq_of_row(kv, t);
-    if (b < 0) return;
-    const Seq s = seq_of(kv, b);
-    if (t < s.q0 || t >= s.q0 + s.n) return;
-    const int pos = s.len - s.n + (t - s.q0);
-    if (tid < D) qs[tid] = a.q[(int64_t)t * a.q_stride + (int64_t)hq * D + tid] * a.scale;
-    __syncthreads();
-    const int lo = a.window && pos + 1 > a.window ? pos + 1 - a.window : 0;
-    const int64_t page_codes = (int64_t)(16 * kv.nb) << kv.log2p;
-    float m = NO_KEY, l = 0.0f, o = 0.0f;
-    for (int t0 = lo & ~255; t0 <= pos; t0 += 256) {
-        const int key = t0 + tid;
-        float z = -INFINITY;
-        if (key >= lo && key <= pos) {
-            const int page = page_of(kv, b, key);
-            if (page >= 0) {
-                const int off = key & ((1 << kv.log2p) - 1);
-                const uint8_t* hd = head_of(kv, page, head);
-                const uint16_t* sc = reinterpret_cast<const uint16_t*>(hd + 2 * page_codes);
-                z = 0.0f;
-                for (int bb = 0; bb < kv.nb; bb++) {
-                    float acc = 0.0f;
-                    for (int g = 0; g < 4; g++) {
-                        const uint32_t w = *reinterpret_cast<const uint32_t*>(
-                            hd + (int64_t)off * 16 * kv.nb + (g * kv.nb + bb) * 4);
-                        for (int e = 0; e < 8; e++)
-                            acc += qs[32 * bb + 8 * g + e] *
-                                   (float)((int)((w >> (4 * k_nibble(e))) & 15) - 8);
-                    }
-                    z += half_value(sc[off * kv.nb + bb]) * acc;
-                }
-            }
-        }
-        float c = z;
-        for (int x = 1; x < 64; x <<= 1) c = fmaxf(c, __shfl_xor(c, x));
-        if ((tid & 63) == 0) red[tid >> 6] = c;
-        __syncthreads();
-        const float mn = fmaxf(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])), m);
-        const float al = expf(m - mn);
-        ps[tid] = expf(z - mn);
-        __syncthreads();
-        m = mn;
-        l *= al;
-        o *= al;
-        for (int i = 0; i < 256; i++) l += ps[i];
-        if (tid < D) {
-            const int bb = tid >> 5, mm = (tid & 31) >> 1, sh = 4 * (tid & 1);
-            for (int i = 0; i < 256; i++) {
-                const float p = ps[i];
-                if (p == 0.0f) continue;
-                const int k2 = t0 + i, page = page_of(kv, b, k2);
-                const int off = k2 & ((1 << kv.log2p) - 1);
-                const uint8_t* hd = head_of(kv, page, head);
-                const uint16_t* sc = reinterpret_cast<const uint16_t*>(hd + 2 * page_codes) +
-                                     ((int64_t)kv.nb << kv.log2p);
-                const int byte = hd[page_codes + (int64_t)(off >> 2) * 64 * kv.nb + (off & 3) +
-                                    (mm * kv.nb + bb) * 4];
-                o += p * (half_value(sc[off * kv.nb + bb]) * (float)(((byte >> sh) & 15) - 8));
-            }
-        }
-        __syncthreads();
-    }
-    if (tid < D) a.out[((int64_t)t * a.Hq + hq) * D + tid] = l > 0.0f ? o / l : (l != l ? l : 0.0f);
-}
-
 }  // namespace
 
 int launch_kv_append(const AppendArgs& a, hipStream_t s) {
@@ -319,13 +187,6 @@ int launch_kv_read(const KvArgs& kv, float* k, float* v, hipStream_t s) {
     const int per = kv.Hkv * 4 * kv.nb;
     hipLaunchKernelGGL(k_kv_read, dim3((unsigned)kv.T, (unsigned)((per + 255) / 256)), dim3(256), 0,
                        s, kv, k, v);
-    return (int)hipGetLastError();
-}
-
-int64_t kv_attention_bytes(int64_t, int64_t, int, int, int, int64_t) { return 16; }
-
-int launch_kv_attention(const AttnArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL(k_kv_attention, dim3((unsigned)a.kv.T, (unsigned)a.Hq), dim3(256), 0, s, a);
     return (int)hipGetLastError();
 }
 

@@ -152,7 +152,7 @@ int qmv_kv_attention(const qmv_kv* kv, const qmv_kv_batch* seqs, const float* q,
     a.q_stride = q_stride;
     a.Hq = q_heads;
     a.scale = scale;
-    a.window = window > QMV_KV_MAX_LEN ? 0 : (int32_t)window;  // longer than any sequence
+    a.window = window >= seqs->max_len ? 0 : (int32_t)window;  // longer than any sequence: none
     a.out = out;
     a.work = static_cast<float*>(work);
     return launched(qmv::launch_kv_attention(a, static_cast<hipStream_t>(stream)));

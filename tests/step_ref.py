@@ -78,11 +78,11 @@ def encode_page(kc, kd, vc, vd, page, nb):
 
 def attention(q, k, v, pos, scale, window=0, seen=None):
     """One sequence: q [n, Hq, D], k, v [L, Hkv, D] f64, pos [n].  Returns out
-    [n, Hq, D] and the error scale per row and head: (max_t sum_d |q k| scale,
-    sum_t p |v| [D])."""
+    [n, Hq, D] and sizes that errors are measured by, per row and head: max_t
+    sum_d |q k| scale, sum_t p |v| [D], max_t p max_d |v|."""
     n, hq, _ = q.shape
     g = hq // k.shape[1]
-    out, amax = np.zeros(q.shape), np.zeros((n, hq))
+    out, amax, pmax = np.zeros(q.shape), np.zeros((n, hq)), np.zeros((n, hq))
     pv = np.zeros(q.shape)
     t = np.arange(len(k))
     for j in range(n):
@@ -101,4 +101,5 @@ def attention(q, k, v, pos, scale, window=0, seen=None):
             out[j, h] = p @ vv
             amax[j, h] = (np.abs(kk) @ np.abs(q[j, h].astype(np.float64))).max() * scale
             pv[j, h] = p @ np.abs(vv)
-    return out, amax, pv
+            pmax[j, h] = (p * np.abs(vv).max(-1)).max()
+    return out, amax, pv, pmax

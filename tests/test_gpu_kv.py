@@ -286,14 +286,19 @@ def filled(c, hq, dscale=1.0):
     return cells.reshape(-1), [of(ks, b) for b in range(c.B)], [of(vs, b) for b in range(c.B)]
 
 
-def bound(d, length, out, amax, pv):
+def bound(d, length, amax, pv, pmax):
     """How far an f32 computation may be off.  A score is a sum of d products: each product and each
     of at most d + 8 roundings (scaling and splitting q, the block scales, the sums) is off by half a
     step of a magnitude below sum |q k| scale (amax, natural units), and exp adds 2^-22; both enter
     every weight and their sum.  The weighted sums run over partial sums of at most 64 terms and
-    the runs of 512 keys; each is off by half a step of sum p |v|."""
+    the runs of 512 keys; each is off by half a step of sum p |v|.
+    Weights times block scales are split into two f16 numbers in a unit where the largest such term
+    of a run, p max_b |d| = p max |v| / 8, is 2^13 at least: one of them is off by at most half of
+    f16's smallest step, 2^-25, that is 2^-38 of that largest term, and meets codes of at most 8, so
+    each key adds at most 2^-38 max_t (p max |v|) (a weight of e^-69 beside one of 1 is lost so)."""
     delta = (d + 8) * 2.0 ** -24 * amax[..., None] + 2.0 ** -21
-    return (2 * delta + (80 + length / 512) * 2.0 ** -24) * pv + 1e-30
+    floor = length * 2.0 ** -38 * pmax[..., None]
+    return (2 * delta + (80 + length / 512) * 2.0 ** -24) * pv + floor
 
 
 ATTNS = [
@@ -341,13 +346,12 @@ def check(c, got, q, ks, vs, hq, scale, window, seen=None):
         if lo == hi:
             continue
         pos = np.arange(c.lens[b] - c.ns[b], c.lens[b])
-        want, amax, pv = attention(q[lo:hi].reshape(hi - lo, hq, c.d), ks[b], vs[b], pos, scale, window,
+        want, *sizes = attention(q[lo:hi].reshape(hi - lo, hq, c.d), ks[b], vs[b], pos, scale, window,
                                    None if seen is None else seen[b])
         x = got[lo:hi].reshape(hi - lo, hq, c.d)
         assert np.all(x[pos < 0] == 0)
-        lim = bound(c.d, c.lens[b], want, amax, pv)
-        worst = np.max(np.abs(x - want) / lim)
-        assert np.all(np.abs(x - want) <= lim), (b, worst)
+        lim = bound(c.d, c.lens[b], *sizes)
+        assert np.all(np.abs(x - want) <= lim), (b, np.max(np.abs(x - want) - lim))
 
 
 @pytest.mark.parametrize("dscale", [1e-6, 1e-3, 1.0, 1e3, 6e4])
@@ -443,3 +447,36 @@ def test_shared_pages_and_offsets(g):
     rk, rv = g.kv_read(cache, batch)
     assert np.array_equal(rk.cpu().numpy(), q4_value(*q4_0(k)).astype(np.float32))
     assert np.array_equal(rv.cpu().numpy(), q4_value(*q4_0(v)).astype(np.float32))
+
+
+@pytest.mark.parametrize("d,hq,hkv,window", [(32, 4, 2, 0), (64, 7, 1, 0), (96, 3, 3, 600), (128, 8, 2, 0),
+                                             (128, 40, 2, 90), (160, 4, 4, 0), (192, 4, 1, 0),
+                                             (224, 2, 2, 700), (256, 4, 2, 0)])
+def test_a_row_does_not_depend_on_its_call(g, d, hq, hkv, window):
+    """The same token's row, bit for bit: in a prompt at once, in chunks, alone, beside other
+    sequences, with a larger bound of the lengths (another split of the work)."""
+    L, n, page = 1100, 37, 16
+    c = Case([L, 50, 333], [n, 50, 1], page, hkv, d, 17)
+    raw, _, _ = filled(c, hq)
+    q = dev((1.5 * c.rng.standard_normal((c.T, hq * d))).astype(np.float32))
+    cache, table = g.KVCache(dev(raw), page, hkv, d), dev(c.table)
+
+    def call(q, seqs, lens, ns=None, max_len=None):
+        starts = None if ns is None else dev(np.concatenate([[0], np.cumsum(ns)]).astype(np.int32))
+        batch = g.KVBatch(table[seqs].contiguous(), dev(np.array(lens, np.int32)), starts,
+                          None if ns is None else sum(ns), max_len or max(lens))
+        return g.kv_attention(cache, batch, q.contiguous(), d ** -0.5, window=window)
+
+    whole = call(q, [0, 1, 2], [L, 50, 333], [n, 50, 1])
+    assert torch.equal(call(q[:n], [0], [L], [n]), whole[:n])
+    assert torch.equal(call(q[:n], [0], [L], [n], max_len=c.table.shape[1] * page), whole[:n])
+    assert torch.equal(call(q[5:20], [0], [L - n + 20], [15]), whole[5:20])
+    rows = [0, 1, 12, n - 1]
+    alone = torch.cat([call(q[j:j + 1], [0], [L - n + j + 1]) for j in rows])
+    assert torch.equal(alone, whole[rows])
+    # as one decode batch of many lengths of the same pages, enough of them to need no split
+    js = list(range(n)) * 20
+    many = call(q[js], [0] * len(js), [L - n + j + 1 for j in js])
+    assert torch.equal(many.view(20, n, -1), whole[:n].expand(20, n, -1))
+    assert torch.equal(call(q[n:n + 50], [1], [50], [50]), whole[n:n + 50])
+    assert torch.equal(call(q[n + 50:], [2], [333]), whole[n + 50:])
