@@ -21,7 +21,7 @@
 // - the fp16 block scales multiply the f32 block sums (keys) and the weights
 //   before their split (values), v_fma_mix taking the halves as they are.
 //
-// Work split.  A wave takes 16 R rows that share a key/value head and SUB
+// Work split.  A wave takes 16 (or 8) rows that share a key/value head and SUB
 // positions at a time: all scores first, one maximum, then the values; the
 // WAVES waves of a workgroup take consecutive runs of SUB positions, and their
 // results are joined in LDS into a segment of SEG positions.  Segments are
@@ -30,10 +30,12 @@
 // and every step depends on the row's own query and positions alone, so a row's
 // bits do not depend on the batch, on the prompt's chunking or on the split.
 //
-// Weights are held relative to a reference r: p = 2^(s log2e - r), where r
-// makes the largest p[t] * max_b |dv[t][b]| about 2^14, the top of f16's range:
-// what is split then keeps 22 bits down to 2^-17 of the largest term, whatever
-// the size of the values.
+// Weights.  With max_b |dv[t][b]| < 2^e[t], a weight is held as p[t] =
+// 2^(s[t] log2e + e[t] - r), where r makes the largest of a run 2^14, and its
+// scales as dv 2^-e: the products, which are split into two f16 numbers, then
+// fill f16's range from the top, keep 22 bits down to 2^-17 of the largest term
+// and are off by 2^-39 of it below, whatever the size of the values.  The sum
+// of the weights is that of p 2^-e, in f32.
 //
 // Built with -ffp-contract=off: every float operation is the one written.
 #include <hip/hip_runtime.h>
@@ -44,10 +46,12 @@
 namespace qmv {
 namespace {
 
-constexpr int SUB = 128;           // positions a wave takes at a time
-constexpr int TILES = SUB / 16;
 constexpr int WAVES = 4;
-constexpr int SEG = SUB * WAVES;   // positions of a segment
+// Positions a wave takes at a time: 128, or for heads beyond 128 elements 64, so
+// that their codes, scores and sums fit the 256 registers of two waves per
+// SIMD.  And of a segment.
+constexpr int sub_of(int nb) { return nb <= 4 ? 128 : 64; }
+constexpr int seg_of(int nb) { return WAVES * sub_of(nb); }
 constexpr float NO_KEY = -1e30f;   // reference of a row that has seen no position
 
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
@@ -71,26 +75,76 @@ __device__ __forceinline__ half8 operand(uint32_t a, uint32_t b, uint32_t c, uin
 }
 
 // code - 8 of the nibbles at bits 0..3 (low) or 4..7 (high) of both halves.
+// The constants come from registers that the compiler cannot see through, so
+// that mask and exponent are one v_and_or_b32 (which takes no literals).
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ uint32_t plus(uint32_t w, float c) {
-    half2v h;
-    __builtin_memcpy(&h, &w, 4);
-    h = h + (half2v){(_Float16)c, (_Float16)c};
-    __builtin_memcpy(&w, &h, 4);
-    return w;
-}
-__device__ __forceinline__ uint32_t low_codes(uint32_t w) {
-    return plus((w & 0x000F000Fu) | 0x64006400u, -1032.0f);
-}
-__device__ __forceinline__ uint32_t high_codes(uint32_t w) {
-    return plus((w & 0x00F000F0u) | 0x54005400u, -72.0f);
-}
+struct Unpack {
+    uint32_t low_mask = 0x000F000Fu, low_exp = 0x64006400u;    // 1024 + code
+    uint32_t high_mask = 0x00F000F0u, high_exp = 0x54005400u;  // 64 + code
+    __device__ __forceinline__ Unpack() {
+        asm("" : "+s"(low_mask), "+v"(low_exp), "+s"(high_mask), "+v"(high_exp));
+    }
+    __device__ __forceinline__ static uint32_t plus(uint32_t w, float c) {
+        half2v h;
+        __builtin_memcpy(&h, &w, 4);
+        h = h + (half2v){(_Float16)c, (_Float16)c};
+        __builtin_memcpy(&w, &h, 4);
+        return w;
+    }
+    __device__ __forceinline__ uint32_t low(uint32_t w) const {
+        return plus((w & low_mask) | low_exp, -1032.0f);
+    }
+    __device__ __forceinline__ uint32_t high(uint32_t w) const {
+        return plus((w & high_mask) | high_exp, -72.0f);
+    }
+};
+
+__device__ __forceinline__ uint32_t half_bits(uint32_t w, int i) { return i ? w >> 16 : w & 0xFFFFu; }
 
 __device__ __forceinline__ _Float16 half_of(uint32_t w, int i) {
     const uint16_t b = (uint16_t)(i ? w >> 16 : w);
     _Float16 h;
     __builtin_memcpy(&h, &b, 2);
     return h;
+}
+
+// p0 d0 and p1 d1, each as the sum of two f16 numbers: what the first leaves is
+// exact in the fma and rounded once more.  (The empty asm statements keep
+// each number one v_fma_mixlo or v_fma_mixhi.)
+__device__ __forceinline__ half2v halves(uint32_t w) {
+    half2v h;
+    __builtin_memcpy(&h, &w, 4);
+    return h;
+}
+__device__ __forceinline__ uint32_t word(half2v h) {
+    uint32_t w;
+    __builtin_memcpy(&w, &h, 4);
+    return w;
+}
+
+// A number as the sum of two f16 numbers, two at a time.
+struct Split {
+    half2v h, l;
+};
+__device__ __forceinline__ Split two_parts(float a, float b) {
+    Split s;
+    s.h = half2v{(_Float16)a, (_Float16)b};
+    s.l = half2v{(_Float16)(a - (float)s.h[0]), (_Float16)(b - (float)s.h[1])};
+    return s;
+}
+// s d, split again: what the rounded product of the first part leaves is exact in the f16 fma,
+// the second part's product joins it.  Three packed instructions for two numbers (v_fma_mixlo_f16
+// and v_fma_mixhi_f16 do two in four, at half the rate).
+__device__ __forceinline__ Split times(Split s, half2v d) {
+    Split r;
+    r.h = s.h * d;
+    r.l = __builtin_elementwise_fma(s.l, d, __builtin_elementwise_fma(s.h, d, -r.h));
+    return r;
+}
+
+// The value of lane n ^ 8 among 16.
+__device__ __forceinline__ float across8(float x) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(x), __float_as_int(x), 0x128, 0xF, 0xF, false));
 }
 
 __device__ __forceinline__ float exp2_raw(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -103,10 +157,11 @@ __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// The launch: `tiles` row tiles of 16 R rows (per key/value head), `splits`
-// workgroups each of `per` segments; splits > 1: segment results go to work.
+// The launch: `tiles` row tiles (per key/value head), `splits` workgroups each
+// of `per` segments; splits > 1: segment results go to work.
 struct Plan {
-    int32_t tiles, splits, per, segs, R;
+    int32_t tiles, splits, per, segs;
+    bool pack;
 };
 
 // A segment's result of one row in the workspace: O [D], then (for all rows)
@@ -133,20 +188,30 @@ __device__ __forceinline__ float joined(float o, float part, Join j) { return o 
 
 __device__ __forceinline__ float result(float o, float l) { return l == 0.0f ? 0.0f : o / l; }
 
-template <int NB, int R>
-__global__ __launch_bounds__(64 * WAVES) void k_attn(AttnArgs a, Plan plan) {
+// PACK: at most 8 rows share a key/value head in the tile.  The 16 columns of
+// a product then hold them twice, and each half of the columns keeps its own
+// positions: the tiles of 16 positions of even number in columns 0..7, those of
+// odd number in columns 8..15.  Scores, weights and their split are so done for
+// two tiles at a time.  The values' sums run over the even
+// tiles, move across, and go on over the odd tiles, which is the order of the
+// sums in every variant.
+template <int NB, bool PACK>
+__global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a, Plan plan) {
     const KvArgs& kv = a.kv;
-    constexpr int D = 32 * NB;
-    constexpr int NBP = NB < 4 ? NB : 4;  // blocks joined at a time
+    constexpr int D = 32 * NB, SUB = sub_of(NB), SEG = seg_of(NB), TILES = SUB / 16;
+    constexpr int ROWS = PACK ? 8 : 16;           // rows of a tile
+    constexpr int SLOTS = PACK ? TILES / 2 : TILES;  // tiles of positions a column sees
+    constexpr int NBP = NB < 4 ? NB : 4;          // blocks joined at a time
     constexpr int LD = 32 * NBP + 4;
-    __shared__ __align__(16) uint32_t s_dk[WAVES][SUB * NB / 2];
-    __shared__ __align__(16) uint32_t s_dv[WAVES][SUB * NB / 2];
-    __shared__ __align__(16) float s_ev[WAVES][SUB];
-    __shared__ __align__(16) float s_o[WAVES][16 * LD];
-    __shared__ float s_r[WAVES][16 * R], s_l[WAVES][16 * R];
+    constexpr int PER_ROW = 64 * WAVES / ROWS;    // threads that join a row
+    __shared__ __align__(16) uint32_t s_dk[WAVES][NB][SUB / 2];  // [block][position] fp16
+    __shared__ __align__(16) uint32_t s_dv[WAVES][NB][SUB / 2];
+    __shared__ __align__(16) float s_ev[WAVES][SUB], s_down[WAVES][SUB];
+    __shared__ __align__(16) float s_o[WAVES][ROWS * LD];
+    __shared__ float s_r[WAVES][ROWS], s_l[WAVES][ROWS];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-    const int n = lane & 15, g = lane >> 4;
+    const int n = lane & (ROWS - 1), par = PACK ? (lane >> 3) & 1 : 0, g = lane >> 4;
     const int G = a.Hq / kv.Hkv;
     const int head = blockIdx.x % kv.Hkv;
     int at = blockIdx.x / kv.Hkv;
@@ -156,24 +221,24 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn(AttnArgs a, Plan plan) {
     // the tile's sequence and rows
     int b, first;
     if (!kv.q_start) {
-        const int per = (G + 16 * R - 1) / (16 * R);
+        const int per = (G + ROWS - 1) / ROWS;
         b = tile / per;
-        first = (tile - b * per) * 16 * R;
+        first = (tile - b * per) * ROWS;
         if (b >= kv.B) return;
     } else {
-        // sequence b owns the tiles from (start[b] * G) / (16 R) + b on
+        // sequence b owns the tiles from start[b] * G / ROWS + b on
         int below = 0;
         for (int b0 = 0; b0 < kv.B; b0 += 64) {
             const int i = b0 + lane;
             bool le = false;
-            if (i < kv.B) le = (int64_t)kv.q_start[i] * G / (16 * R) + i <= tile;
+            if (i < kv.B) le = (int64_t)kv.q_start[i] * G / ROWS + i <= tile;
             const unsigned long long m = __ballot(le);
             below += __popcll(m);
             if (m != ~0ull) break;
         }
         if (below == 0) return;
         b = uniform(below - 1);
-        const int64_t f = (tile - ((int64_t)kv.q_start[b] * G / (16 * R) + b)) * 16 * R;
+        const int64_t f = (tile - ((int64_t)kv.q_start[b] * G / ROWS + b)) * ROWS;
         if (f < 0 || f > INT32_MAX) return;
         first = (int)f;
     }
@@ -181,7 +246,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn(AttnArgs a, Plan plan) {
     const int64_t rows64 = (int64_t)s.n * G;
     if (first >= rows64) return;
     const int rows = (int)rows64;
-    const int last = first + 16 * R < rows ? first + 16 * R - 1 : rows - 1;
+    const int last = first + ROWS < rows ? first + ROWS - 1 : rows - 1;
     const int pos_lo = s.len - s.n + first / G, pos_hi = s.len - s.n + last / G;
     const int t_end = pos_hi + 1;
     const int t_begin = a.window && pos_lo + 1 > a.window ? pos_lo + 1 - a.window : 0;
@@ -194,18 +259,62 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn(AttnArgs a, Plan plan) {
         if (seg0 >= seg1) return;
     }
 
+    // What a wave holds ahead of a run of SUB positions: the pages of its tiles (lane u of
+    // TILES: where tile u's K codes begin; its V codes, 16 positions of the same size, are `codes`
+    // further), the K codes, and the scales of two positions a lane.
+    const int page_tokens = 1 << kv.log2p;
+    const int64_t codes = (int64_t)(16 * NB) << kv.log2p;
+    const int32_t* table = kv.table + (int64_t)b * kv.table_stride;
+    int pg = -1;
+    uint32_t there = 0, at_lo = 0, at_hi = 0;
+    Words<NB> cw[TILES], dk, dv;  // codes: keys, then values, then the next run's keys
+    const auto works = [&](int seg) {
+        const int t0 = seg * SEG + wave * SUB;
+        return seg < seg1 && t0 < t_end && t0 + SUB > t_begin;
+    };
+    const auto fetch_pages = [&](int seg) {
+        const int t = seg * SEG + wave * SUB + 16 * lane;
+        pg = -1;
+        if (works(seg) && lane < TILES && t < s.len) pg = table[t >> kv.log2p];
+    };
+    const auto tile_codes = [&](int u) {
+        const uint64_t at = (uint32_t)__builtin_amdgcn_readlane(at_lo, u) |
+                            (uint64_t)(uint32_t)__builtin_amdgcn_readlane(at_hi, u) << 32;
+        return kv.pages + at;
+    };
+    const auto fetch_scales = [&](int seg) {  // and where the codes are
+        const int t0 = seg * SEG + wave * SUB;
+        const bool ok = pg >= 0 && (int64_t)pg < kv.n_pages;
+        there = (uint32_t)__ballot(ok);  // tiles that have a page
+        const int p = ok ? pg : 0;       // the others read page 0, which is not used
+        const int64_t at_k = ((int64_t)p * kv.Hkv + head) * kv.head_bytes +
+                             (int64_t)((t0 + 16 * lane) & (page_tokens - 1)) * (16 * NB);
+        at_lo = (uint32_t)at_k;
+        at_hi = (uint32_t)(at_k >> 32);
+        const int u = lane >> 3, t = t0 + 16 * u + 2 * (lane & 7);
+        const uint8_t* hd = head_of(kv, __shfl(p, u), head) + 2 * codes +
+                            (int64_t)(t & (page_tokens - 1)) * 2 * NB;
+        if (TILES == 8 || u < TILES) {
+            dk = load_words<NB>(hd);
+            dv = load_words<NB>(hd + ((int64_t)(2 * NB) << kv.log2p));
+        }
+    };
+    const auto fetch_keys = [&](int u) {
+        cw[u] = load_words<NB>(tile_codes(u) + (lane & 15) * (16 * NB) + g * (4 * NB));
+    };
+    fetch_pages(seg0);
+
     // q as two f16 parts: lane (n, g) holds elements 32b + 8g ... + 7 of row n
-    half8 qh[R][NB], ql[R][NB];
-    float factor[R];
-    int pos[R];
-    const float to_log2 = a.scale * 1.44269504f;
-#pragma unroll
-    for (int rt = 0; rt < R; rt++) {
-        const int rr = first + 16 * rt + n;
+    half8 qh[NB], ql[NB];
+    float factor;
+    int pos;
+    {
+        const int rr = first + n;
         const bool valid = rr < rows;
         const int j = valid ? rr / G : 0, hg = valid ? rr - j * G : 0;
-        pos[rt] = valid ? s.len - s.n + j : -1;
+        pos = valid ? s.len - s.n + j : -1;
         const float* qp = a.q + (int64_t)(s.q0 + j) * a.q_stride + (int64_t)(head * G + hg) * D + 8 * g;
+        const float to_log2 = a.scale * 1.44269504f;
         float x[NB][8];
         float big = 0.0f;
 #pragma unroll
@@ -217,73 +326,57 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn(AttnArgs a, Plan plan) {
             }
             const float t[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int e = 0; e < 8; e++) {
-                x[bb][e] = t[e] * to_log2;
-                big = fmaxf(big, fabsf(x[bb][e]));
-            }
+            for (int e = 0; e < 8; e++) x[bb][e] = t[e] * to_log2;
         }
+        if (works(seg0)) {
+            fetch_scales(seg0);
+#pragma unroll
+            for (int u = 0; u < TILES; u++) fetch_keys(u);
+        }
+        fetch_pages(seg0 + 1);
+#pragma unroll
+        for (int bb = 0; bb < NB; bb++)
+#pragma unroll
+            for (int e = 0; e < 8; e++) big = fmaxf(big, fabsf(x[bb][e]));
         big = fmaxf(big, __shfl_xor(big, 16));
         big = fmaxf(big, __shfl_xor(big, 32));
         int ex = (int)((__float_as_uint(big) >> 23) & 255) - 126;  // big < 2^ex
         ex = ex < -100 ? -100 : ex;
         const float up = ldexpf(1.0f, 15 - ex);
-        factor[rt] = ldexpf(1.0f, ex - 15);
+        factor = ldexpf(1.0f, ex - 15);
 #pragma unroll
         for (int bb = 0; bb < NB; bb++) {
 #pragma unroll
             for (int e = 0; e < 8; e++) {
                 const float y = x[bb][e] * up;
-                qh[rt][bb][e] = (_Float16)y;
-                ql[rt][bb][e] = (_Float16)(y - (float)qh[rt][bb][e]);
+                const _Float16 h = (_Float16)y, l = (_Float16)(y - (float)h);
+                qh[bb][e] = h;
+                ql[bb][e] = l;
             }
         }
     }
 
-    const int page_tokens = 1 << kv.log2p;
-    const int64_t codes = (int64_t)(16 * NB) << kv.log2p;
-    const int32_t* table = kv.table + (int64_t)b * kv.table_stride;
-
-    // the joined state: thread (row tid / 16, part tid % 16) of each row tile
-    // holds 2 NBP elements of every NBP blocks
-    const int jr = tid >> 4, jp = tid & 15;
-    float O[R][2 * NB], L[R], RR[R];
+    // the joined state: thread (row tid / PER_ROW, part tid % PER_ROW) holds its share of every
+    // NBP blocks
+    const int jr = tid / PER_ROW, jp = tid % PER_ROW;
+    constexpr int SHARE = 32 * NB / PER_ROW;
+    float O[SHARE], L = 0.0f, RR = NO_KEY;
 #pragma unroll
-    for (int rt = 0; rt < R; rt++) {
-        L[rt] = 0.0f;
-        RR[rt] = NO_KEY;
-#pragma unroll
-        for (int i = 0; i < 2 * NB; i++) O[rt][i] = 0.0f;
-    }
+    for (int i = 0; i < SHARE; i++) O[i] = 0.0f;
+    const Unpack unpack;
 
     for (int seg = seg0; seg < seg1; seg++) {
         const int t0 = seg * SEG + wave * SUB;
-        const bool work = t0 < t_end && t0 + SUB > t_begin;
-        f4 o[R][2 * NB];
-        float r[R], l[R];
-#pragma unroll
-        for (int rt = 0; rt < R; rt++) {
-            r[rt] = NO_KEY;
-            l[rt] = 0.0f;
-        }
+        const bool work = works(seg);
+        f4 o[2 * NB];
+        float r = NO_KEY, l = 0.0f;
         if (work) {
-            // pages of the wave's tiles of 16 positions
-            int pg = -1;
-            if (lane < TILES && t0 + 16 * lane < s.len) {
-                const int p = table[(t0 + 16 * lane) >> kv.log2p];
-                if (p >= 0 && (int64_t)p < kv.n_pages) pg = p;
-            }
-            const uint32_t there = (uint32_t)__ballot(pg >= 0);  // tiles that have a page
-            pg = pg < 0 ? 0 : pg;  // loads of the others read page 0 and are not used
             const bool masked = t0 + SUB > pos_lo + 1 || (a.window && t0 <= pos_hi - a.window) ||
                                 there != (1u << TILES) - 1;
-            // scales: lane i of 8 per tile takes two positions
-            {
+            const uint32_t here = there;
+            if (TILES == 8 || lane < 8 * TILES) {
                 const int u = lane >> 3, t = t0 + 16 * u + 2 * (lane & 7);
-                const uint8_t* hd = head_of(kv, __shfl(pg, u), head) + 2 * codes +
-                                    (int64_t)(t & (page_tokens - 1)) * 2 * NB;
-                Words<NB> dk = load_words<NB>(hd);
-                Words<NB> dv = load_words<NB>(hd + ((int64_t)(2 * NB) << kv.log2p));
-                const int live = ((there >> u) & 1) ? s.len - t : 0;  // positions behind the last: scale 0
+                const int live = ((here >> u) & 1) ? s.len - t : 0;  // positions behind the last: scale 0
                 uint32_t top[2] = {0, 0};
 #pragma unroll
                 for (int i = 0; i < NB; i++) {
@@ -303,298 +396,392 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn(AttnArgs a, Plan plan) {
                 // turns the reference of a row that sees it infinite and its result NaN, and
                 // scales of 0, so that the rows that do not see it have no 0 * NaN
                 const bool bad[2] = {top[0] >= 0x7C00u, top[1] >= 0x7C00u};
+                float down[2];
 #pragma unroll
-                for (int i = 0; i < NB; i++) {
-                    if (bad[(2 * i) / NB]) dv.w[i] &= 0xFFFF0000u;
-                    if (bad[(2 * i + 1) / NB]) dv.w[i] &= 0x0000FFFFu;
-                    s_dk[wave][lane * NB + i] = dk.w[i];
-                    s_dv[wave][lane * NB + i] = dv.w[i];
+                for (int i = 0; i < 2; i++) {
+                    const int e = (int)(top[i] >> 10) - 14;
+                    s_ev[wave][2 * lane + i] = bad[i] ? INFINITY : (float)e;
+                    // 2^-e
+                    down[i] = bad[i] ? 0.0f : __uint_as_float((uint32_t)(127 - e) << 23);
+                    s_down[wave][2 * lane + i] = down[i];
                 }
 #pragma unroll
-                for (int i = 0; i < 2; i++)
-                    s_ev[wave][2 * lane + i] = bad[i] ? INFINITY : (float)((int)(top[i] >> 10) - 14);
+                for (int i = 0; i < NB; i++) {  // block i of both positions
+                    s_dk[wave][i][lane] = half_bits(dk.w[i >> 1], i & 1) |
+                                          half_bits(dk.w[(NB + i) >> 1], (NB + i) & 1) << 16;
+                    // dv 2^-ev, below 1; the lanes of positions 0, 1 and 2, 3 exchange to words of
+                    // positions 0, 2 and 1, 3, the order of the code words
+                    half2v v = {half_of(dv.w[i >> 1], i & 1), half_of(dv.w[(NB + i) >> 1], (NB + i) & 1)};
+                    v[0] = bad[0] ? (_Float16)0.0f : (_Float16)((float)v[0] * down[0]);
+                    v[1] = bad[1] ? (_Float16)0.0f : (_Float16)((float)v[1] * down[1]);
+                    const uint32_t own = word(v), other = (uint32_t)__builtin_amdgcn_update_dpp(
+                                                      (int)own, (int)own, 0xB1, 0xF, 0xF, false);
+                    s_dv[wave][i][lane] = lane & 1 ? (other >> 16) | (own & 0xFFFF0000u)
+                                                   : (own & 0xFFFFu) | (other << 16);
+                }
             }
-            // lane u of TILES: where tile u's K codes begin (its V codes, 16 positions of the
-            // same size, are `codes` further)
-            const int64_t at_k = ((int64_t)pg * kv.Hkv + head) * kv.head_bytes +
-                                 (int64_t)((t0 + 16 * lane) & (page_tokens - 1)) * (16 * NB);
-            const uint32_t at_lo = (uint32_t)at_k, at_hi = (uint32_t)(at_k >> 32);
-            const auto tile_codes = [&](int u) {
-                const uint64_t at = (uint32_t)__builtin_amdgcn_readlane(at_lo, u) |
-                                    (uint64_t)(uint32_t)__builtin_amdgcn_readlane(at_hi, u) << 32;
-                return kv.pages + at;
-            };
-            Words<NB> kw[TILES];
-#pragma unroll
-            for (int u = 0; u < TILES; u++)
-                kw[u] = load_words<NB>(tile_codes(u) + n * (16 * NB) + g * (4 * NB));
             wave_sync();
 
-            // scores: sc[rt][u][i] of position t0 + 16u + 4g + i, row n
-            f4 sc[R][TILES];
+            // scores: sc[U][i] of row n at position t0 + 16 u + 4g + i, u the slot's tile
+            // (the block scales of a lane's four positions are read from LDS one step ahead of use,
+            // here and below: the scheduler left to itself waits for each)
+            f4 sc[SLOTS];
+            const auto scales = [&](const uint32_t (&from)[NB][SUB / 2], int U, int bb) {
+                return *reinterpret_cast<const Words<2>*>(
+                    &from[bb][8 * (PACK ? 2 * U + par : U) + 2 * g]);
+            };
+            Words<2> dn[NB];
 #pragma unroll
-            for (int u = 0; u < TILES; u++) {
-                half8 ko[NB];
+            for (int bb = 0; bb < NB; bb++) dn[bb] = scales(s_dk[wave], 0, bb);
 #pragma unroll
-                for (int bb = 0; bb < NB; bb++) {
-                    const uint32_t w = kw[u].w[bb], v = w >> 8;
-                    ko[bb] = operand(low_codes(w), high_codes(w), low_codes(v), high_codes(v));
-                }
-                const Words<2 * NB> d = *reinterpret_cast<const Words<2 * NB>*>(
-                    &s_dk[wave][(16 * u + 4 * g) * NB / 2]);
+            for (int U = 0; U < SLOTS; U++) {
+                f4 z = {0, 0, 0, 0};
+                Words<2> dc[NB];
 #pragma unroll
-                for (int rt = 0; rt < R; rt++) {
-                    f4 z = {0, 0, 0, 0};
+                for (int bb = 0; bb < NB; bb++) dc[bb] = dn[bb];
+                if (U + 1 < SLOTS) {
 #pragma unroll
-                    for (int bb = 0; bb < NB; bb++) {
-                        f4 acc = {0, 0, 0, 0};
-                        acc = mfma(ko[bb], ql[rt][bb], acc);
-                        acc = mfma(ko[bb], qh[rt][bb], acc);
-#pragma unroll
-                        for (int i = 0; i < 4; i++)
-                            z[i] = __builtin_fmaf(
-                                (float)half_of(d.w[(i * NB + bb) >> 1], (i * NB + bb) & 1), acc[i],
-                                z[i]);
-                    }
-                    sc[rt][u] = z;
+                    for (int bb = 0; bb < NB; bb++) dn[bb] = scales(s_dk[wave], U + 1, bb);
                 }
                 __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int bb = 0; bb < NB; bb++) {
+                    const Words<2> d = dc[bb];
+                    f4 acc[PACK ? 2 : 1];
+#pragma unroll
+                    for (int h = 0; h < (PACK ? 2 : 1); h++) {
+                        const uint32_t w = cw[PACK ? 2 * U + h : U].w[bb], v = w >> 8;
+                        const half8 ko =
+                            operand(unpack.low(w), unpack.high(w), unpack.low(v), unpack.high(v));
+                        acc[h] = mfma(ko, ql[bb], f4{0, 0, 0, 0});
+                        acc[h] = mfma(ko, qh[bb], acc[h]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        z[i] = __builtin_fmaf((float)half_of(d.w[i >> 1], i & 1),
+                                              PACK && par ? acc[PACK ? 1 : 0][i] : acc[0][i], z[i]);
+                }
+                // in base 2, relative to the size of the position's values
+                const f4 e = *reinterpret_cast<const f4*>(
+                    &s_ev[wave][16 * (PACK ? 2 * U + par : U) + 4 * g]);
+#pragma unroll
+                for (int i = 0; i < 4; i++) sc[U][i] = __builtin_fmaf(z[i], factor, e[i]);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            Words<NB> vw[TILES];
+            // the values' codes take the keys' registers and arrive during the softmax
 #pragma unroll
             for (int u = 0; u < TILES; u++)
-                vw[u] = load_words<NB>(tile_codes(u) + codes + lane * (4 * NB));
+                cw[u] = load_words<NB>(tile_codes(u) + codes + lane * (4 * NB));
 
             // weights
             if (masked) {
+                // a position is seen in (rel - window, rel]
+                const int rel = pos - t0 - 4 * g - 16 * par;
+                const int from = a.window ? rel - a.window : -(1 << 30);
 #pragma unroll
-                for (int rt = 0; rt < R; rt++) {
-                    // a position 16u + i is seen in (rel - window, rel]
-                    const int rel = pos[rt] - t0 - 4 * g;
-                    const int from = a.window ? rel - a.window : -(1 << 30);
-#pragma unroll
-                    for (int u = 0; u < TILES; u++) {
-                        const int hi = (there >> u) & 1 ? rel : -(1 << 30);
-#pragma unroll
-                        for (int i = 0; i < 4; i++)
-                            sc[rt][u][i] = 16 * u + i <= hi && 16 * u + i > from ? sc[rt][u][i] : -INFINITY;
-                    }
-                }
-            }
-#pragma unroll
-            for (int rt = 0; rt < R; rt++) {
-                float top = -INFINITY;
-#pragma unroll
-                for (int u = 0; u < TILES; u++) {
-                    const f4 e = *reinterpret_cast<const f4*>(&s_ev[wave][16 * u + 4 * g]);
+                for (int U = 0; U < SLOTS; U++) {
+                    const int off = PACK ? 32 * U : 16 * U;
+                    const int hi = (here >> (PACK ? 2 * U + par : U)) & 1 ? rel : -(1 << 30);
 #pragma unroll
                     for (int i = 0; i < 4; i++)
-                        top = fmaxf(top, __builtin_fmaf(sc[rt][u][i], factor[rt], e[i]));
+                        sc[U][i] = off + i <= hi && off + i > from ? sc[U][i] : -INFINITY;
                 }
-                top = fmaxf(top, __shfl_xor(top, 16));
-                top = fmaxf(top, __shfl_xor(top, 32));
-                const float ref = top > -INFINITY ? top - 14.0f : 0.0f;
-                float sum = 0.0f;
-#pragma unroll
-                for (int u = 0; u < TILES; u++)
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        sc[rt][u][i] = exp2_raw(__builtin_fmaf(sc[rt][u][i], factor[rt], -ref));
-                        sum += sc[rt][u][i];
-                    }
-                sum += __shfl_xor(sum, 16);
-                sum += __shfl_xor(sum, 32);
-                l[rt] = sum;
-                // no maximum: nothing seen, or NaN scores, whose sum is NaN and stays
-                r[rt] = top == -INFINITY && sum == 0.0f ? NO_KEY : ref;
-#pragma unroll
-                for (int i = 0; i < 2 * NB; i++) o[rt][i] = f4{0, 0, 0, 0};
             }
-
-            // values, 32 positions at a time
+            float top = -INFINITY;
 #pragma unroll
-            for (int q = 0; q < TILES / 2; q++) {
-                const Words<2 * NB> d0 = *reinterpret_cast<const Words<2 * NB>*>(
-                    &s_dv[wave][(32 * q + 4 * g) * NB / 2]);
-                const Words<2 * NB> d1 = *reinterpret_cast<const Words<2 * NB>*>(
-                    &s_dv[wave][(32 * q + 16 + 4 * g) * NB / 2]);
+            for (int U = 0; U < SLOTS; U++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) top = fmaxf(top, sc[U][i]);
+            if constexpr (PACK) top = fmaxf(top, across8(top));
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float ref = top > -INFINITY ? top - 14.0f : 0.0f;
+            float sum[2] = {0.0f, 0.0f};  // over the even and the odd tiles
+            Split p[SLOTS][2];            // positions 0, 2 and 1, 3
+#pragma unroll
+            for (int U = 0; U < SLOTS; U++) {
+                const f4 down = *reinterpret_cast<const f4*>(
+                    &s_down[wave][16 * (PACK ? 2 * U + par : U) + 4 * g]);
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    sc[U][i] = exp2_raw(sc[U][i] - ref);
+                    float& l2 = sum[PACK ? 0 : U & 1];
+                    l2 = __builtin_fmaf(sc[U][i], down[i], l2);
+                }
+                p[U][0] = two_parts(sc[U][0], sc[U][2]);
+                p[U][1] = two_parts(sc[U][1], sc[U][3]);
+            }
+            l = sum[0] + (PACK ? across8(sum[0]) : sum[1]);
+            l += __shfl_xor(l, 16);
+            l += __shfl_xor(l, 32);
+            // no maximum: nothing seen, or NaN scores, whose sum is NaN and stays
+            r = top == -INFINITY && l == 0.0f ? NO_KEY : ref;
+
+            // Values, two tiles of one parity (32 positions) at a product: the weights of slots
+            // U0, U1 times the block's scales.
+            const auto split_weights = [&](int U0, int U1, Words<2> d0, Words<2> d1, half8& ph,
+                                           half8& pl) {
+                const Split a0 = times(p[U0][0], halves(d0.w[0])), a1 = times(p[U0][1], halves(d0.w[1]));
+                const Split a2 = times(p[U1][0], halves(d1.w[0])), a3 = times(p[U1][1], halves(d1.w[1]));
+                ph = operand(word(a0.h), word(a1.h), word(a2.h), word(a3.h));
+                pl = operand(word(a0.l), word(a1.l), word(a2.l), word(a3.l));
+            };
+            const auto add_values = [&](int u0, int u1, int bb, half8 ph, half8 pl, bool fresh) {
+                const uint32_t w0 = cw[u0].w[bb], w1 = cw[u1].w[bb];
+                const uint32_t v0 = w0 >> 8, v1 = w1 >> 8;
+                const half8 even =
+                    operand(unpack.low(w0), unpack.low(v0), unpack.low(w1), unpack.low(v1));
+                const half8 odd =
+                    operand(unpack.high(w0), unpack.high(v0), unpack.high(w1), unpack.high(v1));
+                const f4 zero = {0, 0, 0, 0};
+                o[2 * bb] = mfma(even, pl, fresh ? zero : o[2 * bb]);
+                o[2 * bb + 1] = mfma(odd, pl, fresh ? zero : o[2 * bb + 1]);
+                o[2 * bb] = mfma(even, ph, o[2 * bb]);
+                o[2 * bb + 1] = mfma(odd, ph, o[2 * bb + 1]);
+            };
+            const bool more = works(seg + 1);
+            if (more) fetch_scales(seg + 1);
+            fetch_pages(seg + 2);
+            if constexpr (PACK) {
+                constexpr int Q = TILES / 4;
+                Words<2> dn[SLOTS];
+#pragma unroll
+                for (int U = 0; U < SLOTS; U++) dn[U] = scales(s_dv[wave], U, 0);
 #pragma unroll
                 for (int bb = 0; bb < NB; bb++) {
-                    const uint32_t w0 = vw[2 * q].w[bb], w1 = vw[2 * q + 1].w[bb];
-                    const uint32_t v0 = w0 >> 8, v1 = w1 >> 8;
-                    const half8 even = operand(low_codes(w0), low_codes(v0), low_codes(w1), low_codes(v1));
-                    const half8 odd = operand(high_codes(w0), high_codes(v0), high_codes(w1), high_codes(v1));
+                    half8 ph[Q], pl[Q];
+                    Words<2> dc[SLOTS];
 #pragma unroll
-                    for (int rt = 0; rt < R; rt++) {
-                        half8 ph, pl;
+                    for (int U = 0; U < SLOTS; U++) dc[U] = dn[U];
+                    if (bb + 1 < NB) {
 #pragma unroll
-                        for (int j = 0; j < 8; j++) {
-                            // the order of the code words: positions 0, 2, 1, 3 of each tile
-                            const int i = ((j & 1) << 1) | ((j >> 1) & 1), u = 2 * q + (j >> 2);
-                            const float dd = (float)half_of((j < 4 ? d0 : d1).w[(i * NB + bb) >> 1],
-                                                            (i * NB + bb) & 1);
-                            ph[j] = (_Float16)(sc[rt][u][i] * dd);
-                            pl[j] = (_Float16)__builtin_fmaf(sc[rt][u][i], dd, -(float)ph[j]);
-                        }
-                        o[rt][2 * bb] = mfma(even, pl, o[rt][2 * bb]);
-                        o[rt][2 * bb + 1] = mfma(odd, pl, o[rt][2 * bb + 1]);
-                        o[rt][2 * bb] = mfma(even, ph, o[rt][2 * bb]);
-                        o[rt][2 * bb + 1] = mfma(odd, ph, o[rt][2 * bb + 1]);
+                        for (int U = 0; U < SLOTS; U++) dn[U] = scales(s_dv[wave], U, bb + 1);
                     }
                     __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int q = 0; q < Q; q++) {
+                        split_weights(2 * q, 2 * q + 1, dc[2 * q], dc[2 * q + 1], ph[q], pl[q]);
+                        add_values(4 * q, 4 * q + 2, bb, ph[q], pl[q], q == 0);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        o[2 * bb][i] = across8(o[2 * bb][i]);
+                        o[2 * bb + 1][i] = across8(o[2 * bb + 1][i]);
+                    }
+#pragma unroll
+                    for (int q = 0; q < Q; q++)
+                        add_values(4 * q + 1, 4 * q + 3, bb, ph[q], pl[q], false);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                if (more) {
+#pragma unroll
+                    for (int u = 0; u < TILES; u++) fetch_keys(u);
+                }
+            } else {
+                // tiles u and u + 2, even before odd
+                const auto tile_of = [&](int q) { return 4 * (q % (TILES / 4)) + q / (TILES / 4); };
+                Words<2> n0 = scales(s_dv[wave], tile_of(0), 0), n1 = scales(s_dv[wave], tile_of(0) + 2, 0);
+#pragma unroll
+                for (int q = 0; q < TILES / 2; q++) {
+                    const int u = tile_of(q);
+#pragma unroll
+                    for (int bb = 0; bb < NB; bb++) {
+                        const Words<2> d0 = n0, d1 = n1;
+                        if (bb + 1 < NB || q + 1 < TILES / 2) {
+                            const int un = bb + 1 < NB ? u : tile_of(q + 1), bn = bb + 1 < NB ? bb + 1 : 0;
+                            n0 = scales(s_dv[wave], un, bn);
+                            n1 = scales(s_dv[wave], un + 2, bn);
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
+                        half8 ph, pl;
+                        split_weights(u, u + 2, d0, d1, ph, pl);
+                        add_values(u, u + 2, bb, ph, pl, q == 0);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                    if (more) {  // the next run's keys take the registers
+                        fetch_keys(u);
+                        fetch_keys(u + 2);
+                    }
                 }
             }
+        } else {
+            if (works(seg + 1)) {
+                fetch_scales(seg + 1);
+#pragma unroll
+                for (int u = 0; u < TILES; u++) fetch_keys(u);
+            }
+            fetch_pages(seg + 2);
         }
 
         // join the waves' parts of the segment, then the segment to the state
+        if (lane < ROWS) {
+            s_r[wave][n] = r;
+            s_l[wave][n] = l;
+        }
+        float f[WAVES], sr = NO_KEY, sl = 0.0f;
+        Join jn{1.0f, 0.0f};
 #pragma unroll
-        for (int rt = 0; rt < R; rt++) {
-            if (g == 0) {
-                s_r[wave][16 * rt + n] = r[rt];
-                s_l[wave][16 * rt + n] = l[rt];
+        for (int b0 = 0; b0 < NB; b0 += NBP) {
+            const int nbp = NB - b0 < NBP ? NB - b0 : NBP;
+            if (work && (!PACK || par)) {
+#pragma unroll
+                for (int bb = 0; bb < nbp; bb++) {
+                    const f4 x = o[2 * (b0 + bb)], y = o[2 * (b0 + bb) + 1];
+                    float* to = &s_o[wave][n * LD + 32 * bb + 8 * g];
+                    *reinterpret_cast<f4*>(to) = f4{x[0], y[0], x[1], y[1]};
+                    *reinterpret_cast<f4*>(to + 4) = f4{x[2], y[2], x[3], y[3]};
+                }
             }
-            float f[WAVES], sr = NO_KEY, sl = 0.0f;
-            Join jn{1.0f, 0.0f};
+            __syncthreads();
+            if (b0 == 0) {
 #pragma unroll
-            for (int b0 = 0; b0 < NB; b0 += NBP) {
-                const int nbp = NB - b0 < NBP ? NB - b0 : NBP;
-                if (work) {
-#pragma unroll
-                    for (int bb = 0; bb < nbp; bb++) {
-                        float v[8];
-#pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            v[2 * i] = o[rt][2 * (b0 + bb)][i];
-                            v[2 * i + 1] = o[rt][2 * (b0 + bb) + 1][i];
-                        }
-                        float* to = &s_o[wave][n * LD + 32 * bb + 8 * g];
-                        *reinterpret_cast<f4*>(to) = f4{v[0], v[1], v[2], v[3]};
-                        *reinterpret_cast<f4*>(to + 4) = f4{v[4], v[5], v[6], v[7]};
-                    }
+                for (int w = 0; w < WAVES; w++) {
+                    f[w] = s_r[w][jr];
+                    sr = fmaxf(sr, f[w]);
                 }
-                __syncthreads();
-                if (b0 == 0) {
 #pragma unroll
-                    for (int w = 0; w < WAVES; w++) {
-                        f[w] = s_r[w][16 * rt + jr];
-                        sr = fmaxf(sr, f[w]);
-                    }
-#pragma unroll
-                    for (int w = 0; w < WAVES; w++) {
-                        const bool has = f[w] != NO_KEY;
-                        f[w] = has ? exp2_raw(f[w] - sr) : -1.0f;  // -1: nothing there
-                        if (has) sl = __builtin_fmaf(f[w], s_l[w][16 * rt + jr], sl);
-                    }
-                    if (plan.splits == 1 && sr != NO_KEY) {
-                        jn = join(RR[rt], sr);
-                        L[rt] = joined(L[rt], sl, jn);
-                    }
+                for (int w = 0; w < WAVES; w++) {
+                    const bool has = f[w] != NO_KEY;
+                    f[w] = has ? exp2_raw(f[w] - sr) : -1.0f;  // -1: nothing there
+                    if (has) sl = __builtin_fmaf(f[w], s_l[w][jr], sl);
                 }
-                const int per = 2 * nbp;
-                float v[2 * NBP];
-#pragma unroll
-                for (int i = 0; i < 2 * NBP; i++) v[i] = 0.0f;
-#pragma unroll
-                for (int w = 0; w < WAVES; w++)
-                    if (f[w] >= 0.0f || f[w] != f[w]) {
-#pragma unroll
-                        for (int i = 0; i < per; i++)
-                            v[i] = __builtin_fmaf(f[w], s_o[w][jr * LD + jp * per + i], v[i]);
-                    }
                 if (plan.splits == 1) {
-                    if (sr != NO_KEY) {
+                    jn = join(RR, sr);
+                    L = joined(L, sl, jn);
+                }
+            }
+            const int per = 32 * nbp / PER_ROW, o0 = 32 * b0 / PER_ROW;
+            float v[32 * NBP / PER_ROW];
 #pragma unroll
-                        for (int i = 0; i < per; i++)
-                            O[rt][2 * b0 + i] = joined(O[rt][2 * b0 + i], v[i], jn);
-                    }
-                } else {
-                    const int rr = first + 16 * rt + jr;
-                    if (rr < rows) {
-                        const int64_t row =
-                            (int64_t)(s.q0 + rr / G) * a.Hq + head * G + rr % G;
-                        float* to = part_o(a, row, plan.segs, seg) + 32 * b0 + jp * per;
+            for (int i = 0; i < per; i++) v[i] = 0.0f;
 #pragma unroll
-                        for (int i = 0; i < per; i++) to[i] = v[i];
-                        if (b0 == 0 && jp == 0) {
-                            float* rl = part_rl(a, row, plan.segs, seg);
-                            rl[0] = sr;
-                            rl[1] = sl;
-                        }
+            for (int w = 0; w < WAVES; w++)
+                if (f[w] >= 0.0f || f[w] != f[w]) {
+#pragma unroll
+                    for (int i = 0; i < per; i++)
+                        v[i] = __builtin_fmaf(f[w], s_o[w][jr * LD + jp * per + i], v[i]);
+                }
+            if (plan.splits == 1) {
+#pragma unroll
+                for (int i = 0; i < per; i++) O[o0 + i] = joined(O[o0 + i], v[i], jn);
+            } else {
+                const int rr = first + jr;
+                if (rr < rows) {
+                    const int64_t row = (int64_t)(s.q0 + rr / G) * a.Hq + head * G + rr % G;
+                    float* to = part_o(a, row, plan.segs, seg) + 32 * b0 + jp * per;
+#pragma unroll
+                    for (int i = 0; i < per; i++) to[i] = v[i];
+                    if (b0 == 0 && jp == 0) {
+                        float* rl = part_rl(a, row, plan.segs, seg);
+                        rl[0] = sr;
+                        rl[1] = sl;
                     }
                 }
-                __syncthreads();
             }
+            __syncthreads();
         }
     }
     if (plan.splits > 1) return;
+    const int rr = first + jr;
+    if (rr >= rows) return;
+    float* out = a.out + ((int64_t)(s.q0 + rr / G) * a.Hq + head * G + rr % G) * D;
 #pragma unroll
-    for (int rt = 0; rt < R; rt++) {
-        const int rr = first + 16 * rt + jr;
-        if (rr >= rows) continue;
-        float* out = a.out + ((int64_t)(s.q0 + rr / G) * a.Hq + head * G + rr % G) * D;
+    for (int b0 = 0; b0 < NB; b0 += NBP) {
+        const int per = 32 * (NB - b0 < NBP ? NB - b0 : NBP) / PER_ROW, o0 = 32 * b0 / PER_ROW;
 #pragma unroll
-        for (int b0 = 0; b0 < NB; b0 += NBP) {
-            const int per = 2 * (NB - b0 < NBP ? NB - b0 : NBP);
-#pragma unroll
-            for (int i = 0; i < per; i++)
-                out[32 * b0 + jp * per + i] = result(O[rt][2 * b0 + i], L[rt]);
-        }
+        for (int i = 0; i < per; i++) out[32 * b0 + jp * per + i] = result(O[o0 + i], L);
     }
 }
 
 // Joins the segments of a row in ascending order, as k_attn does when it has
 // them all: one workgroup per row and query head, one element a thread.  The
-// references' running maxima come from a scan over 64 segments at a time.
+// references' running maxima come from a scan, so only two multiplications and
+// an addition a segment stand in the chain; the segments' results come 8192
+// floats at a time through LDS, the next lot in registers meanwhile.
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, int segs) {
     const KvArgs& kv = a.kv;
-    const int t = blockIdx.x / a.Hq, lane = threadIdx.x & 63;
-    const int D = 32 * kv.nb, e = threadIdx.x;
+    constexpr int LOT = 8192;
+    __shared__ __align__(16) float s_o[LOT];
+    __shared__ float s_a[64], s_b[64], s_l[64];
+    const int t = blockIdx.x / a.Hq, tid = threadIdx.x, lane = tid & 63;
+    const int D = 32 * kv.nb;
     const int b = seq_of_row(kv, t);
     if (b < 0) return;
     const Seq s = seq_of(kv, b);
     if (t < s.q0 || t >= s.q0 + s.n) return;
-    const int pos = s.len - s.n + (t - s.q0);
+    const int pos = s.len - s.n + (t - s.q0), SEG = seg_of(kv.nb);
     const int64_t row = blockIdx.x;
     const int lo = a.window && pos + 1 > a.window ? (pos + 1 - a.window) / SEG : 0;
     const int hi = pos < 0 ? lo : pos / SEG + 1;
-    const float* po = part_o(a, row, segs, 0) + (e < D ? e : 0);
+    const int most = kv.nb <= 4 ? 64 : 32;  // segments of a lot
+    const float* po = part_o(a, row, segs, 0);
     const float* rl = part_rl(a, row, segs, 0);
+    float4 v[LOT / 1024];
+    float r = NO_KEY, l = 0.0f;
+    const auto fetch = [&](int c0) {
+        const int m = hi - c0 < most ? hi - c0 : most;
+        const float* from = po + (int64_t)c0 * D;
+#pragma unroll
+        for (int i = 0; i < LOT / 1024; i++) {
+            const int at = 4 * (tid + 256 * i);
+            v[i] = make_float4(0, 0, 0, 0);
+            if (at < m * D) v[i] = *reinterpret_cast<const float4*>(from + at);
+        }
+        const bool has = lane < m;
+        r = has ? rl[2 * (int64_t)(c0 + lane)] : NO_KEY;
+        l = has ? rl[2 * (int64_t)(c0 + lane) + 1] : 0.0f;
+    };
     float O = 0.0f, L = 0.0f, R = NO_KEY;
-    for (int c0 = lo; c0 < hi; c0 += 64) {
-        const int c = c0 + lane;
-        const float r = c < hi ? rl[2 * (int64_t)c] : NO_KEY;
-        const float l = c < hi ? rl[2 * (int64_t)c + 1] : 0.0f;
-        float top = fmaxf(R, r);  // maximum up to and with segment c
+    if (lo < hi) fetch(lo);
+    for (int c0 = lo; c0 < hi; c0 += most) {
+        const int m = hi - c0 < most ? hi - c0 : most;
+        float top = fmaxf(R, r);  // maximum up to and with segment c0 + lane
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
-            const float v = __shfl_up(top, o);
-            if (lane >= o) top = fmaxf(top, v);
+            const float x = __shfl_up(top, o);
+            if (lane >= o) top = fmaxf(top, x);
         }
         float before = __shfl_up(top, 1);
         if (lane == 0) before = R;
-        R = before;
-        const Join j = join(R, r);
         R = __shfl(top, 63);
-        const int m = hi - c0 < 64 ? hi - c0 : 64;
-        for (int i = 0; i < m; i++) {
-            const float rc = __shfl(r, i);
-            if (rc == NO_KEY) continue;
-            const Join k{__shfl(j.a, i), __shfl(j.b, i)};
-            O = joined(O, po[(int64_t)(c0 + i) * D], k);
-            L = joined(L, __shfl(l, i), k);
+        const Join j = join(before, r);
+        if (tid < 64) {
+            s_a[lane] = j.a;
+            s_b[lane] = j.b;
+            s_l[lane] = l;
         }
+#pragma unroll
+        for (int i = 0; i < LOT / 1024; i++)
+            *reinterpret_cast<float4*>(&s_o[4 * (tid + 256 * i)]) = v[i];
+        __syncthreads();
+        if (c0 + most < hi) fetch(c0 + most);
+        if (tid < D) {
+#pragma unroll 8
+            for (int i = 0; i < m; i++) {
+                const Join k{s_a[i], s_b[i]};
+                O = joined(O, s_o[i * D + tid], k);
+                L = joined(L, s_l[i], k);
+            }
+        }
+        __syncthreads();
     }
-    if (e < D) a.out[row * D + e] = result(O, L);
+    if (tid < D) a.out[row * D + tid] = result(O, L);
+}
+
+// Packed tiles of 8 rows where the sequences of a call have that few per
+// key/value head on average: beyond, tiles of 16 rows do more per product.
+bool packs(bool one, int64_t T, int64_t B, int64_t G, int nb) {
+    return nb <= 4 && (one ? G <= 8 : T * G <= 8 * B);
 }
 
 // one: a row each (no starts).
 Plan plan_of(bool one, int64_t T, int64_t B, int Hq, int Hkv, int nb, int64_t max_len) {
     const int64_t G = Hq / Hkv;
     Plan p;
-    p.R = 1;
-    const int64_t tr = 16 * p.R;
+    p.pack = packs(one, T, B, G, nb);
+    const int64_t tr = p.pack ? 8 : 16;
     p.tiles = (int32_t)(one ? B * ((G + tr - 1) / tr) : T * G / tr + B);
-    p.segs = (int32_t)((max_len + SEG - 1) / SEG);
+    p.segs = (int32_t)((max_len + seg_of(nb) - 1) / seg_of(nb));
     const int64_t want = 1024, groups = (int64_t)p.tiles * Hkv;
     int64_t splits = groups >= want / 2 ? 1 : (want + groups - 1) / groups;
     if (splits > p.segs) splits = p.segs;
@@ -606,7 +793,13 @@ Plan plan_of(bool one, int64_t T, int64_t B, int Hq, int Hkv, int nb, int64_t ma
 template <int NB>
 void launch_nb(const AttnArgs& a, const Plan& p, hipStream_t s) {
     const dim3 grid((unsigned)((int64_t)p.tiles * p.splits * a.kv.Hkv));
-    hipLaunchKernelGGL((k_attn<NB, 1>), grid, dim3(64 * WAVES), 0, s, a, p);
+    if constexpr (NB <= 4) {
+        if (p.pack) {
+            hipLaunchKernelGGL((k_attn<NB, true>), grid, dim3(64 * WAVES), 0, s, a, p);
+            return;
+        }
+    }
+    hipLaunchKernelGGL((k_attn<NB, false>), grid, dim3(64 * WAVES), 0, s, a, p);
 }
 
 }  // namespace
@@ -632,8 +825,7 @@ int launch_kv_attention(const AttnArgs& a, hipStream_t s) {
     }
     int rc = (int)hipGetLastError();
     if (rc || p.splits == 1) return rc;
-    const unsigned block = (unsigned)((32 * a.kv.nb + 63) / 64 * 64);
-    hipLaunchKernelGGL(k_attn_join, dim3((unsigned)((int64_t)a.kv.T * a.Hq)), dim3(block), 0, s, a,
+    hipLaunchKernelGGL(k_attn_join, dim3((unsigned)((int64_t)a.kv.T * a.Hq)), dim3(256), 0, s, a,
                        p.segs);
     return (int)hipGetLastError();
 }

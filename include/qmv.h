@@ -461,8 +461,9 @@ int qmv_kv_append(const qmv_kv* kv, const qmv_kv_batch* seqs, const float* q, in
  * Rows without a token or a page are left alone. */
 int qmv_kv_read(const qmv_kv* kv, const qmv_kv_batch* seqs, float* k, float* v, void* stream);
 
-/* Bytes of workspace of qmv_kv_attention; 0 for an invalid shape.  It does
- * not shrink as T, B or max_len grow. */
+/* Bytes of workspace of qmv_kv_attention; 0 for an invalid shape.  Few rows
+ * over long sequences are split over the chip and need room for the parts, so
+ * more rows may need less. */
 size_t qmv_kv_attention_bytes(int64_t T, int64_t B, int q_heads, int kv_heads, int head_dim,
                               int64_t max_len);
 

@@ -144,11 +144,10 @@ def test_attention_workspace():
     for n in (1, 100, 511, 512, 513, 4096, 70000, 1 << 20):
         assert f(1, 1, 32, 8, 128, n) >= max(last, 16)
         last = f(1, 1, 32, 8, 128, n)
-    last = 0
     for t in (1, 2, 7, 16, 100, 511, 512, 513, 4096, 1 << 20):
-        assert f(t, t, 32, 8, 128, 4096) >= last
-        assert f(t, 1, 32, 8, 128, 4096) >= 16
-        last = f(t, t, 32, 8, 128, 4096)
+        assert f(t, t, 32, 8, 128, 4096) >= 16 and f(t, 1, 32, 8, 128, 4096) >= 16
+    # few rows of a long context: the workspace holds parts; many rows: nothing to hold
+    assert f(1, 1, 32, 8, 128, 4096) > 32 * 128 * 4 * 2 and f(1 << 20, 1 << 20, 32, 8, 128, 4096) == 16
 
 
 def test_helpers_refuse_on_the_host():
