@@ -17,123 +17,171 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "qmv_internal.h"
 #include "qmv_kv_device.h"
+#include "qmv_lanes.h"
 
 namespace qmv {
 namespace {
 
 // --------------------------------------------------------------- append ----
-constexpr int HEADS = 8;  // heads (of q, k and v together) per workgroup
+// One workgroup: some heads of one row, 8 adjacent elements a thread, which are
+// a K code word, or 4 V code bytes, once quantised; the 4 threads of a 32-block
+// find its largest magnitude by lane exchange, so nothing goes through LDS but
+// the row's sines and cosines.  The rotation runs in f64 from the angle to the
+// result (an angle of a far position loses its low bits in f32, and a value next
+// to a rounding border decides a 4-bit code), rounded once to f32.
+//
+// A thread needs its elements' partners: within its 8 when pairs are adjacent,
+// 8 others when they are halves apart, loaded a second time.  VEC: 16-byte loads
+// and stores (aligned rows, partners in whole eights).
+template <bool VEC>
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+    if constexpr (VEC) {
+        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; e++) x[e] = p[e];
+    }
+}
 
-// One workgroup: HEADS heads of one row.  The rotation runs in f64 from the
-// angle to the result (an angle of a far position loses its low bits in f32,
-// and a value next to a rounding border decides a 4-bit code), rounded once
-// to f32; rotated keys and the values are staged in LDS and quantised by 4
-// lanes per 32-element block.
-__global__ __launch_bounds__(256) void k_kv_append(AppendArgs a) {
+// Q4_0 codes of the thread's 8 of a 32-block, and the block's scale (every lane
+// of the 4 takes part).
+__device__ __forceinline__ _Float16 quantise8(const float (&x)[8], int g, uint32_t (&code)[8]) {
+    float big = -1.0f, top = 0.0f;
+    int at = 0, bad = 0;
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+        bad |= !__builtin_isfinite(x[e]);
+        if (fabsf(x[e]) > big) {
+            big = fabsf(x[e]);
+            top = x[e];
+            at = 8 * g + e;
+        }
+    }
+    const auto meet = [&](float ob, float ot, int oa, int obad) {  // the first of the largest magnitude
+        bad |= obad;
+        if (ob > big || (ob == big && oa < at)) {
+            big = ob;
+            top = ot;
+            at = oa;
+        }
+    };
+    meet(dpp<DPP_XOR1>(big), dpp<DPP_XOR1>(top), dpp<DPP_XOR1>(at), dpp<DPP_XOR1>(bad));
+    meet(dpp<DPP_XOR2>(big), dpp<DPP_XOR2>(top), dpp<DPP_XOR2>(at), dpp<DPP_XOR2>(bad));
+    const float d = top / -8.0f;
+    const float r = 1.0f / d, id = __builtin_isinf(r) ? 0.0f : r;
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+        const int c = (int)(x[e] * id + 8.5f);
+        code[e] = bad ? 8u : (uint32_t)(c > 15 ? 15 : c);
+    }
+    return bad ? (_Float16)__builtin_nanf("") : (_Float16)d;
+}
+
+template <bool VEC>
+__global__ __launch_bounds__(256) void k_kv_append(AppendArgs a, int passes) {
     const KvArgs& kv = a.kv;
     __shared__ double turn[2][128];
-    extern __shared__ float stage[];  // [HEADS][D]
     const int t = blockIdx.x, tid = threadIdx.x;
-    const int D = 32 * kv.nb;
+    const int D = 32 * kv.nb, eights = 4 * kv.nb;  // of a head
+    const int hp = 256 / eights, hu = tid / eights, w = tid - hu * eights;  // heads a pass
+    const int units = a.Hq + 2 * kv.Hkv;
+    const int half = a.rot >> 1;
+    int apart = 0;
+    if (a.halves && 8 * w < a.rot) apart = 8 * w < half ? half : -half;
+    // a pass's elements and their partners, loaded a pass ahead, and the first before anything else
+    float x[8], p[8];
+    const auto fetch = [&](int pass) {
+        const int u = ((int)blockIdx.y * passes + pass) * hp + hu;
+        if (pass >= passes || hu >= hp || u >= units) return;
+        const bool is_q = u < a.Hq, is_v = u >= a.Hq + kv.Hkv;
+        const float* src = is_q ? a.q + (int64_t)t * a.q_stride + (int64_t)u * D
+                         : is_v ? a.v + (int64_t)t * a.v_stride + (int64_t)(u - a.Hq - kv.Hkv) * D
+                                : a.k + (int64_t)t * a.k_stride + (int64_t)(u - a.Hq) * D;
+        load8<VEC>(src + 8 * w, x);
+        if (a.halves && !is_v) {
+            if constexpr (VEC) {
+                load8<true>(src + 8 * w + apart, p);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                    const int i = 8 * w + e;
+                    p[e] = src[i >= a.rot ? i : i < half ? i + half : i - half];
+                }
+            }
+        }
+    };
+    fetch(0);
     const int b = seq_of_row(kv, t);
     if (b < 0) return;
     const Seq s = seq_of(kv, b);
     const int pos = s.len - s.n + (t - s.q0);
     if (t < s.q0 || t >= s.q0 + s.n || pos < 0) return;  // uniform per workgroup
-    const int half = a.rot >> 1;
     if (tid < half) {
         double sn, cs;
         sincos((double)pos * a.freq[tid], &sn, &cs);
         turn[0][tid] = cs;
         turn[1][tid] = sn;
     }
-    __syncthreads();
-    const int u0 = blockIdx.y * HEADS, units = a.Hq + 2 * kv.Hkv;
-    const int heads = units - u0 < HEADS ? units - u0 : HEADS;
-    const int pairs = D >> 1;
-    for (int i = tid; i < heads * pairs; i += 256) {
-        const int hu = i / pairs, j = i - hu * pairs, u = u0 + hu;
-        const bool is_q = u < a.Hq, is_v = u >= a.Hq + kv.Hkv;
-        const float* src = is_q ? a.q + (int64_t)t * a.q_stride + (int64_t)u * D
-                         : is_v ? a.v + (int64_t)t * a.v_stride + (int64_t)(u - a.Hq - kv.Hkv) * D
-                                : a.k + (int64_t)t * a.k_stride + (int64_t)(u - a.Hq) * D;
-        float* dst = is_q ? a.q_out + ((int64_t)t * a.Hq + u) * D : stage + hu * D;
-        int e0 = 2 * j, e1 = 2 * j + 1;
-        if (a.halves && j < half) {
-            e0 = j;
-            e1 = j + half;
-        }
-        const float x0 = src[e0], x1 = src[e1];
-        if (!is_v && j < half) {
-            const double c = turn[0][j], n = turn[1][j];
-            dst[e0] = (float)((double)x0 * c - (double)x1 * n);
-            dst[e1] = (float)((double)x0 * n + (double)x1 * c);
-        } else {
-            dst[e0] = x0;
-            dst[e1] = x1;
-        }
-    }
-    __syncthreads();
     const int page = page_of(kv, b, pos);
-    if (page < 0) return;
-    const int off = pos & ((1 << kv.log2p) - 1), g = tid & 3;
+    __syncthreads();
+    const int bb = w >> 2, g = w & 3;
+    double c[8], n[8];  // y[e] = x[e] c[e] + partner[e] n[e]
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+        const int i = 8 * w + e;
+        const int j = a.halves ? (i < half ? i : i - half) : i >> 1;
+        const bool turned = i < a.rot, second = a.halves ? i >= half : i & 1;
+        c[e] = turned ? turn[0][j] : 1.0;
+        n[e] = turned ? (second ? turn[1][j] : -turn[1][j]) : 0.0;
+    }
+    const int off = pos & ((1 << kv.log2p) - 1);
     const int64_t page_codes = (int64_t)(16 * kv.nb) << kv.log2p;
-    const int blocks = heads * kv.nb;  // 4 lanes each: every lane of a group agrees on `live`
-    for (int i0 = 0; i0 < blocks; i0 += 64) {
-        const int blk = i0 + (tid >> 2), hu = blk / kv.nb, bb = blk - hu * kv.nb, u = u0 + hu;
-        const bool live = blk < blocks && u >= a.Hq;
-        float x[8];
-        float big = -1.0f, top = 0.0f;
-        int at = 0, bad = 0;
+    for (int pass = 0; pass < passes; pass++) {
+        const int u = ((int)blockIdx.y * passes + pass) * hp + hu;
+        const bool live = hu < hp && u < units;
+        const bool is_q = u < a.Hq, is_v = u >= a.Hq + kv.Hkv;
+        float y[8];
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-            x[e] = live ? stage[hu * D + 32 * bb + 8 * g + e] : 0.0f;
-            bad |= !__builtin_isfinite(x[e]);
-            if (fabsf(x[e]) > big) {
-                big = fabsf(x[e]);
-                top = x[e];
-                at = 8 * g + e;
+            const float q = a.halves ? p[e] : x[e ^ 1];
+            y[e] = is_v || 8 * w + e >= a.rot ? x[e] : (float)((double)x[e] * c[e] + (double)q * n[e]);
+        }
+        fetch(pass + 1);
+        if (a.halves) __syncthreads();  // q in place: partners are read before any is written
+        if (live && is_q) {
+            float* dst = a.q_out + ((int64_t)t * a.Hq + u) * D + 8 * w;
+            if constexpr (VEC) {
+                *reinterpret_cast<float4*>(dst) = make_float4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<float4*>(dst + 4) = make_float4(y[4], y[5], y[6], y[7]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; e++) dst[e] = y[e];
             }
         }
+        if (live && !is_q && page >= 0) {  // the same for the 4 threads of a block
+            uint32_t code[8];
+            const _Float16 dh = quantise8(y, g, code);
+            uint8_t* hd = head_of(kv, page, is_v ? u - a.Hq - kv.Hkv : u - a.Hq);
+            if (is_v) {
+                uint8_t* to = hd + page_codes + (int64_t)(off >> 2) * 64 * kv.nb + (off & 3);
 #pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {  // the first of the largest magnitude
-            const float ob = __shfl_xor(big, o), ot = __shfl_xor(top, o);
-            const int oa = __shfl_xor(at, o);
-            bad |= __shfl_xor(bad, o);
-            if (ob > big || (ob == big && oa < at)) {
-                big = ob;
-                top = ot;
-                at = oa;
+                for (int m = 0; m < 4; m++)
+                    to[((4 * g + m) * kv.nb + bb) * 4] = (uint8_t)(code[2 * m] | (code[2 * m + 1] << 4));
+            } else {
+                uint32_t word = 0;
+#pragma unroll
+                for (int e = 0; e < 8; e++) word |= code[e] << (4 * k_nibble(e));
+                *reinterpret_cast<uint32_t*>(hd + (int64_t)off * 16 * kv.nb + (g * kv.nb + bb) * 4) = word;
             }
-        }
-        if (!live) continue;
-        const float d = top / -8.0f;
-        const float r = 1.0f / d, id = __builtin_isinf(r) ? 0.0f : r;
-        uint32_t code[8];
-#pragma unroll
-        for (int e = 0; e < 8; e++) {
-            const int c = (int)(x[e] * id + 8.5f);
-            code[e] = bad ? 8u : (uint32_t)(c > 15 ? 15 : c);
-        }
-        const _Float16 dh = bad ? (_Float16)__builtin_nanf("") : (_Float16)d;
-        const bool is_v = u >= a.Hq + kv.Hkv;
-        uint8_t* hd = head_of(kv, page, is_v ? u - a.Hq - kv.Hkv : u - a.Hq);
-        if (is_v) {
-            uint8_t* c = hd + page_codes + (int64_t)(off >> 2) * 64 * kv.nb + (off & 3);
-#pragma unroll
-            for (int m = 0; m < 4; m++)
-                c[((4 * g + m) * kv.nb + bb) * 4] = (uint8_t)(code[2 * m] | (code[2 * m + 1] << 4));
-        } else {
-            uint32_t w = 0;
-#pragma unroll
-            for (int e = 0; e < 8; e++) w |= code[e] << (4 * k_nibble(e));
-            *reinterpret_cast<uint32_t*>(hd + (int64_t)off * 16 * kv.nb + (g * kv.nb + bb) * 4) = w;
-        }
-        if (g == 0) {
-            _Float16* sc = reinterpret_cast<_Float16*>(hd + 2 * page_codes);
-            if (is_v) sc += (int64_t)kv.nb << kv.log2p;
-            sc[off * kv.nb + bb] = dh;
+            if (g == 0) {
+                _Float16* sc = reinterpret_cast<_Float16*>(hd + 2 * page_codes);
+                if (is_v) sc += (int64_t)kv.nb << kv.log2p;
+                sc[off * kv.nb + bb] = dh;
+            }
         }
     }
 }
@@ -177,9 +225,16 @@ __global__ __launch_bounds__(256) void k_kv_read(KvArgs kv, float* __restrict__ 
 }  // namespace
 
 int launch_kv_append(const AppendArgs& a, hipStream_t s) {
-    const int units = a.Hq + 2 * a.kv.Hkv;
-    hipLaunchKernelGGL(k_kv_append, dim3((unsigned)a.kv.T, (unsigned)((units + HEADS - 1) / HEADS)),
-                       dim3(256), (size_t)HEADS * 32 * a.kv.nb * 4, s, a);
+    const int units = a.Hq + 2 * a.kv.Hkv, hp = 256 / (4 * a.kv.nb);
+    // few rows: one pass of heads a workgroup; many: all of a row's heads, its sines once
+    const int all = (units + hp - 1) / hp;
+    const int passes = (int64_t)a.kv.T * all >= 2048 ? all : 1;
+    const bool vec = aligned16(a.q) && aligned16(a.k) && aligned16(a.v) && aligned16(a.q_out) &&
+                     (a.q_stride | a.k_stride | a.v_stride) % 4 == 0 &&
+                     (!a.halves || a.rot % 16 == 0);
+    const dim3 grid((unsigned)a.kv.T, (unsigned)((all + passes - 1) / passes));
+    if (vec) hipLaunchKernelGGL(k_kv_append<true>, grid, dim3(256), 0, s, a, passes);
+    else hipLaunchKernelGGL(k_kv_append<false>, grid, dim3(256), 0, s, a, passes);
     return (int)hipGetLastError();
 }
 

@@ -42,6 +42,7 @@
 #include <stdint.h>
 
 #include "qmv_kv_device.h"
+#include "qmv_lanes.h"
 
 namespace qmv {
 namespace {
@@ -143,9 +144,7 @@ __device__ __forceinline__ Split times(Split s, half2v d) {
 }
 
 // The value of lane n ^ 8 among 16.
-__device__ __forceinline__ float across8(float x) {
-    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(x), __float_as_int(x), 0x128, 0xF, 0xF, false));
-}
+__device__ __forceinline__ float across8(float x) { return dpp<DPP_ROR8>(x); }
 
 __device__ __forceinline__ float exp2_raw(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -338,8 +337,7 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
         for (int bb = 0; bb < NB; bb++)
 #pragma unroll
             for (int e = 0; e < 8; e++) big = fmaxf(big, fabsf(x[bb][e]));
-        big = fmaxf(big, __shfl_xor(big, 16));
-        big = fmaxf(big, __shfl_xor(big, 32));
+        big = max_rows(big);
         int ex = (int)((__float_as_uint(big) >> 23) & 255) - 126;  // big < 2^ex
         ex = ex < -100 ? -100 : ex;
         const float up = ldexpf(1.0f, 15 - ex);
@@ -374,6 +372,7 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
             const bool masked = t0 + SUB > pos_lo + 1 || (a.window && t0 <= pos_hi - a.window) ||
                                 there != (1u << TILES) - 1;
             const uint32_t here = there;
+            const bool more = works(seg + 1);
             if (TILES == 8 || lane < 8 * TILES) {
                 const int u = lane >> 3, t = t0 + 16 * u + 2 * (lane & 7);
                 const int live = ((here >> u) & 1) ? s.len - t : 0;  // positions behind the last: scale 0
@@ -414,8 +413,7 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
                     half2v v = {half_of(dv.w[i >> 1], i & 1), half_of(dv.w[(NB + i) >> 1], (NB + i) & 1)};
                     v[0] = bad[0] ? (_Float16)0.0f : (_Float16)((float)v[0] * down[0]);
                     v[1] = bad[1] ? (_Float16)0.0f : (_Float16)((float)v[1] * down[1]);
-                    const uint32_t own = word(v), other = (uint32_t)__builtin_amdgcn_update_dpp(
-                                                      (int)own, (int)own, 0xB1, 0xF, 0xF, false);
+                    const uint32_t own = word(v), other = dpp_bits<DPP_XOR1>(own);
                     s_dv[wave][i][lane] = lane & 1 ? (other >> 16) | (own & 0xFFFF0000u)
                                                    : (own & 0xFFFFu) | (other << 16);
                 }
@@ -493,8 +491,7 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
 #pragma unroll
                 for (int i = 0; i < 4; i++) top = fmaxf(top, sc[U][i]);
             if constexpr (PACK) top = fmaxf(top, across8(top));
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
+            top = max_rows(top);
             const float ref = top > -INFINITY ? top - 14.0f : 0.0f;
             float sum[2] = {0.0f, 0.0f};  // over the even and the odd tiles
             Split p[SLOTS][2];            // positions 0, 2 and 1, 3
@@ -512,8 +509,7 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
                 p[U][1] = two_parts(sc[U][1], sc[U][3]);
             }
             l = sum[0] + (PACK ? across8(sum[0]) : sum[1]);
-            l += __shfl_xor(l, 16);
-            l += __shfl_xor(l, 32);
+            l = sum_rows(l);
             // no maximum: nothing seen, or NaN scores, whose sum is NaN and stays
             r = top == -INFINITY && l == 0.0f ? NO_KEY : ref;
 
@@ -539,7 +535,6 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
                 o[2 * bb] = mfma(even, ph, o[2 * bb]);
                 o[2 * bb + 1] = mfma(odd, ph, o[2 * bb + 1]);
             };
-            const bool more = works(seg + 1);
             if (more) fetch_scales(seg + 1);
             fetch_pages(seg + 2);
             if constexpr (PACK) {
@@ -694,16 +689,21 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
 }
 
 // Joins the segments of a row in ascending order, as k_attn does when it has
-// them all: one workgroup per row and query head, one element a thread.  The
-// references' running maxima come from a scan, so only two multiplications and
-// an addition a segment stand in the chain; the segments' results come 8192
-// floats at a time through LDS, the next lot in registers meanwhile.
+// them all: one workgroup per row, query head and W elements (all, or 32 where
+// rows are few and segments many), one element a thread and the sum of the
+// weights in one more.  Only a multiplication and an addition a segment stand
+// in the chain: the references' running maxima come from a scan, and every
+// part is multiplied by its factor on its way to LDS, LOT segments at a time,
+// from where the chain takes four at a read.
+template <int W>  // below 256
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, int segs) {
     const KvArgs& kv = a.kv;
-    constexpr int LOT = 8192;
-    __shared__ __align__(16) float s_o[LOT];
-    __shared__ float s_a[64], s_b[64], s_l[64];
-    const int t = blockIdx.x / a.Hq, tid = threadIdx.x, lane = tid & 63;
+    constexpr int LOT = 8192 / W / 4 * 4 < 256 ? 8192 / W / 4 * 4 : 256;  // segments
+    constexpr int LD = LOT + 4, HELD = (LOT * W / 4 + 255) / 256;
+    __shared__ __align__(16) float s_x[(W + 1) * LD];  // part * b: [element, then the sum][segment]
+    __shared__ __align__(16) float s_a[LD];
+    __shared__ float s_b[LD], s_top[4];
+    const int t = blockIdx.x / a.Hq, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int D = 32 * kv.nb;
     const int b = seq_of_row(kv, t);
     if (b < 0) return;
@@ -713,59 +713,76 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, int segs) {
     const int64_t row = blockIdx.x;
     const int lo = a.window && pos + 1 > a.window ? (pos + 1 - a.window) / SEG : 0;
     const int hi = pos < 0 ? lo : pos / SEG + 1;
-    const int most = kv.nb <= 4 ? 64 : 32;  // segments of a lot
-    const float* po = part_o(a, row, segs, 0);
+    const float* po = part_o(a, row, segs, 0) + W * blockIdx.y;
     const float* rl = part_rl(a, row, segs, 0);
-    float4 v[LOT / 1024];
-    float r = NO_KEY, l = 0.0f;
+    float4 v[HELD];
+    float r = NO_KEY, l = 0.0f;  // of segment c0 + tid
     const auto fetch = [&](int c0) {
-        const int m = hi - c0 < most ? hi - c0 : most;
-        const float* from = po + (int64_t)c0 * D;
+        const int m = hi - c0 < LOT ? hi - c0 : LOT;
 #pragma unroll
-        for (int i = 0; i < LOT / 1024; i++) {
-            const int at = 4 * (tid + 256 * i);
+        for (int i = 0; i < HELD; i++) {
+            const int at = tid + 256 * i, c = at / (W / 4), e = at % (W / 4);
             v[i] = make_float4(0, 0, 0, 0);
-            if (at < m * D) v[i] = *reinterpret_cast<const float4*>(from + at);
+            if (c < m) v[i] = *reinterpret_cast<const float4*>(po + (int64_t)(c0 + c) * D + 4 * e);
         }
-        const bool has = lane < m;
-        r = has ? rl[2 * (int64_t)(c0 + lane)] : NO_KEY;
-        l = has ? rl[2 * (int64_t)(c0 + lane) + 1] : 0.0f;
+        const bool has = tid < m;
+        r = has ? rl[2 * (int64_t)(c0 + tid)] : NO_KEY;
+        l = has ? rl[2 * (int64_t)(c0 + tid) + 1] : 0.0f;
     };
-    float O = 0.0f, L = 0.0f, R = NO_KEY;
+    float O = 0.0f, R = NO_KEY;
     if (lo < hi) fetch(lo);
-    for (int c0 = lo; c0 < hi; c0 += most) {
-        const int m = hi - c0 < most ? hi - c0 : most;
-        float top = fmaxf(R, r);  // maximum up to and with segment c0 + lane
+    for (int c0 = lo; c0 < hi; c0 += LOT) {
+        const int m = hi - c0 < LOT ? hi - c0 : LOT;
+        float top = r;  // maximum up to and with the thread's segment: in its wave, then in all
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
             const float x = __shfl_up(top, o);
             if (lane >= o) top = fmaxf(top, x);
         }
-        float before = __shfl_up(top, 1);
-        if (lane == 0) before = R;
-        R = __shfl(top, 63);
-        const Join j = join(before, r);
-        if (tid < 64) {
-            s_a[lane] = j.a;
-            s_b[lane] = j.b;
-            s_l[lane] = l;
-        }
-#pragma unroll
-        for (int i = 0; i < LOT / 1024; i++)
-            *reinterpret_cast<float4*>(&s_o[4 * (tid + 256 * i)]) = v[i];
+        if (lane == 63) s_top[wave] = top;
         __syncthreads();
-        if (c0 + most < hi) fetch(c0 + most);
-        if (tid < D) {
-#pragma unroll 8
-            for (int i = 0; i < m; i++) {
-                const Join k{s_a[i], s_b[i]};
-                O = joined(O, s_o[i * D + tid], k);
-                L = joined(L, s_l[i], k);
+        float before = R;
+        for (int w = 0; w < wave; w++) before = fmaxf(before, s_top[w]);
+        const float up = __shfl_up(top, 1);
+        if (lane) before = fmaxf(before, up);
+        R = fmaxf(R, fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3])));
+        const Join j = join(before, r);
+        if (tid < LOT) {  // segments past the last: a = 1, part 0
+            const bool has = tid < m && r != NO_KEY;
+            s_a[tid] = has ? j.a : 1.0f;
+            s_b[tid] = has ? j.b : -1.0f;
+            s_x[W * LD + tid] = has ? l * j.b : 0.0f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < HELD; i++) {
+            const int at = tid + 256 * i, c = at / (W / 4), e = at % (W / 4);
+            if (c < LOT && c < m + 3) {  // the chain reads up to the next multiple of 4
+                const float f = s_b[c];
+                const bool has = !(f < 0.0f);  // (nothing was written for a segment without keys)
+                float* to = &s_x[4 * e * LD + c];
+                to[0] = has ? v[i].x * f : 0.0f;
+                to[LD] = has ? v[i].y * f : 0.0f;
+                to[2 * LD] = has ? v[i].z * f : 0.0f;
+                to[3 * LD] = has ? v[i].w * f : 0.0f;
+            }
+        }
+        __syncthreads();
+        if (c0 + LOT < hi) fetch(c0 + LOT);
+        if (tid <= W) {
+#pragma unroll 4
+            for (int i = 0; i < m; i += 4) {
+                const f4 k = *reinterpret_cast<const f4*>(&s_a[i]);
+                const f4 x = *reinterpret_cast<const f4*>(&s_x[tid * LD + i]);
+#pragma unroll
+                for (int e = 0; e < 4; e++) O = O * k[e] + x[e];
             }
         }
         __syncthreads();
     }
-    if (tid < D) a.out[row * D + tid] = result(O, L);
+    if (tid == W) s_b[0] = O;
+    __syncthreads();
+    if (tid < W) a.out[row * D + W * blockIdx.y + tid] = result(O, s_b[0]);
 }
 
 // Packed tiles of 8 rows where the sequences of a call have that few per
@@ -782,8 +799,12 @@ Plan plan_of(bool one, int64_t T, int64_t B, int Hq, int Hkv, int nb, int64_t ma
     const int64_t tr = p.pack ? 8 : 16;
     p.tiles = (int32_t)(one ? B * ((G + tr - 1) / tr) : T * G / tr + B);
     p.segs = (int32_t)((max_len + seg_of(nb) - 1) / seg_of(nb));
-    const int64_t want = 1024, groups = (int64_t)p.tiles * Hkv;
-    int64_t splits = groups >= want / 2 ? 1 : (want + groups - 1) / groups;
+    // One sequence: as many workgroups as run at once (two per CU), each with several segments,
+    // so that the loads ahead work and the prologue is paid once (131072 positions: 44 us, and 48
+    // with twice as many).  Several sequences differ in length: four times as many, which even out
+    // (32 of 301..8191: 64 us, 73 with twice, 97 with one workgroup per sequence and head).
+    const int64_t groups = (int64_t)p.tiles * Hkv, want = B == 1 ? 512 : 2048;
+    int64_t splits = groups >= 512 ? 1 : (want + groups - 1) / groups;
     if (splits > p.segs) splits = p.segs;
     p.per = (int32_t)((p.segs + splits - 1) / splits);
     p.splits = (p.segs + p.per - 1) / p.per;
@@ -825,8 +846,19 @@ int launch_kv_attention(const AttnArgs& a, hipStream_t s) {
     }
     int rc = (int)hipGetLastError();
     if (rc || p.splits == 1) return rc;
-    hipLaunchKernelGGL(k_attn_join, dim3((unsigned)((int64_t)a.kv.T * a.Hq)), dim3(256), 0, s, a,
-                       p.segs);
+    const int64_t joins = (int64_t)a.kv.T * a.Hq;
+    const bool narrow = p.segs >= 64 && joins < 256;
+    const dim3 grid((unsigned)joins, narrow ? (unsigned)a.kv.nb : a.kv.nb == 8 ? 2u : 1u);
+    switch (narrow ? 1 : a.kv.nb) {
+    case 1: hipLaunchKernelGGL(k_attn_join<32>, grid, dim3(256), 0, s, a, p.segs); break;
+    case 2: hipLaunchKernelGGL(k_attn_join<64>, grid, dim3(256), 0, s, a, p.segs); break;
+    case 3: hipLaunchKernelGGL(k_attn_join<96>, grid, dim3(256), 0, s, a, p.segs); break;
+    case 4: hipLaunchKernelGGL(k_attn_join<128>, grid, dim3(256), 0, s, a, p.segs); break;
+    case 5: hipLaunchKernelGGL(k_attn_join<160>, grid, dim3(256), 0, s, a, p.segs); break;
+    case 6: hipLaunchKernelGGL(k_attn_join<192>, grid, dim3(256), 0, s, a, p.segs); break;
+    case 7: hipLaunchKernelGGL(k_attn_join<224>, grid, dim3(256), 0, s, a, p.segs); break;
+    default: hipLaunchKernelGGL(k_attn_join<128>, grid, dim3(256), 0, s, a, p.segs); break;
+    }
     return (int)hipGetLastError();
 }
 

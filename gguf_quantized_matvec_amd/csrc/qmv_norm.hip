@@ -21,6 +21,7 @@
 #include <stdint.h>
 
 #include "qmv_internal.h"
+#include "qmv_lanes.h"
 #include "qmv_step.h"
 
 namespace qmv {
@@ -92,20 +93,19 @@ __device__ __forceinline__ void quantise_chunk(float4 v, bool live, int lane, in
                                                int64_t r, const NormArgs& a, const Layout& L) {
     float amax = amax4(v);
     if constexpr (MODE != 0) {  // one 32-block per 8 lanes
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
+        amax = max8(amax);
         const float d = amax / 127.0f;
         int s4;
         const uint32_t c4 = codes4(v, inv_scale(d), s4);
-        int s16 = s4 + __shfl_xor(s4, 1);
-        s16 += __shfl_xor(s16, 2);            // the sum of this lane's 16-code half
-        const int s16o = __shfl_xor(s16, 4);  // the other half's
-        if (!live) return;
+        int s16 = s4 + dpp<DPP_XOR1>(s4);
+        s16 += dpp<DPP_XOR2>(s16);            // the sum of this lane's 16-code half
+        const int s16o = dpp<DPP_MIRROR8>(s16);  // the other half's
         const int sub = lane & 7;
         const int64_t b = chunk * 8 + (lane >> 3), bi = r * L.nb + b;
         const uint16_t hb = half_bits(d);
         const float dval = half_value(hb);
         const int S = s16 + s16o;
+        if (!live) return;
         uint8_t* pub = a.xq + bi * 34;
         uint16_t* pc = reinterpret_cast<uint16_t*>(pub + 2 + 4 * sub);
         pc[0] = (uint16_t)(c4 & 0xFFFFu);
@@ -143,14 +143,13 @@ __device__ __forceinline__ void quantise_chunk(float4 v, bool live, int lane, in
             }
         }
     } else {  // one superblock per wave; K % 256 == 0, so every lane is live
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
+        amax = max64(amax);
         const float d = amax / 127.0f;
         int s4;
         const uint32_t c4 = codes4(v, inv_scale(d), s4);
-        int s16 = s4 + __shfl_xor(s4, 1);
-        s16 += __shfl_xor(s16, 2);
-        const int s16o = __shfl_xor(s16, 4);
+        int s16 = s4 + dpp<DPP_XOR1>(s4);
+        s16 += dpp<DPP_XOR2>(s16);
+        const int s16o = dpp<DPP_MIRROR8>(s16);
         const int64_t task = r * L.nsb + chunk;
         uint8_t* pub = a.xq + task * 292;
         if (lane == 0) *reinterpret_cast<float*>(pub) = d;
@@ -214,10 +213,10 @@ __global__ __launch_bounds__(1024) void k_add_rmsnorm(NormArgs a, Layout L, int 
     const float* xr = a.x + r * a.K;
     const float* rr = a.res ? a.res + r * a.K : nullptr;
     float* hr = a.h ? a.h + r * a.K : nullptr;
-    float4 keep[V > 0 ? V : 1];
+    float4 keep[V > 0 ? V : 1], weight[V > 0 ? V : 1];
     const int steps = V > 0 ? V : (chunks + waves - 1) / waves;
 #pragma unroll
-    for (int i = 0; i < (V > 0 ? V : 1); i++) keep[i] = make_float4(0, 0, 0, 0);
+    for (int i = 0; i < (V > 0 ? V : 1); i++) keep[i] = weight[i] = make_float4(0, 0, 0, 0);
     const auto first = [&](int i, float4& v) {
         const int c = wave + i * waves;
         if (c >= chunks) return;  // uniform per wave
@@ -225,6 +224,7 @@ __global__ __launch_bounds__(1024) void k_add_rmsnorm(NormArgs a, Layout L, int 
         v = make_float4(0, 0, 0, 0);
         if (e < a.K) {
             v = load4(xr + e, a16);
+            if constexpr (V > 0) weight[i] = load4(a.w + e, a16);  // ahead of the sum
             if (rr) {
                 v = add4(v, load4(rr + e, a16));
                 store4(hr + e, v, a16);
@@ -233,8 +233,7 @@ __global__ __launch_bounds__(1024) void k_add_rmsnorm(NormArgs a, Layout L, int 
         double s = (double)v.x * v.x + (double)v.y * v.y;
         s = s + (double)v.z * v.z;
         s = s + (double)v.w * v.w;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o);
+        s = sum64(s);
         if (lane == 0) chunk_sum[c] = s;
     };
     if constexpr (V > 0) {
@@ -255,7 +254,7 @@ __global__ __launch_bounds__(1024) void k_add_rmsnorm(NormArgs a, Layout L, int 
         float4 y = make_float4(0, 0, 0, 0);
         if (live) {
             if constexpr (V == 0) v = load4(rr ? hr + e : xr + e, a16);
-            const float4 w = load4(a.w + e, a16);
+            const float4 w = V > 0 ? weight[V > 0 ? i : 0] : load4(a.w + e, a16);
             y.x = (float)(((double)v.x * rs) * (double)w.x);
             y.y = (float)(((double)v.y * rs) * (double)w.y);
             y.z = (float)(((double)v.z * rs) * (double)w.z);
@@ -278,7 +277,11 @@ int launch_mode(NormArgs a, const Layout& L, int64_t grid, hipStream_t s) {
     const int a16 = aligned16(a.x) && aligned16(a.w) && (!a.res || aligned16(a.res)) &&
                     (!a.h || aligned16(a.h)) && (!a.y || aligned16(a.y));
     const size_t lds = (size_t)chunks * 8;
-    const int per = chunks <= 16 ? 1 : chunks <= 32 ? 2 : chunks <= 64 ? 4 : 0;
+    // Few rows: as many waves per row as there are chunks, for latency.  Many: two chunks a wave,
+    // so that more rows share a CU and one's loads overlap another's sums (2048 rows of 4096: 31.7
+    // us, 34.6 with one chunk a wave, 34.8 with four).
+    int per = chunks <= 16 ? 1 : chunks <= 32 ? 2 : chunks <= 64 ? 4 : 0;
+    if (a.rows >= 512 && per == 1 && chunks > 1) per = 2;
     const int waves = per ? (chunks + per - 1) / per : 16;
     constexpr int64_t SLICE = 1 << 21;  // a grid holds fewer than 2^32 threads
     for (a.row0 = 0; a.row0 < grid; a.row0 += SLICE) {
