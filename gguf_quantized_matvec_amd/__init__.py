@@ -575,11 +575,34 @@ class _On:
         return False
 
 
+def _on_device(device, stream, call):
+    """call(handle) on a device and stream; the common case, the current stream
+    of the current device, without a context (these calls take microseconds)."""
+    import torch
+    if stream is None and torch.cuda.current_device() == device.index:
+        return call(torch.cuda.current_stream().cuda_stream if _raw_stream is None
+                    else _raw_stream(device.index))
+    with _On(device, stream) as handle:
+        return call(handle)
+
+
+def _find_raw_stream():
+    import torch
+    return getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+try:
+    _raw_stream = _find_raw_stream()  # the handle without a Stream object around it
+except ImportError:
+    _raw_stream = None
+
+
 def _on(t, dtype, what, device):
     """The address of a contiguous tensor of a type on a device."""
-    if t.device != device:
-        raise ValueError(f"{what} must be on {device}, got {t.device}")
-    return _dev(t, dtype, what)
+    if t.dtype is dtype and t.device == device and t.is_contiguous():
+        return t.data_ptr()
+    _dev(t, dtype, what)
+    raise ValueError(f"{what} must be on {device}, got {t.device}")
 
 
 def _add_rmsnorm(q8k, x, w, eps, res, h, y, xq, stream):
@@ -600,16 +623,18 @@ def _add_rmsnorm(q8k, x, w, eps, res, h, y, xq, stream):
         raise ValueError(f"bad shape rows={rows} K={K}")
     if xq is not None and xq.numel() < n:
         raise ValueError(f"xq must hold {n} bytes, got {xq.numel()}")
-    with _On(dev, stream) as s:
-        if xq is None:
-            xq = torch.empty(n, dtype=torch.uint8, device=dev)
-        if h is None and res is not None:
-            h = torch.empty_like(x)
-        fn = qmv_add_rmsnorm_q8_k if q8k else qmv_add_rmsnorm_q8_0
-        fn(xp, None if res is None else _on(res, f32, "res", dev), _on(w, f32, "w", dev), eps, rows,
-           K, None if h is None else _on(h, f32, "h", dev),
-           None if y is None else _on(y, f32, "y", dev), _on(xq, torch.uint8, "xq", dev), s)
-    return h, xq
+    rp, wp = None if res is None else _on(res, f32, "res", dev), _on(w, f32, "w", dev)
+    yp = None if y is None else _on(y, f32, "y", dev)
+
+    def call(s):
+        q = torch.empty(n, dtype=torch.uint8, device=dev) if xq is None else xq
+        out = torch.empty(x.shape, dtype=f32, device=dev) if h is None and res is not None else h
+        (qmv_add_rmsnorm_q8_k if q8k else qmv_add_rmsnorm_q8_0)(
+            xp, rp, wp, eps, rows, K, None if out is None else _on(out, f32, "h", dev), yp,
+            _on(q, torch.uint8, "xq", dev), s)
+        return out, q
+
+    return _on_device(dev, stream, call)
 
 
 def add_rmsnorm(x, w, eps, res=None, h=None, y=None, xq=None, stream=None):
@@ -679,14 +704,14 @@ class KVBatch:
 def _rows(t, T, width, what, device):
     """(address, row stride) of T rows of `width` f32 with adjacent elements."""
     import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
-        raise ValueError(f"{what} must be a tensor on {device}")
-    if t.dtype != torch.float32:
+    if t.device != device:
+        raise ValueError(f"{what} must be on {device}, got {t.device}")
+    if t.dtype is not torch.float32:
         raise TypeError(f"{what} must be torch.float32, got {t.dtype}")
-    if t.dim() != 2 or t.shape != (T, width) or t.stride(1) != 1:
+    if t.shape != (T, width) or t.stride(1) != 1:
         raise ValueError(f"{what} must be [{T}, {width}] with adjacent elements, got "
                          f"{tuple(t.shape)} with strides {t.stride()}")
-    return t.data_ptr(), t.stride(0) if T > 1 else max(width, t.stride(0))
+    return t.data_ptr(), t.stride(0) if T > 1 else width
 
 
 def _heads(q, cache, what="q"):
@@ -719,12 +744,14 @@ def kv_append(cache: KVCache, batch: KVBatch, q, k, v, freq=None, halves: bool =
     rot, fp = 0, None
     if freq is not None:
         rot, fp = 2 * freq.numel(), _on(freq, torch.float64, "freq", dev)
-    with _On(dev, stream) as s:
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.float32, device=dev)
+
+    def call(s):
+        out = torch.empty(q.shape, dtype=torch.float32, device=dev) if q_out is None else q_out
         qmv_kv_append(cache.c, batch.c, qp, qs, heads, kp, ks, vp, vs, fp, rot, int(halves),
-                      _on(q_out, torch.float32, "q_out", dev), s)
-    return q_out
+                      _on(out, torch.float32, "q_out", dev), s)
+        return out
+
+    return _on_device(dev, stream, call)
 
 
 def kv_read(cache: KVCache, batch: KVBatch, k=None, v=None, stream=None):
@@ -735,14 +762,15 @@ def kv_read(cache: KVCache, batch: KVBatch, k=None, v=None, stream=None):
     for t, what in ((k, "k"), (v, "v")):
         if t is not None and t.shape != shape:
             raise ValueError(f"{what} must be {shape}, got {tuple(t.shape)}")
-    with _On(dev, stream) as s:
-        if k is None:
-            k = torch.empty(shape, dtype=torch.float32, device=dev)
-        if v is None:
-            v = torch.empty(shape, dtype=torch.float32, device=dev)
-        qmv_kv_read(cache.c, batch.c, _on(k, torch.float32, "k", dev),
-                    _on(v, torch.float32, "v", dev), s)
-    return k, v
+
+    def call(s):
+        ko = torch.empty(shape, dtype=torch.float32, device=dev) if k is None else k
+        vo = torch.empty(shape, dtype=torch.float32, device=dev) if v is None else v
+        qmv_kv_read(cache.c, batch.c, _on(ko, torch.float32, "k", dev),
+                    _on(vo, torch.float32, "v", dev), s)
+        return ko, vo
+
+    return _on_device(dev, stream, call)
 
 
 def kv_attention(cache: KVCache, batch: KVBatch, q, scale: float, window: int = 0, out=None,
@@ -758,11 +786,12 @@ def kv_attention(cache: KVCache, batch: KVBatch, q, scale: float, window: int = 
     n = qmv_kv_attention_bytes(T, batch.B, heads, cache.kv_heads, cache.head_dim, batch.max_len)
     if work is not None and work.numel() < n:
         raise ValueError(f"work must hold {n} bytes, got {work.numel()}")
-    with _On(dev, stream) as s:
-        if out is None:
-            out = torch.empty(q.shape, dtype=torch.float32, device=dev)
-        if work is None:
-            work = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
+
+    def call(s):
+        o = torch.empty(q.shape, dtype=torch.float32, device=dev) if out is None else out
+        ws = torch.empty(max(n, 16), dtype=torch.uint8, device=dev) if work is None else work
         qmv_kv_attention(cache.c, batch.c, qp, qs, heads, scale, window,
-                         _on(out, torch.float32, "out", dev), _on(work, torch.uint8, "work", dev), s)
-    return out
+                         _on(o, torch.float32, "out", dev), _on(ws, torch.uint8, "work", dev), s)
+        return o
+
+    return _on_device(dev, stream, call)
