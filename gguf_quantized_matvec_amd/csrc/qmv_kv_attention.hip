@@ -41,6 +41,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "qmv_kv_device.h"
 #include "qmv_lanes.h"
 
@@ -160,7 +162,7 @@ __device__ __forceinline__ void wave_sync() {
 // of `per` segments; splits > 1: segment results go to work.
 struct Plan {
     int32_t tiles, splits, per, segs;
-    bool pack;
+    bool pack, wide;
 };
 
 // A segment's result of one row in the workspace: O [D], then (for all rows)
@@ -183,9 +185,162 @@ __device__ __forceinline__ Join join(float& R, float r) {
     R = n;
     return j;
 }
-__device__ __forceinline__ float joined(float o, float part, Join j) { return o * j.a + part * j.b; }
+__device__ __forceinline__ float joined(float o, float part, Join j) {
+    return __builtin_fmaf(o, j.a, part * j.b);
+}
 
 __device__ __forceinline__ float result(float o, float l) { return l == 0.0f ? 0.0f : o / l; }
+
+// The sequence b and its first row of row tile `tile` of ROWS rows; false if
+// there is none.
+template <int ROWS>
+__device__ __forceinline__ bool locate(const KvArgs& kv, int G, int tile, int lane, int& b, int& first) {
+    if (!kv.q_start) {
+        const int per = (G + ROWS - 1) / ROWS;
+        b = tile / per;
+        first = (tile - b * per) * ROWS;
+        return b < kv.B;
+    }
+    // sequence b owns the tiles from start[b] * G / ROWS + b on
+    int below = 0;
+    for (int b0 = 0; b0 < kv.B; b0 += 64) {
+        const int i = b0 + lane;
+        bool le = false;
+        if (i < kv.B) le = (int64_t)kv.q_start[i] * G / ROWS + i <= tile;
+        const unsigned long long m = __ballot(le);
+        below += __popcll(m);
+        if (m != ~0ull) break;
+    }
+    if (below == 0) return false;
+    b = uniform(below - 1);
+    const int64_t f = (tile - ((int64_t)kv.q_start[b] * G / ROWS + b)) * ROWS;
+    if (f < 0 || f > INT32_MAX) return false;
+    first = (int)f;
+    return true;
+}
+
+// Row rr of a sequence's rows as two f16 parts (lane group g holds elements
+// 32b + 8g ... + 7), scaled so that its largest element is just below 2^15; what
+// brings a product with it to base-2 scores (factor), and its position (-1 for
+// rows past the last).  meanwhile() runs between the loads and their use.
+template <int NB, class F>
+__device__ __forceinline__ void prepare_q(const AttnArgs& a, const Seq& s, int head, int G, int rr,
+                                          int rows, int g, half8 (&qh)[NB], half8 (&ql)[NB],
+                                          float& factor, int& pos, F&& meanwhile) {
+    constexpr int D = 32 * NB;
+    const bool valid = rr < rows;
+    const int j = valid ? rr / G : 0, hg = valid ? rr - j * G : 0;
+    pos = valid ? s.len - s.n + j : -1;
+    const float* qp = a.q + (int64_t)(s.q0 + j) * a.q_stride + (int64_t)(head * G + hg) * D + 8 * g;
+    const float to_log2 = a.scale * 1.44269504f;
+    float x[NB][8];
+    float big = 0.0f;
+#pragma unroll
+    for (int bb = 0; bb < NB; bb++) {
+        float4 u = make_float4(0, 0, 0, 0), v = u;
+        if (valid) {
+            u = *reinterpret_cast<const float4*>(qp + 32 * bb);
+            v = *reinterpret_cast<const float4*>(qp + 32 * bb + 4);
+        }
+        const float t[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 8; e++) x[bb][e] = t[e] * to_log2;
+    }
+    meanwhile();
+#pragma unroll
+    for (int bb = 0; bb < NB; bb++)
+#pragma unroll
+        for (int e = 0; e < 8; e++) big = fmaxf(big, fabsf(x[bb][e]));
+    big = max_rows(big);
+    int ex = (int)((__float_as_uint(big) >> 23) & 255) - 126;  // big < 2^ex
+    ex = ex < -100 ? -100 : ex;
+    const float up = ldexpf(1.0f, 15 - ex);
+    factor = ldexpf(1.0f, ex - 15);
+#pragma unroll
+    for (int bb = 0; bb < NB; bb++) {
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            const float y = x[bb][e] * up;
+            qh[bb][e] = (_Float16)y;
+            ql[bb][e] = (_Float16)(y - (float)qh[bb][e]);
+        }
+    }
+}
+
+// Block scales of two positions (2 lane and 2 lane + 1 of a run) into LDS, by
+// block; `live` of them lie before the sequence's end, the others get 0.
+template <int NB>
+__device__ __forceinline__ void keep_live(Words<NB>& d, int live) {
+#pragma unroll
+    for (int i = 0; i < NB; i++) {
+        uint32_t keep = 0;
+        if (live > (2 * i) / NB) keep |= 0xFFFFu;
+        if (live > (2 * i + 1) / NB) keep |= 0xFFFF0000u;
+        d.w[i] &= keep;
+    }
+}
+template <int NB>
+__device__ __forceinline__ void stage_key_scales(Words<NB> dk, int live, int lane,
+                                                 uint32_t (*to)[sub_of(NB) / 2]) {
+    keep_live<NB>(dk, live);
+#pragma unroll
+    for (int i = 0; i < NB; i++)
+        to[i][lane] = half_bits(dk.w[i >> 1], i & 1) | half_bits(dk.w[(NB + i) >> 1], (NB + i) & 1) << 16;
+}
+// The exponent that bounds the largest scale of a position's values, max_b |dv|
+// < 2^ev.  A position with an infinite or NaN scale gets ev = inf, which turns
+// the reference of a row that sees it infinite and its result NaN, and scales of
+// 0, so that the rows that do not see it have no 0 * NaN.
+struct Sizes {
+    int e[2];
+    bool bad[2];
+};
+template <int NB>
+__device__ __forceinline__ Sizes sizes_of(const Words<NB>& dv) {
+    uint32_t top[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 2 * NB; i++) {
+        const uint32_t m = half_bits(dv.w[i >> 1], i & 1) & 0x7FFFu;
+        top[i / NB] = m > top[i / NB] ? m : top[i / NB];
+    }
+    Sizes z;
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        z.e[i] = (int)(top[i] >> 10) - 14;
+        z.bad[i] = top[i] >= 0x7C00u;
+    }
+    return z;
+}
+template <int NB>
+__device__ __forceinline__ void stage_value_sizes(Words<NB> dv, int live, int lane, float* ev) {
+    keep_live<NB>(dv, live);
+    const Sizes z = sizes_of<NB>(dv);
+#pragma unroll
+    for (int i = 0; i < 2; i++) ev[2 * lane + i] = z.bad[i] ? INFINITY : (float)z.e[i];
+}
+// The values' scales as dv 2^-ev, below 1, and 2^-ev.
+template <int NB>
+__device__ __forceinline__ void stage_value_scales(Words<NB> dv, int live, int lane,
+                                                   uint32_t (*to)[sub_of(NB) / 2], float* down) {
+    keep_live<NB>(dv, live);
+    const Sizes z = sizes_of<NB>(dv);
+    float f[2];
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        f[i] = z.bad[i] ? 0.0f : __uint_as_float((uint32_t)(127 - z.e[i]) << 23);
+        down[2 * lane + i] = f[i];
+    }
+#pragma unroll
+    for (int i = 0; i < NB; i++) {
+        half2v v = {half_of(dv.w[i >> 1], i & 1), half_of(dv.w[(NB + i) >> 1], (NB + i) & 1)};
+        v[0] = z.bad[0] ? (_Float16)0.0f : (_Float16)((float)v[0] * f[0]);
+        v[1] = z.bad[1] ? (_Float16)0.0f : (_Float16)((float)v[1] * f[1]);
+        // the lanes of positions 0, 1 and 2, 3 exchange to words of positions 0, 2 and 1, 3, the
+        // order of the code words
+        const uint32_t own = word(v), other = dpp_bits<DPP_XOR1>(own);
+        to[i][lane] = lane & 1 ? (other >> 16) | (own & 0xFFFF0000u) : (own & 0xFFFFu) | (other << 16);
+    }
+}
 
 // PACK: at most 8 rows share a key/value head in the tile.  The 16 columns of
 // a product then hold them twice, and each half of the columns keeps its own
@@ -217,30 +372,8 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
     const int split = at % plan.splits;
     const int tile = plan.tiles - 1 - at / plan.splits;  // long rows first
 
-    // the tile's sequence and rows
     int b, first;
-    if (!kv.q_start) {
-        const int per = (G + ROWS - 1) / ROWS;
-        b = tile / per;
-        first = (tile - b * per) * ROWS;
-        if (b >= kv.B) return;
-    } else {
-        // sequence b owns the tiles from start[b] * G / ROWS + b on
-        int below = 0;
-        for (int b0 = 0; b0 < kv.B; b0 += 64) {
-            const int i = b0 + lane;
-            bool le = false;
-            if (i < kv.B) le = (int64_t)kv.q_start[i] * G / ROWS + i <= tile;
-            const unsigned long long m = __ballot(le);
-            below += __popcll(m);
-            if (m != ~0ull) break;
-        }
-        if (below == 0) return;
-        b = uniform(below - 1);
-        const int64_t f = (tile - ((int64_t)kv.q_start[b] * G / ROWS + b)) * ROWS;
-        if (f < 0 || f > INT32_MAX) return;
-        first = (int)f;
-    }
+    if (!locate<ROWS>(kv, G, tile, lane, b, first)) return;
     const Seq s = seq_of(kv, b);
     const int64_t rows64 = (int64_t)s.n * G;
     if (first >= rows64) return;
@@ -303,56 +436,17 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
     };
     fetch_pages(seg0);
 
-    // q as two f16 parts: lane (n, g) holds elements 32b + 8g ... + 7 of row n
     half8 qh[NB], ql[NB];
     float factor;
     int pos;
-    {
-        const int rr = first + n;
-        const bool valid = rr < rows;
-        const int j = valid ? rr / G : 0, hg = valid ? rr - j * G : 0;
-        pos = valid ? s.len - s.n + j : -1;
-        const float* qp = a.q + (int64_t)(s.q0 + j) * a.q_stride + (int64_t)(head * G + hg) * D + 8 * g;
-        const float to_log2 = a.scale * 1.44269504f;
-        float x[NB][8];
-        float big = 0.0f;
-#pragma unroll
-        for (int bb = 0; bb < NB; bb++) {
-            float4 u = make_float4(0, 0, 0, 0), v = u;
-            if (valid) {
-                u = *reinterpret_cast<const float4*>(qp + 32 * bb);
-                v = *reinterpret_cast<const float4*>(qp + 32 * bb + 4);
-            }
-            const float t[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < 8; e++) x[bb][e] = t[e] * to_log2;
-        }
+    prepare_q<NB>(a, s, head, G, first + n, rows, g, qh, ql, factor, pos, [&] {
         if (works(seg0)) {
             fetch_scales(seg0);
 #pragma unroll
             for (int u = 0; u < TILES; u++) fetch_keys(u);
         }
         fetch_pages(seg0 + 1);
-#pragma unroll
-        for (int bb = 0; bb < NB; bb++)
-#pragma unroll
-            for (int e = 0; e < 8; e++) big = fmaxf(big, fabsf(x[bb][e]));
-        big = max_rows(big);
-        int ex = (int)((__float_as_uint(big) >> 23) & 255) - 126;  // big < 2^ex
-        ex = ex < -100 ? -100 : ex;
-        const float up = ldexpf(1.0f, 15 - ex);
-        factor = ldexpf(1.0f, ex - 15);
-#pragma unroll
-        for (int bb = 0; bb < NB; bb++) {
-#pragma unroll
-            for (int e = 0; e < 8; e++) {
-                const float y = x[bb][e] * up;
-                const _Float16 h = (_Float16)y, l = (_Float16)(y - (float)h);
-                qh[bb][e] = h;
-                ql[bb][e] = l;
-            }
-        }
-    }
+    });
 
     // the joined state: thread (row tid / PER_ROW, part tid % PER_ROW) holds its share of every
     // NBP blocks
@@ -375,48 +469,10 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
             const bool more = works(seg + 1);
             if (TILES == 8 || lane < 8 * TILES) {
                 const int u = lane >> 3, t = t0 + 16 * u + 2 * (lane & 7);
-                const int live = ((here >> u) & 1) ? s.len - t : 0;  // positions behind the last: scale 0
-                uint32_t top[2] = {0, 0};
-#pragma unroll
-                for (int i = 0; i < NB; i++) {
-                    uint32_t keep = 0;
-                    if (live > (2 * i) / NB) keep |= 0xFFFFu;
-                    if (live > (2 * i + 1) / NB) keep |= 0xFFFF0000u;
-                    dk.w[i] &= keep;
-                    dv.w[i] &= keep;
-#pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        const uint32_t m = (h ? dv.w[i] >> 16 : dv.w[i]) & 0x7FFFu;
-                        const int tok = (2 * i + h) / NB;
-                        top[tok] = m > top[tok] ? m : top[tok];
-                    }
-                }
-                // max_b |dv| < 2^ev; a position with an infinite or NaN scale gets ev = inf, which
-                // turns the reference of a row that sees it infinite and its result NaN, and
-                // scales of 0, so that the rows that do not see it have no 0 * NaN
-                const bool bad[2] = {top[0] >= 0x7C00u, top[1] >= 0x7C00u};
-                float down[2];
-#pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    const int e = (int)(top[i] >> 10) - 14;
-                    s_ev[wave][2 * lane + i] = bad[i] ? INFINITY : (float)e;
-                    // 2^-e
-                    down[i] = bad[i] ? 0.0f : __uint_as_float((uint32_t)(127 - e) << 23);
-                    s_down[wave][2 * lane + i] = down[i];
-                }
-#pragma unroll
-                for (int i = 0; i < NB; i++) {  // block i of both positions
-                    s_dk[wave][i][lane] = half_bits(dk.w[i >> 1], i & 1) |
-                                          half_bits(dk.w[(NB + i) >> 1], (NB + i) & 1) << 16;
-                    // dv 2^-ev, below 1; the lanes of positions 0, 1 and 2, 3 exchange to words of
-                    // positions 0, 2 and 1, 3, the order of the code words
-                    half2v v = {half_of(dv.w[i >> 1], i & 1), half_of(dv.w[(NB + i) >> 1], (NB + i) & 1)};
-                    v[0] = bad[0] ? (_Float16)0.0f : (_Float16)((float)v[0] * down[0]);
-                    v[1] = bad[1] ? (_Float16)0.0f : (_Float16)((float)v[1] * down[1]);
-                    const uint32_t own = word(v), other = dpp_bits<DPP_XOR1>(own);
-                    s_dv[wave][i][lane] = lane & 1 ? (other >> 16) | (own & 0xFFFF0000u)
-                                                   : (own & 0xFFFFu) | (other << 16);
-                }
+                const int live = ((here >> u) & 1) ? s.len - t : 0;
+                stage_key_scales<NB>(dk, live, lane, s_dk[wave]);
+                stage_value_sizes<NB>(dv, live, lane, s_ev[wave]);
+                stage_value_scales<NB>(dv, live, lane, s_dv[wave], s_down[wave]);
             }
             wave_sync();
 
@@ -613,8 +669,9 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
             s_r[wave][n] = r;
             s_l[wave][n] = l;
         }
-        float f[WAVES], sr = NO_KEY, sl = 0.0f;
-        Join jn{1.0f, 0.0f};
+        bool has[WAVES];
+        float sr = NO_KEY, sl = 0.0f;
+        Join jw[WAVES], jn{1.0f, 0.0f};
 #pragma unroll
         for (int b0 = 0; b0 < NB; b0 += NBP) {
             const int nbp = NB - b0 < NBP ? NB - b0 : NBP;
@@ -631,14 +688,12 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
             if (b0 == 0) {
 #pragma unroll
                 for (int w = 0; w < WAVES; w++) {
-                    f[w] = s_r[w][jr];
-                    sr = fmaxf(sr, f[w]);
-                }
-#pragma unroll
-                for (int w = 0; w < WAVES; w++) {
-                    const bool has = f[w] != NO_KEY;
-                    f[w] = has ? exp2_raw(f[w] - sr) : -1.0f;  // -1: nothing there
-                    if (has) sl = __builtin_fmaf(f[w], s_l[w][jr], sl);
+                    const float rw = s_r[w][jr];
+                    has[w] = rw != NO_KEY;
+                    if (has[w]) {
+                        jw[w] = join(sr, rw);
+                        sl = joined(sl, s_l[w][jr], jw[w]);
+                    }
                 }
                 if (plan.splits == 1) {
                     jn = join(RR, sr);
@@ -651,10 +706,9 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
             for (int i = 0; i < per; i++) v[i] = 0.0f;
 #pragma unroll
             for (int w = 0; w < WAVES; w++)
-                if (f[w] >= 0.0f || f[w] != f[w]) {
+                if (has[w]) {
 #pragma unroll
-                    for (int i = 0; i < per; i++)
-                        v[i] = __builtin_fmaf(f[w], s_o[w][jr * LD + jp * per + i], v[i]);
+                    for (int i = 0; i < per; i++) v[i] = joined(v[i], s_o[w][jr * LD + jp * per + i], jw[w]);
                 }
             if (plan.splits == 1) {
 #pragma unroll
@@ -687,6 +741,265 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
         for (int i = 0; i < per; i++) out[32 * b0 + jp * per + i] = result(O[o0 + i], L);
     }
 }
+
+// Many rows: 64 of them a workgroup, 16 a wave, over the same positions.  The
+// waves unpack a run of SUB positions together, a quarter each, into LDS in
+// operand order, and each takes all of it from there: 144 instructions of
+// unpacking a wave and run instead of 576, against 64 LDS reads.  Keys (and what the
+// scores need) are replaced while values are worked on, and values while scores
+// are, from words loaded a run ahead; two barriers a run.  Every wave joins its
+// runs to segments and its segments to its state itself, in the steps of k_attn.
+template <int NB>
+__global__ __launch_bounds__(64 * WAVES, 2) void k_attn_wide(AttnArgs a, Plan plan) {
+    static_assert(sub_of(NB) == 128 && WAVES == 4, "a wave unpacks two tiles of keys and a pair of values");
+    const KvArgs& kv = a.kv;
+    constexpr int D = 32 * NB, SUB = 128, TILES = 8, ROWS = 64;
+    extern __shared__ __align__(16) uint8_t lds[];
+    uint4 (*s_k)[64] = reinterpret_cast<uint4 (*)[64]>(lds);                 // [TILES * NB][lane]
+    uint4 (*s_v)[64] = s_k + TILES * NB;                                     // [pair * NB * 2][lane]
+    uint32_t (*s_dk)[SUB / 2] = reinterpret_cast<uint32_t (*)[SUB / 2]>(s_v + TILES * NB);
+    uint32_t (*s_dv)[SUB / 2] = s_dk + NB;
+    float* s_ev = reinterpret_cast<float*>(s_dv + NB);
+    float* s_down = s_ev + SUB;
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int n = lane & 15, g = lane >> 4;
+    const int G = a.Hq / kv.Hkv;
+    const int head = blockIdx.x % kv.Hkv;
+    const int tile = plan.tiles - 1 - blockIdx.x / kv.Hkv;  // long rows first
+    int b, first;
+    if (!locate<ROWS>(kv, G, tile, lane, b, first)) return;
+    const Seq s = seq_of(kv, b);
+    const int64_t rows64 = (int64_t)s.n * G;
+    if (first >= rows64) return;
+    const int rows = (int)rows64;
+    // positions that the workgroup's rows see, and this wave's
+    const auto pos_of = [&](int rr) { return s.len - s.n + (rr < rows ? rr : rows - 1) / G; };
+    const auto begin_of = [&](int p) { return a.window && p + 1 > a.window ? p + 1 - a.window : 0; };
+    const int t_end = pos_of(first + ROWS - 1) + 1, t_begin = begin_of(pos_of(first));
+    const int row0 = first + 16 * wave;
+    const bool mine = row0 < rows;
+    const int pos_lo = pos_of(row0), pos_hi = pos_of(row0 + 15);
+    const int w_end = mine ? pos_hi + 1 : 0, w_begin = begin_of(pos_lo);
+    const int sub0 = t_begin / SUB, sub1 = t_end > 0 ? (t_end + SUB - 1) / SUB : 0;
+
+    const int page_tokens = 1 << kv.log2p;
+    const int64_t codes = (int64_t)(16 * NB) << kv.log2p;
+    const int32_t* table = kv.table + (int64_t)b * kv.table_stride;
+    const Unpack unpack;
+    int pg = -1;
+    uint32_t there = 0;
+    Words<NB> kw[2], vw[2], dd;
+    const auto tile_of = [](int q) { return 4 * (q & 1) + (q >> 1); };  // of a pair: this and two on
+    const auto fetch_pages = [&](int sub) {
+        const int t = sub * SUB + 16 * lane;
+        pg = -1;
+        if (sub < sub1 && lane < TILES && t < s.len) pg = table[t >> kv.log2p];
+    };
+    // the wave's share: tiles 2w, 2w + 1 of keys, pair w of values, wave 0 the keys' and wave 1 the
+    // values' scales; returns which tiles have a page
+    const auto fetch = [&](int sub) {
+        const int t0 = sub * SUB;
+        const bool ok = pg >= 0 && (int64_t)pg < kv.n_pages;
+        const uint32_t have = (uint32_t)__ballot(ok);
+        const int p = ok ? pg : 0;  // tiles without a page read page 0, which is not used
+        const int64_t at = ((int64_t)p * kv.Hkv + head) * kv.head_bytes +
+                           (int64_t)((t0 + 16 * lane) & (page_tokens - 1)) * (16 * NB);
+        const uint32_t lo = (uint32_t)at, hi = (uint32_t)(at >> 32);
+        const auto tile_codes = [&](int u) {
+            return kv.pages + ((uint32_t)__builtin_amdgcn_readlane(lo, u) |
+                               (uint64_t)(uint32_t)__builtin_amdgcn_readlane(hi, u) << 32);
+        };
+        const int vu = tile_of(wave);
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            kw[i] = load_words<NB>(tile_codes(2 * wave + i) + n * (16 * NB) + g * (4 * NB));
+            vw[i] = load_words<NB>(tile_codes(vu + 2 * i) + codes + lane * (4 * NB));
+        }
+        if (wave < 2) {
+            const int u = lane >> 3, t = t0 + 16 * u + 2 * (lane & 7);
+            dd = load_words<NB>(head_of(kv, __shfl(p, u), head) + 2 * codes +
+                                ((int64_t)(wave ? 2 * NB : 0) << kv.log2p) +
+                                (int64_t)(t & (page_tokens - 1)) * 2 * NB);
+        }
+        return have;
+    };
+    const auto live_of = [&](int sub, uint32_t have) {
+        const int u = lane >> 3, t = sub * SUB + 16 * u + 2 * (lane & 7);
+        return ((have >> u) & 1) ? s.len - t : 0;
+    };
+    const auto stage_keys = [&](int sub, uint32_t have) {
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+#pragma unroll
+            for (int bb = 0; bb < NB; bb++) {
+                const uint32_t w = kw[i].w[bb], v = w >> 8;
+                s_k[(2 * wave + i) * NB + bb][lane] =
+                    make_uint4(unpack.low(w), unpack.high(w), unpack.low(v), unpack.high(v));
+            }
+        if (wave == 0) stage_key_scales<NB>(dd, live_of(sub, have), lane, s_dk);
+        if (wave == 1) stage_value_sizes<NB>(dd, live_of(sub, have), lane, s_ev);
+    };
+    const auto stage_values = [&](int sub, uint32_t have) {
+#pragma unroll
+        for (int bb = 0; bb < NB; bb++) {
+            const uint32_t w0 = vw[0].w[bb], w1 = vw[1].w[bb], v0 = w0 >> 8, v1 = w1 >> 8;
+            uint4 (*to)[64] = s_v + (wave * NB + bb) * 2;
+            to[0][lane] = make_uint4(unpack.low(w0), unpack.low(v0), unpack.low(w1), unpack.low(v1));
+            to[1][lane] = make_uint4(unpack.high(w0), unpack.high(v0), unpack.high(w1), unpack.high(v1));
+        }
+        if (wave == 1) stage_value_scales<NB>(dd, live_of(sub, have), lane, s_dv, s_down);
+    };
+    const auto at_lds = [](const uint4& v) {
+        half8 h;
+        __builtin_memcpy(&h, &v, 16);
+        return h;
+    };
+
+    fetch_pages(sub0);
+    half8 qh[NB], ql[NB];
+    float factor;
+    int pos;
+    prepare_q<NB>(a, s, head, G, row0 + n, rows, g, qh, ql, factor, pos, [&] {
+        if (sub0 < sub1) there = fetch(sub0);
+        fetch_pages(sub0 + 1);
+    });
+    if (sub0 < sub1) {
+        stage_keys(sub0, there);
+        stage_values(sub0, there);
+    }
+    __syncthreads();
+
+    // the state over whole segments, and the segment's; row n of the wave, elements 32b + 8g + 2i
+    // (first of a pair of f4) and + 1
+    f4 O[2 * NB], os[2 * NB];
+    float R = NO_KEY, L = 0.0f, rs = NO_KEY, ls = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2 * NB; i++) O[i] = os[i] = f4{0, 0, 0, 0};
+
+    for (int sub = sub0; sub < sub1; sub++) {
+        const int t0 = sub * SUB;
+        const bool work = t0 < w_end && t0 + SUB > w_begin;
+        const bool masked = t0 + SUB > pos_lo + 1 || (a.window && t0 <= pos_hi - a.window) || there != 0xFF;
+        const uint32_t here = there;
+        const bool more = sub + 1 < sub1;
+        if (more) there = fetch(sub + 1);
+        fetch_pages(sub + 2);
+        f4 sc[TILES];
+        if (work) {
+#pragma unroll
+            for (int u = 0; u < TILES; u++) {
+                f4 z = {0, 0, 0, 0};
+#pragma unroll
+                for (int bb = 0; bb < NB; bb++) {
+                    const Words<2> d = *reinterpret_cast<const Words<2>*>(&s_dk[bb][8 * u + 2 * g]);
+                    const half8 ko = at_lds(s_k[u * NB + bb][lane]);
+                    f4 acc = mfma(ko, ql[bb], f4{0, 0, 0, 0});
+                    acc = mfma(ko, qh[bb], acc);
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        z[i] = __builtin_fmaf((float)half_of(d.w[i >> 1], i & 1), acc[i], z[i]);
+                }
+                const f4 e = *reinterpret_cast<const f4*>(&s_ev[16 * u + 4 * g]);
+#pragma unroll
+                for (int i = 0; i < 4; i++) sc[u][i] = __builtin_fmaf(z[i], factor, e[i]);
+            }
+        }
+        __syncthreads();  // every wave is done with the keys
+        if (more) stage_keys(sub + 1, there);
+        if (work) {
+            if (masked) {
+                const int rel = pos - t0 - 4 * g;
+                const int from = a.window ? rel - a.window : -(1 << 30);
+#pragma unroll
+                for (int u = 0; u < TILES; u++) {
+                    const int hi = (here >> u) & 1 ? rel : -(1 << 30);
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        sc[u][i] = 16 * u + i <= hi && 16 * u + i > from ? sc[u][i] : -INFINITY;
+                }
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < TILES; u++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) top = fmaxf(top, sc[u][i]);
+            top = max_rows(top);
+            const float ref = top > -INFINITY ? top - 14.0f : 0.0f;
+            float sum[2] = {0.0f, 0.0f};  // over the even and the odd tiles
+            Split p[TILES][2];            // positions 0, 2 and 1, 3
+#pragma unroll
+            for (int u = 0; u < TILES; u++) {
+                const f4 down = *reinterpret_cast<const f4*>(&s_down[16 * u + 4 * g]);
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    sc[u][i] = exp2_raw(sc[u][i] - ref);
+                    sum[u & 1] = __builtin_fmaf(sc[u][i], down[i], sum[u & 1]);
+                }
+                p[u][0] = two_parts(sc[u][0], sc[u][2]);
+                p[u][1] = two_parts(sc[u][1], sc[u][3]);
+            }
+            const float l = sum_rows(sum[0] + sum[1]);
+            const float r = top == -INFINITY && l == 0.0f ? NO_KEY : ref;
+            const Join js = join(rs, r);
+            ls = joined(ls, l, js);
+#pragma unroll
+            for (int bb = 0; bb < NB; bb++) {
+                f4 o0 = {0, 0, 0, 0}, o1 = o0;
+#pragma unroll
+                for (int q = 0; q < TILES / 2; q++) {
+                    const int u = tile_of(q);
+                    const Words<2> d0 = *reinterpret_cast<const Words<2>*>(&s_dv[bb][8 * u + 2 * g]);
+                    const Words<2> d1 = *reinterpret_cast<const Words<2>*>(&s_dv[bb][8 * u + 16 + 2 * g]);
+                    const Split a0 = times(p[u][0], halves(d0.w[0])), a1 = times(p[u][1], halves(d0.w[1]));
+                    const Split a2 = times(p[u + 2][0], halves(d1.w[0]));
+                    const Split a3 = times(p[u + 2][1], halves(d1.w[1]));
+                    const half8 ph = operand(word(a0.h), word(a1.h), word(a2.h), word(a3.h));
+                    const half8 pl = operand(word(a0.l), word(a1.l), word(a2.l), word(a3.l));
+                    const half8 even = at_lds(s_v[(q * NB + bb) * 2][lane]);
+                    const half8 odd = at_lds(s_v[(q * NB + bb) * 2 + 1][lane]);
+                    o0 = mfma(even, pl, o0);
+                    o1 = mfma(odd, pl, o1);
+                    o0 = mfma(even, ph, o0);
+                    o1 = mfma(odd, ph, o1);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    os[2 * bb][i] = joined(os[2 * bb][i], o0[i], js);
+                    os[2 * bb + 1][i] = joined(os[2 * bb + 1][i], o1[i], js);
+                }
+            }
+        }
+        __syncthreads();  // every wave is done with the values
+        if (more) stage_values(sub + 1, there);
+        if ((sub & (WAVES - 1)) == WAVES - 1 || !more) {  // the segment is complete
+            const Join jn = join(R, rs);
+            L = joined(L, ls, jn);
+#pragma unroll
+            for (int i = 0; i < 2 * NB; i++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    O[i][e] = joined(O[i][e], os[i][e], jn);
+                    os[i][e] = 0.0f;
+                }
+            rs = NO_KEY;
+            ls = 0.0f;
+        }
+    }
+    const int rr = row0 + n;
+    if (rr >= rows) return;
+    float* out = a.out + ((int64_t)(s.q0 + rr / G) * a.Hq + head * G + rr % G) * D + 8 * g;
+#pragma unroll
+    for (int bb = 0; bb < NB; bb++) {
+        const f4 x = O[2 * bb], y = O[2 * bb + 1];
+        *reinterpret_cast<f4*>(out + 32 * bb) =
+            f4{result(x[0], L), result(y[0], L), result(x[1], L), result(y[1], L)};
+        *reinterpret_cast<f4*>(out + 32 * bb + 4) =
+            f4{result(x[2], L), result(y[2], L), result(x[3], L), result(y[3], L)};
+    }
+}
+
+template <int NB> constexpr int wide_lds() { return 2 * 8 * NB * 1024 + 2 * NB * 256 + 2 * 512; }
 
 // Joins the segments of a row in ascending order, as k_attn does when it has
 // them all: one workgroup per row, query head and W elements (all, or 32 where
@@ -775,7 +1088,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, int segs) {
                 const f4 k = *reinterpret_cast<const f4*>(&s_a[i]);
                 const f4 x = *reinterpret_cast<const f4*>(&s_x[tid * LD + i]);
 #pragma unroll
-                for (int e = 0; e < 4; e++) O = O * k[e] + x[e];
+                for (int e = 0; e < 4; e++) O = __builtin_fmaf(O, k[e], x[e]);
             }
         }
         __syncthreads();
@@ -785,18 +1098,16 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, int segs) {
     if (tid < W) a.out[row * D + W * blockIdx.y + tid] = result(O, s_b[0]);
 }
 
-// Packed tiles of 8 rows where the sequences of a call have that few per
-// key/value head on average: beyond, tiles of 16 rows do more per product.
-bool packs(bool one, int64_t T, int64_t B, int64_t G, int nb) {
-    return nb <= 4 && (one ? G <= 8 : T * G <= 8 * B);
-}
-
 // one: a row each (no starts).
 Plan plan_of(bool one, int64_t T, int64_t B, int Hq, int Hkv, int nb, int64_t max_len) {
     const int64_t G = Hq / Hkv;
     Plan p;
-    p.pack = packs(one, T, B, G, nb);
-    const int64_t tr = p.pack ? 8 : 16;
+    // Packed tiles of 8 rows where the sequences of a call have that few per key/value head on
+    // average; 64 rows a workgroup where that many fill them and the chip (a 2048-token prompt with
+    // a window of 1024, 32 heads on 8: WIDE us, 182 in tiles of 16); else tiles of 16.
+    p.pack = nb <= 4 && (one ? G <= 8 : T * G <= 8 * B);
+    p.wide = nb <= 4 && !one && T * G >= 64 * B && (T * G / 64 + B) * Hkv >= 512;
+    const int64_t tr = p.wide ? 64 : p.pack ? 8 : 16;
     p.tiles = (int32_t)(one ? B * ((G + tr - 1) / tr) : T * G / tr + B);
     p.segs = (int32_t)((max_len + seg_of(nb) - 1) / seg_of(nb));
     // One sequence: as many workgroups as run at once (two per CU), each with several segments,
@@ -811,16 +1122,39 @@ Plan plan_of(bool one, int64_t T, int64_t B, int Hq, int Hkv, int nb, int64_t ma
     return p;
 }
 
+// Raise a kernel's dynamic-LDS limit, once per kernel and device.  Concurrent
+// first calls may both set the attribute, which changes nothing; a failure is
+// returned and tried again on the next call.
+int raise_lds_limit(const void* kernel, std::atomic<int> (&state)[64]) {
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess) return (int)hipErrorInvalidDevice;
+    std::atomic<int>* st = dev >= 0 && dev < 64 ? &state[dev] : nullptr;
+    if (st && st->load(std::memory_order_acquire) == 1) return 0;
+    const hipError_t rc =
+        hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+    if (rc != hipSuccess) return (int)rc;
+    if (st) st->store(1, std::memory_order_release);
+    return 0;
+}
+
 template <int NB>
-void launch_nb(const AttnArgs& a, const Plan& p, hipStream_t s) {
-    const dim3 grid((unsigned)((int64_t)p.tiles * p.splits * a.kv.Hkv));
+int launch_nb(const AttnArgs& a, const Plan& p, hipStream_t s) {
+    const dim3 grid((unsigned)((int64_t)p.tiles * p.splits * a.kv.Hkv)), block(64 * WAVES);
     if constexpr (NB <= 4) {
+        if (p.wide) {
+            static std::atomic<int> lds_state[64];
+            const int rc = raise_lds_limit(reinterpret_cast<const void*>(&k_attn_wide<NB>), lds_state);
+            if (rc) return rc;
+            hipLaunchKernelGGL((k_attn_wide<NB>), grid, block, wide_lds<NB>(), s, a, p);
+            return (int)hipGetLastError();
+        }
         if (p.pack) {
-            hipLaunchKernelGGL((k_attn<NB, true>), grid, dim3(64 * WAVES), 0, s, a, p);
-            return;
+            hipLaunchKernelGGL((k_attn<NB, true>), grid, block, 0, s, a, p);
+            return (int)hipGetLastError();
         }
     }
-    hipLaunchKernelGGL((k_attn<NB, false>), grid, dim3(64 * WAVES), 0, s, a, p);
+    hipLaunchKernelGGL((k_attn<NB, false>), grid, block, 0, s, a, p);
+    return (int)hipGetLastError();
 }
 
 }  // namespace
@@ -834,17 +1168,17 @@ int64_t kv_attention_bytes(int64_t T, int64_t B, int Hq, int Hkv, int nb, int64_
 
 int launch_kv_attention(const AttnArgs& a, hipStream_t s) {
     const Plan p = plan_of(!a.kv.q_start, a.kv.T, a.kv.B, a.Hq, a.kv.Hkv, a.kv.nb, a.kv.max_len);
+    int rc;
     switch (a.kv.nb) {
-    case 1: launch_nb<1>(a, p, s); break;
-    case 2: launch_nb<2>(a, p, s); break;
-    case 3: launch_nb<3>(a, p, s); break;
-    case 4: launch_nb<4>(a, p, s); break;
-    case 5: launch_nb<5>(a, p, s); break;
-    case 6: launch_nb<6>(a, p, s); break;
-    case 7: launch_nb<7>(a, p, s); break;
-    default: launch_nb<8>(a, p, s); break;
+    case 1: rc = launch_nb<1>(a, p, s); break;
+    case 2: rc = launch_nb<2>(a, p, s); break;
+    case 3: rc = launch_nb<3>(a, p, s); break;
+    case 4: rc = launch_nb<4>(a, p, s); break;
+    case 5: rc = launch_nb<5>(a, p, s); break;
+    case 6: rc = launch_nb<6>(a, p, s); break;
+    case 7: rc = launch_nb<7>(a, p, s); break;
+    default: rc = launch_nb<8>(a, p, s); break;
     }
-    int rc = (int)hipGetLastError();
     if (rc || p.splits == 1) return rc;
     const int64_t joins = (int64_t)a.kv.T * a.Hq;
     const bool narrow = p.segs >= 64 && joins < 256;

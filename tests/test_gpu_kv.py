@@ -480,3 +480,56 @@ def test_a_row_does_not_depend_on_its_call(g, d, hq, hkv, window):
     assert torch.equal(many.view(20, n, -1), whole[:n].expand(20, n, -1))
     assert torch.equal(call(q[n:n + 50], [1], [50], [50]), whole[n:n + 50])
     assert torch.equal(call(q[n + 50:], [2], [333]), whole[n + 50:])
+
+
+@pytest.mark.parametrize("d,hq,hkv,window", [(32, 64, 64, 0), (64, 64, 32, 0), (96, 64, 32, 200), (128, 64, 32, 0),
+                                             (128, 120, 24, 333)])
+def test_many_rows(g, d, hq, hkv, window):
+    """Prompts long enough for 64 rows a workgroup, ragged, with a hole in the table and a NaN token:
+    sampled rows against the definition, and every row bit for bit as in a call of few rows."""
+    page = 32
+    c = Case([700, 129, 128, 40], [450, 128, 0, 5], page, hkv, d, 18, spare_rows=3)
+    raw, ks, vs = filled(c, hq)
+    c.table[0, 5] = -1  # positions 160..191
+    seen = [np.ones(n, bool) for n in c.lens]
+    seen[0][160:192] = False
+    q = (1.5 * c.rng.standard_normal((c.T, hq * d))).astype(np.float32)
+    cache, scale = g.KVCache(dev(raw), page, hkv, d), float(np.float32(d ** -0.5))
+    out = torch.full((c.T, hq * d), 7.0, device="cuda")
+    g.kv_attention(cache, c.batch(g), dev(q), scale, window=window, out=out)
+    assert torch.all(out[c.rows:] == 7.0)
+    got, G = out.cpu().numpy(), hq // hkv
+    for i in c.rng.choice(c.rows, 24, replace=False):
+        b, heads = int(c.seq[i]), np.sort(c.rng.choice(hq, 3, replace=False))
+        kv = heads // G
+        want, *sizes = attention(q[i].reshape(1, hq, d)[:, heads], ks[b][:, kv], vs[b][:, kv], c.pos[i:i + 1],
+                                 scale, window, seen[b])
+        x = got[i].reshape(1, hq, d)[:, heads]
+        assert np.all(np.abs(x - want) <= bound(d, c.lens[b], *sizes)), i
+    table = dev(c.table)
+
+    def few(lo, hi, b, length):
+        batch = g.KVBatch(table[b:b + 1].contiguous(), dev(np.array([length], np.int32)),
+                          dev(np.array([0, hi - lo], np.int32)), hi - lo, length)
+        return g.kv_attention(cache, batch, dev(q[lo:hi]), scale, window=window)
+
+    for lo, hi in [(0, 1), (1, 8), (8, 40), (40, 99), (200, 231), (440, 450)]:
+        assert torch.equal(few(lo, hi, 0, 700 - 450 + hi), out[lo:hi]), (lo, hi)
+    assert torch.equal(few(450, 500, 1, 51), out[450:500])
+    assert torch.equal(few(578, 583, 3, 40), out[578:583])
+
+
+def test_many_rows_see_nan_where_it_is(g):
+    """A NaN token in the middle of a long prompt: the rows before it and, with a window, those far
+    behind it are as without it."""
+    d, h, page, n = 64, 64, 64, 600
+    c = Case([n], [n], page, h, d, 19)
+    raw, _, _ = filled(c, h)
+    q = dev((c.rng.standard_normal((n, h * d))).astype(np.float32))
+    clean = g.kv_attention(g.KVCache(dev(raw), page, h, d), c.batch(g), q, 0.125, window=100)
+    cells = c.cells(raw)
+    at = page * 34 * c.nb + (300 % page) * 2 * c.nb
+    cells[c.table[0, 300 // page], :, at:at + 2 * c.nb] = np.array([0x7E00] * c.nb, np.uint16).view(np.uint8)
+    got = g.kv_attention(g.KVCache(dev(raw), page, h, d), c.batch(g), q, 0.125, window=100)
+    assert torch.equal(got[:300], clean[:300]) and torch.equal(got[400:], clean[400:])
+    assert torch.all(torch.isnan(got[300:400]))
