@@ -59,6 +59,7 @@ constexpr float NO_KEY = -1e30f;   // reference of a row that has seen no positi
 
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef float f4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 
 template <int N> struct Words { uint32_t w[N]; };
 template <int N>
@@ -143,6 +144,19 @@ __device__ __forceinline__ Split times(Split s, half2v d) {
     r.h = s.h * d;
     r.l = __builtin_elementwise_fma(s.l, d, __builtin_elementwise_fma(s.h, d, -r.h));
     return r;
+}
+
+// LDS by byte offset: one register holds a lane's offset and every read adds a
+// constant to it.  (Left to itself the compiler keeps an address for every read
+// of an unrolled loop, some fifty registers.)
+__device__ __forceinline__ uint32_t lds_at(const void* p) {
+    uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+    asm("" : "+v"(at));
+    return at;
+}
+template <class T>
+__device__ __forceinline__ T lds_read(uint32_t at) {
+    return *(__attribute__((address_space(3))) const T*)(uintptr_t)at;
 }
 
 // The value of lane n ^ 8 among 16.
@@ -414,7 +428,11 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
                             (uint64_t)(uint32_t)__builtin_amdgcn_readlane(at_hi, u) << 32;
         return kv.pages + at;
     };
-    const auto fetch_scales = [&](int seg) {  // and where the codes are
+    // The scales, and where the codes are, then the keys of a run.  Both without a branch, whose
+    // other side would keep a second copy of all the registers: where there is no next run, the
+    // lanes read one address of page 0.
+    uint32_t lane_k = 0;
+    const auto fetch_scales = [&](int seg) {
         const int t0 = seg * SEG + wave * SUB;
         const bool ok = pg >= 0 && (int64_t)pg < kv.n_pages;
         there = (uint32_t)__ballot(ok);  // tiles that have a page
@@ -426,13 +444,13 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
         const int u = lane >> 3, t = t0 + 16 * u + 2 * (lane & 7);
         const uint8_t* hd = head_of(kv, __shfl(p, u), head) + 2 * codes +
                             (int64_t)(t & (page_tokens - 1)) * 2 * NB;
-        if (TILES == 8 || u < TILES) {
-            dk = load_words<NB>(hd);
-            dv = load_words<NB>(hd + ((int64_t)(2 * NB) << kv.log2p));
-        }
+        dk = load_words<NB>(hd);
+        dv = load_words<NB>(hd + ((int64_t)(2 * NB) << kv.log2p));
+        lane_k = works(seg) ? (lane & 15) * (16 * NB) + g * (4 * NB) : 0;
     };
-    const auto fetch_keys = [&](int u) {
-        cw[u] = load_words<NB>(tile_codes(u) + (lane & 15) * (16 * NB) + g * (4 * NB));
+    const auto fetch_keys = [&] {
+#pragma unroll
+        for (int u = 0; u < TILES; u++) cw[u] = load_words<NB>(tile_codes(u) + lane_k);
     };
     fetch_pages(seg0);
 
@@ -440,11 +458,8 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
     float factor;
     int pos;
     prepare_q<NB>(a, s, head, G, first + n, rows, g, qh, ql, factor, pos, [&] {
-        if (works(seg0)) {
-            fetch_scales(seg0);
-#pragma unroll
-            for (int u = 0; u < TILES; u++) fetch_keys(u);
-        }
+        fetch_scales(seg0);
+        fetch_keys();
         fetch_pages(seg0 + 1);
     });
 
@@ -456,6 +471,10 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
 #pragma unroll
     for (int i = 0; i < SHARE; i++) O[i] = 0.0f;
     const Unpack unpack;
+    const uint32_t dk_at = lds_at(&s_dk[wave][0][8 * par + 2 * g]);
+    const uint32_t dv_at = lds_at(&s_dv[wave][0][8 * par + 2 * g]);
+    const uint32_t ev_at = lds_at(&s_ev[wave][16 * par + 4 * g]);
+    const uint32_t down_at = lds_at(&s_down[wave][16 * par + 4 * g]);
 
     for (int seg = seg0; seg < seg1; seg++) {
         const int t0 = seg * SEG + wave * SUB;
@@ -466,7 +485,6 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
             const bool masked = t0 + SUB > pos_lo + 1 || (a.window && t0 <= pos_hi - a.window) ||
                                 there != (1u << TILES) - 1;
             const uint32_t here = there;
-            const bool more = works(seg + 1);
             if (TILES == 8 || lane < 8 * TILES) {
                 const int u = lane >> 3, t = t0 + 16 * u + 2 * (lane & 7);
                 const int live = ((here >> u) & 1) ? s.len - t : 0;
@@ -480,27 +498,26 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
             // (the block scales of a lane's four positions are read from LDS one step ahead of use,
             // here and below: the scheduler left to itself waits for each)
             f4 sc[SLOTS];
-            const auto scales = [&](const uint32_t (&from)[NB][SUB / 2], int U, int bb) {
-                return *reinterpret_cast<const Words<2>*>(
-                    &from[bb][8 * (PACK ? 2 * U + par : U) + 2 * g]);
+            const auto scales = [&](uint32_t from, int U, int bb) {
+                return lds_read<u2>(from + 4 * (bb * (SUB / 2) + 8 * (PACK ? 2 * U : U)));
             };
-            Words<2> dn[NB];
+            u2 dn[NB];
 #pragma unroll
-            for (int bb = 0; bb < NB; bb++) dn[bb] = scales(s_dk[wave], 0, bb);
+            for (int bb = 0; bb < NB; bb++) dn[bb] = scales(dk_at, 0, bb);
 #pragma unroll
             for (int U = 0; U < SLOTS; U++) {
                 f4 z = {0, 0, 0, 0};
-                Words<2> dc[NB];
+                u2 dc[NB];
 #pragma unroll
                 for (int bb = 0; bb < NB; bb++) dc[bb] = dn[bb];
                 if (U + 1 < SLOTS) {
 #pragma unroll
-                    for (int bb = 0; bb < NB; bb++) dn[bb] = scales(s_dk[wave], U + 1, bb);
+                    for (int bb = 0; bb < NB; bb++) dn[bb] = scales(dk_at, U + 1, bb);
                 }
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int bb = 0; bb < NB; bb++) {
-                    const Words<2> d = dc[bb];
+                    const u2 d = dc[bb];
                     f4 acc[PACK ? 2 : 1];
 #pragma unroll
                     for (int h = 0; h < (PACK ? 2 : 1); h++) {
@@ -512,12 +529,11 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
                     }
 #pragma unroll
                     for (int i = 0; i < 4; i++)
-                        z[i] = __builtin_fmaf((float)half_of(d.w[i >> 1], i & 1),
+                        z[i] = __builtin_fmaf((float)half_of(d[i >> 1], i & 1),
                                               PACK && par ? acc[PACK ? 1 : 0][i] : acc[0][i], z[i]);
                 }
                 // in base 2, relative to the size of the position's values
-                const f4 e = *reinterpret_cast<const f4*>(
-                    &s_ev[wave][16 * (PACK ? 2 * U + par : U) + 4 * g]);
+                const f4 e = lds_read<f4>(ev_at + 4 * 16 * (PACK ? 2 * U : U));
 #pragma unroll
                 for (int i = 0; i < 4; i++) sc[U][i] = __builtin_fmaf(z[i], factor, e[i]);
                 __builtin_amdgcn_sched_barrier(0);
@@ -553,8 +569,7 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
             Split p[SLOTS][2];            // positions 0, 2 and 1, 3
 #pragma unroll
             for (int U = 0; U < SLOTS; U++) {
-                const f4 down = *reinterpret_cast<const f4*>(
-                    &s_down[wave][16 * (PACK ? 2 * U + par : U) + 4 * g]);
+                const f4 down = lds_read<f4>(down_at + 4 * 16 * (PACK ? 2 * U : U));
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
                     sc[U][i] = exp2_raw(sc[U][i] - ref);
@@ -571,10 +586,10 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
 
             // Values, two tiles of one parity (32 positions) at a product: the weights of slots
             // U0, U1 times the block's scales.
-            const auto split_weights = [&](int U0, int U1, Words<2> d0, Words<2> d1, half8& ph,
+            const auto split_weights = [&](int U0, int U1, u2 d0, u2 d1, half8& ph,
                                            half8& pl) {
-                const Split a0 = times(p[U0][0], halves(d0.w[0])), a1 = times(p[U0][1], halves(d0.w[1]));
-                const Split a2 = times(p[U1][0], halves(d1.w[0])), a3 = times(p[U1][1], halves(d1.w[1]));
+                const Split a0 = times(p[U0][0], halves(d0[0])), a1 = times(p[U0][1], halves(d0[1]));
+                const Split a2 = times(p[U1][0], halves(d1[0])), a3 = times(p[U1][1], halves(d1[1]));
                 ph = operand(word(a0.h), word(a1.h), word(a2.h), word(a3.h));
                 pl = operand(word(a0.l), word(a1.l), word(a2.l), word(a3.l));
             };
@@ -591,22 +606,20 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
                 o[2 * bb] = mfma(even, ph, o[2 * bb]);
                 o[2 * bb + 1] = mfma(odd, ph, o[2 * bb + 1]);
             };
-            if (more) fetch_scales(seg + 1);
-            fetch_pages(seg + 2);
             if constexpr (PACK) {
                 constexpr int Q = TILES / 4;
-                Words<2> dn[SLOTS];
+                u2 dn[SLOTS];
 #pragma unroll
-                for (int U = 0; U < SLOTS; U++) dn[U] = scales(s_dv[wave], U, 0);
+                for (int U = 0; U < SLOTS; U++) dn[U] = scales(dv_at, U, 0);
 #pragma unroll
                 for (int bb = 0; bb < NB; bb++) {
                     half8 ph[Q], pl[Q];
-                    Words<2> dc[SLOTS];
+                    u2 dc[SLOTS];
 #pragma unroll
                     for (int U = 0; U < SLOTS; U++) dc[U] = dn[U];
                     if (bb + 1 < NB) {
 #pragma unroll
-                        for (int U = 0; U < SLOTS; U++) dn[U] = scales(s_dv[wave], U, bb + 1);
+                        for (int U = 0; U < SLOTS; U++) dn[U] = scales(dv_at, U, bb + 1);
                     }
                     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -624,24 +637,20 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
                         add_values(4 * q + 1, 4 * q + 3, bb, ph[q], pl[q], false);
                     __builtin_amdgcn_sched_barrier(0);
                 }
-                if (more) {
-#pragma unroll
-                    for (int u = 0; u < TILES; u++) fetch_keys(u);
-                }
             } else {
                 // tiles u and u + 2, even before odd
                 const auto tile_of = [&](int q) { return 4 * (q % (TILES / 4)) + q / (TILES / 4); };
-                Words<2> n0 = scales(s_dv[wave], tile_of(0), 0), n1 = scales(s_dv[wave], tile_of(0) + 2, 0);
+                u2 n0 = scales(dv_at, tile_of(0), 0), n1 = scales(dv_at, tile_of(0) + 2, 0);
 #pragma unroll
                 for (int q = 0; q < TILES / 2; q++) {
                     const int u = tile_of(q);
 #pragma unroll
                     for (int bb = 0; bb < NB; bb++) {
-                        const Words<2> d0 = n0, d1 = n1;
+                        const u2 d0 = n0, d1 = n1;
                         if (bb + 1 < NB || q + 1 < TILES / 2) {
                             const int un = bb + 1 < NB ? u : tile_of(q + 1), bn = bb + 1 < NB ? bb + 1 : 0;
-                            n0 = scales(s_dv[wave], un, bn);
-                            n1 = scales(s_dv[wave], un + 2, bn);
+                            n0 = scales(dv_at, un, bn);
+                            n1 = scales(dv_at, un + 2, bn);
                         }
                         __builtin_amdgcn_sched_barrier(0);
                         half8 ph, pl;
@@ -649,20 +658,12 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
                         add_values(u, u + 2, bb, ph, pl, q == 0);
                         __builtin_amdgcn_sched_barrier(0);
                     }
-                    if (more) {  // the next run's keys take the registers
-                        fetch_keys(u);
-                        fetch_keys(u + 2);
-                    }
                 }
             }
-        } else {
-            if (works(seg + 1)) {
-                fetch_scales(seg + 1);
-#pragma unroll
-                for (int u = 0; u < TILES; u++) fetch_keys(u);
-            }
-            fetch_pages(seg + 2);
         }
+        fetch_scales(seg + 1);
+        fetch_keys();
+        fetch_pages(seg + 2);
 
         // join the waves' parts of the segment, then the segment to the state
         if (lane < ROWS) {
@@ -797,32 +798,36 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_wide(AttnArgs a, Plan pl
         if (sub < sub1 && lane < TILES && t < s.len) pg = table[t >> kv.log2p];
     };
     // the wave's share: tiles 2w, 2w + 1 of keys, pair w of values, wave 0 the keys' and wave 1 the
-    // values' scales; returns which tiles have a page
-    const auto fetch = [&](int sub) {
+    // values' scales; fetch_keys notes which tiles have a page and where all of them lie
+    uint32_t at_lo = 0, at_hi = 0;
+    const auto tile_codes = [&](int u) {
+        return kv.pages + ((uint32_t)__builtin_amdgcn_readlane(at_lo, u) |
+                           (uint64_t)(uint32_t)__builtin_amdgcn_readlane(at_hi, u) << 32);
+    };
+    const auto fetch_keys = [&](int sub) {
         const int t0 = sub * SUB;
         const bool ok = pg >= 0 && (int64_t)pg < kv.n_pages;
-        const uint32_t have = (uint32_t)__ballot(ok);
+        there = (uint32_t)__ballot(ok);
         const int p = ok ? pg : 0;  // tiles without a page read page 0, which is not used
         const int64_t at = ((int64_t)p * kv.Hkv + head) * kv.head_bytes +
                            (int64_t)((t0 + 16 * lane) & (page_tokens - 1)) * (16 * NB);
-        const uint32_t lo = (uint32_t)at, hi = (uint32_t)(at >> 32);
-        const auto tile_codes = [&](int u) {
-            return kv.pages + ((uint32_t)__builtin_amdgcn_readlane(lo, u) |
-                               (uint64_t)(uint32_t)__builtin_amdgcn_readlane(hi, u) << 32);
-        };
-        const int vu = tile_of(wave);
+        at_lo = (uint32_t)at;
+        at_hi = (uint32_t)(at >> 32);
 #pragma unroll
-        for (int i = 0; i < 2; i++) {
+        for (int i = 0; i < 2; i++)
             kw[i] = load_words<NB>(tile_codes(2 * wave + i) + n * (16 * NB) + g * (4 * NB));
-            vw[i] = load_words<NB>(tile_codes(vu + 2 * i) + codes + lane * (4 * NB));
-        }
         if (wave < 2) {
             const int u = lane >> 3, t = t0 + 16 * u + 2 * (lane & 7);
             dd = load_words<NB>(head_of(kv, __shfl(p, u), head) + 2 * codes +
                                 ((int64_t)(wave ? 2 * NB : 0) << kv.log2p) +
                                 (int64_t)(t & (page_tokens - 1)) * 2 * NB);
         }
-        return have;
+    };
+    const auto fetch_values = [&] {
+        const int u = tile_of(wave);
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+            vw[i] = load_words<NB>(tile_codes(u + 2 * i) + codes + lane * (4 * NB));
     };
     const auto live_of = [&](int sub, uint32_t have) {
         const int u = lane >> 3, t = sub * SUB + 16 * u + 2 * (lane & 7);
@@ -850,18 +855,19 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_wide(AttnArgs a, Plan pl
         }
         if (wave == 1) stage_value_scales<NB>(dd, live_of(sub, have), lane, s_dv, s_down);
     };
-    const auto at_lds = [](const uint4& v) {
-        half8 h;
-        __builtin_memcpy(&h, &v, 16);
-        return h;
-    };
+    const uint32_t k_at = lds_at(&s_k[0][lane]), v_at = lds_at(&s_v[0][lane]);
+    const uint32_t dk_at = lds_at(&s_dk[0][2 * g]), dv_at = lds_at(&s_dv[0][2 * g]);
+    const uint32_t ev_at = lds_at(s_ev + 4 * g), down_at = lds_at(s_down + 4 * g);
 
     fetch_pages(sub0);
     half8 qh[NB], ql[NB];
     float factor;
     int pos;
     prepare_q<NB>(a, s, head, G, row0 + n, rows, g, qh, ql, factor, pos, [&] {
-        if (sub0 < sub1) there = fetch(sub0);
+        if (sub0 < sub1) {
+            fetch_keys(sub0);
+            fetch_values();
+        }
         fetch_pages(sub0 + 1);
     });
     if (sub0 < sub1) {
@@ -870,12 +876,21 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_wide(AttnArgs a, Plan pl
     }
     __syncthreads();
 
-    // the state over whole segments, and the segment's; row n of the wave, elements 32b + 8g + 2i
-    // (first of a pair of f4) and + 1
-    f4 O[2 * NB], os[2 * NB];
+    // The segment's state: row n of the wave, elements 32b + 8g + 2i (first of a pair of f4) and + 1.
+    // The state over whole segments would take as many registers again: its sums wait in the
+    // row's place in out between segments.
+    const int rr = row0 + n;
+    float* out = a.out + 8 * g;
+    if (rr < rows) out += ((int64_t)(s.q0 + rr / G) * a.Hq + head * G + rr % G) * D;
+    f4 os[2 * NB];
     float R = NO_KEY, L = 0.0f, rs = NO_KEY, ls = 0.0f;
+    bool begun = false;
 #pragma unroll
-    for (int i = 0; i < 2 * NB; i++) O[i] = os[i] = f4{0, 0, 0, 0};
+    for (int i = 0; i < 2 * NB; i++) os[i] = f4{0, 0, 0, 0};
+    if (sub0 >= sub1 && rr < rows) {  // rows that see no position
+#pragma unroll
+        for (int i = 0; i < 2 * NB; i++) *reinterpret_cast<f4*>(out + 32 * (i / 2) + 4 * (i & 1)) = os[i];
+    }
 
     for (int sub = sub0; sub < sub1; sub++) {
         const int t0 = sub * SUB;
@@ -883,30 +898,51 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_wide(AttnArgs a, Plan pl
         const bool masked = t0 + SUB > pos_lo + 1 || (a.window && t0 <= pos_hi - a.window) || there != 0xFF;
         const uint32_t here = there;
         const bool more = sub + 1 < sub1;
-        if (more) there = fetch(sub + 1);
-        fetch_pages(sub + 2);
         f4 sc[TILES];
         if (work) {
-#pragma unroll
-            for (int u = 0; u < TILES; u++) {
-                f4 z = {0, 0, 0, 0};
+            // operands and scales are read one step ahead
+            half8 kn[NB];
+            u2 dn[NB];
+            const auto ahead = [&](int u) {
 #pragma unroll
                 for (int bb = 0; bb < NB; bb++) {
-                    const Words<2> d = *reinterpret_cast<const Words<2>*>(&s_dk[bb][8 * u + 2 * g]);
-                    const half8 ko = at_lds(s_k[u * NB + bb][lane]);
-                    f4 acc = mfma(ko, ql[bb], f4{0, 0, 0, 0});
-                    acc = mfma(ko, qh[bb], acc);
+                    kn[bb] = lds_read<half8>(k_at + 1024 * (u * NB + bb));
+                    dn[bb] = lds_read<u2>(dk_at + 4 * (bb * (SUB / 2) + 8 * u));
+                }
+            };
+            ahead(0);
+#pragma unroll
+            for (int u = 0; u < TILES; u++) {
+                half8 ko[NB];
+                u2 d[NB];
+#pragma unroll
+                for (int bb = 0; bb < NB; bb++) {
+                    ko[bb] = kn[bb];
+                    d[bb] = dn[bb];
+                }
+                const f4 e = lds_read<f4>(ev_at + 64 * u);
+                if (u + 1 < TILES) ahead(u + 1);
+                __builtin_amdgcn_sched_barrier(0);
+                f4 acc[NB], z = {0, 0, 0, 0};
+#pragma unroll
+                for (int bb = 0; bb < NB; bb++) acc[bb] = mfma(ko[bb], ql[bb], f4{0, 0, 0, 0});
+#pragma unroll
+                for (int bb = 0; bb < NB; bb++) acc[bb] = mfma(ko[bb], qh[bb], acc[bb]);
+#pragma unroll
+                for (int bb = 0; bb < NB; bb++)
 #pragma unroll
                     for (int i = 0; i < 4; i++)
-                        z[i] = __builtin_fmaf((float)half_of(d.w[i >> 1], i & 1), acc[i], z[i]);
-                }
-                const f4 e = *reinterpret_cast<const f4*>(&s_ev[16 * u + 4 * g]);
+                        z[i] = __builtin_fmaf((float)half_of(d[bb][i >> 1], i & 1), acc[bb][i], z[i]);
 #pragma unroll
                 for (int i = 0; i < 4; i++) sc[u][i] = __builtin_fmaf(z[i], factor, e[i]);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
+        // the next run's keys arrive during the softmax, its values while these are worked on
+        if (more) fetch_keys(sub + 1);
         __syncthreads();  // every wave is done with the keys
-        if (more) stage_keys(sub + 1, there);
+        Split p[TILES][2];  // weights of positions 0, 2 and 1, 3 of each four
+        Join js{1.0f, 0.0f};
         if (work) {
             if (masked) {
                 const int rel = pos - t0 - 4 * g;
@@ -927,10 +963,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_wide(AttnArgs a, Plan pl
             top = max_rows(top);
             const float ref = top > -INFINITY ? top - 14.0f : 0.0f;
             float sum[2] = {0.0f, 0.0f};  // over the even and the odd tiles
-            Split p[TILES][2];            // positions 0, 2 and 1, 3
 #pragma unroll
             for (int u = 0; u < TILES; u++) {
-                const f4 down = *reinterpret_cast<const f4*>(&s_down[16 * u + 4 * g]);
+                const f4 down = lds_read<f4>(down_at + 64 * u);
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
                     sc[u][i] = exp2_raw(sc[u][i] - ref);
@@ -938,30 +973,50 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_wide(AttnArgs a, Plan pl
                 }
                 p[u][0] = two_parts(sc[u][0], sc[u][2]);
                 p[u][1] = two_parts(sc[u][1], sc[u][3]);
+                if (u & 1) __builtin_amdgcn_sched_barrier(0);
             }
             const float l = sum_rows(sum[0] + sum[1]);
             const float r = top == -INFINITY && l == 0.0f ? NO_KEY : ref;
-            const Join js = join(rs, r);
+            js = join(rs, r);
             ls = joined(ls, l, js);
+        }
+        if (more) {
+            stage_keys(sub + 1, there);
+            fetch_values();
+        }
+        fetch_pages(sub + 2);
+        if (work) {
+            half8 en, on;  // the next step's operands and scales
+            u2 n0, n1;
+            const auto next = [&](int bb, int q) {
+                const int u = tile_of(q);
+                en = lds_read<half8>(v_at + 1024 * ((q * NB + bb) * 2));
+                on = lds_read<half8>(v_at + 1024 * ((q * NB + bb) * 2 + 1));
+                n0 = lds_read<u2>(dv_at + 4 * (bb * (SUB / 2) + 8 * u));
+                n1 = lds_read<u2>(dv_at + 4 * (bb * (SUB / 2) + 8 * u + 16));
+            };
+            next(0, 0);
 #pragma unroll
             for (int bb = 0; bb < NB; bb++) {
                 f4 o0 = {0, 0, 0, 0}, o1 = o0;
 #pragma unroll
                 for (int q = 0; q < TILES / 2; q++) {
                     const int u = tile_of(q);
-                    const Words<2> d0 = *reinterpret_cast<const Words<2>*>(&s_dv[bb][8 * u + 2 * g]);
-                    const Words<2> d1 = *reinterpret_cast<const Words<2>*>(&s_dv[bb][8 * u + 16 + 2 * g]);
-                    const Split a0 = times(p[u][0], halves(d0.w[0])), a1 = times(p[u][1], halves(d0.w[1]));
-                    const Split a2 = times(p[u + 2][0], halves(d1.w[0]));
-                    const Split a3 = times(p[u + 2][1], halves(d1.w[1]));
+                    const half8 even = en, odd = on;
+                    const u2 d0 = n0, d1 = n1;
+                    if (q + 1 < TILES / 2) next(bb, q + 1);
+                    else if (bb + 1 < NB) next(bb + 1, 0);
+                    __builtin_amdgcn_sched_barrier(0);
+                    const Split a0 = times(p[u][0], halves(d0[0])), a1 = times(p[u][1], halves(d0[1]));
+                    const Split a2 = times(p[u + 2][0], halves(d1[0]));
+                    const Split a3 = times(p[u + 2][1], halves(d1[1]));
                     const half8 ph = operand(word(a0.h), word(a1.h), word(a2.h), word(a3.h));
                     const half8 pl = operand(word(a0.l), word(a1.l), word(a2.l), word(a3.l));
-                    const half8 even = at_lds(s_v[(q * NB + bb) * 2][lane]);
-                    const half8 odd = at_lds(s_v[(q * NB + bb) * 2 + 1][lane]);
                     o0 = mfma(even, pl, o0);
                     o1 = mfma(odd, pl, o1);
                     o0 = mfma(even, ph, o0);
                     o1 = mfma(odd, ph, o1);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
@@ -975,27 +1030,27 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_wide(AttnArgs a, Plan pl
         if ((sub & (WAVES - 1)) == WAVES - 1 || !more) {  // the segment is complete
             const Join jn = join(R, rs);
             L = joined(L, ls, jn);
+            if (rr < rows) {
 #pragma unroll
-            for (int i = 0; i < 2 * NB; i++)
+                for (int i = 0; i < 2 * NB; i++) {
+                    f4* at = reinterpret_cast<f4*>(out + 32 * (i / 2) + 4 * (i & 1));
+                    f4 x = {0, 0, 0, 0};
+                    if (begun) x = *at;
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    O[i][e] = joined(O[i][e], os[i][e], jn);
-                    os[i][e] = 0.0f;
+                    for (int e = 0; e < 4; e++) {
+                        const float part = os[(i & ~1) + (e & 1)][2 * (i & 1) + (e >> 1)];
+                        x[e] = joined(x[e], part, jn);
+                        if (!more) x[e] = result(x[e], L);
+                    }
+                    *at = x;
                 }
+            }
+#pragma unroll
+            for (int i = 0; i < 2 * NB; i++) os[i] = f4{0, 0, 0, 0};
+            begun = true;
             rs = NO_KEY;
             ls = 0.0f;
         }
-    }
-    const int rr = row0 + n;
-    if (rr >= rows) return;
-    float* out = a.out + ((int64_t)(s.q0 + rr / G) * a.Hq + head * G + rr % G) * D + 8 * g;
-#pragma unroll
-    for (int bb = 0; bb < NB; bb++) {
-        const f4 x = O[2 * bb], y = O[2 * bb + 1];
-        *reinterpret_cast<f4*>(out + 32 * bb) =
-            f4{result(x[0], L), result(y[0], L), result(x[1], L), result(y[1], L)};
-        *reinterpret_cast<f4*>(out + 32 * bb + 4) =
-            f4{result(x[2], L), result(y[2], L), result(x[3], L), result(y[3], L)};
     }
 }
 
@@ -1103,17 +1158,19 @@ Plan plan_of(bool one, int64_t T, int64_t B, int Hq, int Hkv, int nb, int64_t ma
     const int64_t G = Hq / Hkv;
     Plan p;
     // Packed tiles of 8 rows where the sequences of a call have that few per key/value head on
-    // average; 64 rows a workgroup where that many fill them and the chip (a 2048-token prompt with
-    // a window of 1024, 32 heads on 8: WIDE us, 182 in tiles of 16); else tiles of 16.
+    // average; 64 rows a workgroup where that many fill them and there are four per CU, as long
+    // and short ones have to even out (a 2048-token prompt with a window of 1024, 32 heads on 8:
+    // 120 us, 182 in tiles of 16; four chunks of 256 tokens on prefixes of up to 3750, with half as
+    // many workgroups, 206 against 171); else tiles of 16.
     p.pack = nb <= 4 && (one ? G <= 8 : T * G <= 8 * B);
-    p.wide = nb <= 4 && !one && T * G >= 64 * B && (T * G / 64 + B) * Hkv >= 512;
+    p.wide = nb <= 4 && !one && T * G >= 64 * B && (T * G / 64 + B) * Hkv >= 1024;
     const int64_t tr = p.wide ? 64 : p.pack ? 8 : 16;
     p.tiles = (int32_t)(one ? B * ((G + tr - 1) / tr) : T * G / tr + B);
     p.segs = (int32_t)((max_len + seg_of(nb) - 1) / seg_of(nb));
     // One sequence: as many workgroups as run at once (two per CU), each with several segments,
-    // so that the loads ahead work and the prologue is paid once (131072 positions: 44 us, and 48
-    // with twice as many).  Several sequences differ in length: four times as many, which even out
-    // (32 of 301..8191: 64 us, 73 with twice, 97 with one workgroup per sequence and head).
+    // so that the loads ahead work and the prologue is paid once (131072 positions, 32 heads on 8: 42
+    // us, and 44 with twice as many).  Several sequences differ in length: four times as many, which
+    // even out (32 of 301..8191: 60 us, and 68 with as many as for one).
     const int64_t groups = (int64_t)p.tiles * Hkv, want = B == 1 ? 512 : 2048;
     int64_t splits = groups >= 512 ? 1 : (want + groups - 1) / groups;
     if (splits > p.segs) splits = p.segs;
