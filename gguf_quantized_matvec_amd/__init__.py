@@ -661,6 +661,8 @@ class KVCache:
             raise ValueError(f"bad cache shape page_tokens={page_tokens} kv_heads={kv_heads} "
                              f"head_dim={head_dim}")
         if pages is None:
+            if n_pages is None or n_pages < 1:
+                raise ValueError(f"give pages, or n_pages for new ones, got n_pages={n_pages}")
             pages = torch.empty(one * n_pages, dtype=torch.uint8, device=device)
         ptr = _dev(pages, torch.uint8, "pages")
         if pages.numel() == 0 or pages.numel() % one:

@@ -25,7 +25,8 @@ int add_rmsnorm(const float* x, const float* res, const float* w, float eps, int
     // the sum is handed on exactly when something is added
     if ((res != nullptr) != (h != nullptr)) return QMV_EINVAL_PTR;
     if (!aligned(res, 4) || !aligned(h, 4) || !aligned(y, 4)) return QMV_EINVAL_PTR;
-    if (y && (y == x || y == res || y == h)) return QMV_EINVAL_PTR;
+    if (y && (y == x || y == res || y == h || y == w)) return QMV_EINVAL_PTR;
+    if (h == w) return QMV_EINVAL_PTR;
     const int rc = check_device();
     if (rc) return rc;
     return launched(qmv::launch_add_rmsnorm(x, res, w, eps, rows, K, h, y,
@@ -69,6 +70,12 @@ bool q_heads_ok(int q_heads, int kv_heads) {
     return q_heads >= kv_heads && q_heads <= QMV_KV_MAX_HEADS && q_heads % kv_heads == 0;
 }
 
+// The workgroups of an attention, one per row tile and key/value head (8 rows or more a tile, one
+// tile more per sequence): a grid of 256 threads each holds fewer than 2^24.
+bool tiles_ok(int64_t T, int64_t B, int64_t q_heads, int64_t kv_heads) {
+    return T * q_heads / 8 + B * kv_heads < (1 << 24);
+}
+
 }  // namespace
 
 extern "C" {
@@ -102,6 +109,7 @@ int qmv_kv_append(const qmv_kv* kv, const qmv_kv_batch* seqs, const float* q, in
         !aligned(v, 4) || !aligned(q_out, 4) || !aligned(freq, 8))
         return QMV_EINVAL_PTR;
     if (q_out == q && q_stride != qd) return QMV_EINVAL_PTR;  // in place: the same rows
+    if (q_out == k || q_out == v) return QMV_EINVAL_PTR;
     if ((rc = check_device())) return rc;
     a.q = q;
     a.k = k;
@@ -130,7 +138,7 @@ size_t qmv_kv_attention_bytes(int64_t T, int64_t B, int q_heads, int kv_heads, i
                               int64_t max_len) {
     if (!cache_shape_ok(1, 16, kv_heads, head_dim) || !q_heads_ok(q_heads, kv_heads) || B < 1 ||
         B > QMV_KV_MAX_ROWS || T < 1 || T > QMV_KV_MAX_ROWS || max_len < 1 ||
-        max_len > QMV_KV_MAX_LEN)
+        max_len > QMV_KV_MAX_LEN || !tiles_ok(T, B, q_heads, kv_heads))
         return 0;
     return (size_t)qmv::kv_attention_bytes(T, B, q_heads, kv_heads, head_dim / 32, max_len);
 }
@@ -142,7 +150,8 @@ int qmv_kv_attention(const qmv_kv* kv, const qmv_kv_batch* seqs, const float* q,
     int rc = kv_args(kv, seqs, &a.kv);
     if (rc) return rc;
     if (!q_heads_ok(q_heads, kv->kv_heads) || q_stride < (int64_t)q_heads * kv->head_dim ||
-        q_stride % 4 || window < 0 || !(scale > 0.0f && scale <= 1e6f))
+        q_stride % 4 || window < 0 || !(scale > 0.0f && scale <= 1e6f) ||
+        !tiles_ok(seqs->T, seqs->B, q_heads, kv->kv_heads))
         return QMV_EINVAL_SHAPE;
     if (!q || !out || !work || !aligned(q, 16) || !aligned(out, 16) || !aligned(work, 16) ||
         out == q)

@@ -449,10 +449,11 @@ size_t qmv_kv_bytes(int64_t n_pages, int page_tokens, int kv_heads, int head_dim
  * when rot is 0): angle, sine, cosine and products in f64, rounded once to
  * f32.  q_out [T][q_heads * head_dim] receives the rotated q (it may be q
  * itself when q_stride is that row); the rotated k and v are quantised into
- * the pages.  A row whose position is negative is skipped, q_out included;
- * one whose page is out of range writes only its q_out.  Every position
- * written must lie in a page that no other sequence of the call writes.
- * Other tokens of the pages keep their bytes. */
+ * the pages; q_out overlaps nothing else.  A row whose position is negative is
+ * skipped, q_out included; one whose page is out of range writes only its
+ * q_out.  Every page written must belong to one sequence of the call, and to
+ * one place of its table: of two rows that meet in one place, either or a mix
+ * of both is stored.  Other tokens of the pages keep their bytes. */
 int qmv_kv_append(const qmv_kv* kv, const qmv_kv_batch* seqs, const float* q, int64_t q_stride,
                   int q_heads, const float* k, int64_t k_stride, const float* v, int64_t v_stride,
                   const double* freq, int rot, int halves, float* q_out, void* stream);
@@ -473,8 +474,15 @@ size_t qmv_kv_attention_bytes(int64_t T, int64_t B, int q_heads, int kv_heads, i
  * that sees no position.  Query heads j * (q_heads / kv_heads) ... read
  * key/value head j.  q: T rows of q_heads * head_dim f32, q_stride floats
  * apart (a multiple of 4), 16-byte aligned; out [T][q_heads * head_dim],
- * 16-byte aligned, not q; work: qmv_kv_attention_bytes(T, B, ...) bytes,
- * 16-byte aligned, used by one call at a time; 0 < scale <= 1e6. */
+ * 16-byte aligned; work: qmv_kv_attention_bytes(T, B, ...) bytes, 16-byte
+ * aligned, used by one call at a time; out and work overlap nothing else;
+ * 0 < scale <= 1e6; T * q_heads / 8 + B * kv_heads < 2^24.
+ * The products keep 22 bits of q and of the weights, sums are f32: the result
+ * has the accuracy of an f32 computation.  A row's bits depend on its q and on
+ * the positions it sees alone: not on the other rows, on how a prompt is cut
+ * into calls, on the pages' order or on max_len.  A row that sees a position
+ * with a non-finite scale, or whose q is not finite, is NaN throughout; what
+ * a row does not see, uninitialised pages included, does not reach it. */
 int qmv_kv_attention(const qmv_kv* kv, const qmv_kv_batch* seqs, const float* q, int64_t q_stride,
                      int q_heads, float scale, int64_t window, float* out, void* work,
                      void* stream);

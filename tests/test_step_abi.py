@@ -171,3 +171,34 @@ def test_helpers_refuse_on_the_host():
         g.KVBatch(torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32),
                   torch.zeros(2, dtype=torch.int32), T=2, max_len=5)
     assert ctypes.sizeof(g.KvStruct) == 32 and ctypes.sizeof(g.KvBatchStruct) == 56
+
+
+@pytest.mark.parametrize("h,y", [(P, None), (2 * P, P)])
+def test_norm_refuses_outputs_over_the_weights(h, y):
+    assert g.lib().qmv_add_rmsnorm_q8_0(3 * P, 4 * P, P, 1e-5, 1, 64, h, y, 5 * P, None) == PTR
+
+
+@pytest.mark.parametrize("out", [2 * P, 3 * P])
+def test_append_refuses_an_output_over_k_or_v(out):
+    args = (P, 256, 4, 2 * P, 128, 3 * P, 128, 4 * P, 64, 0, out)
+    assert g.lib().qmv_kv_append(kv(), seqs(), *args, None) == PTR
+
+
+@pytest.mark.parametrize("T,B,q_heads,kv_heads", [
+    (1 << 20, 1 << 20, 32, 32), (1 << 20, 1, 128, 128), (1 << 17, 1 << 17, 1024, 1024),
+    (1 << 14, 1 << 14, 1024, 1024)])
+def test_attention_refuses_more_tiles_than_a_grid_holds(T, B, q_heads, kv_heads):
+    one = T == B
+    few = 100 if one else 1
+    for t, b, refused in ((T, B, True), (100, few, False)):
+        n = g.qmv_kv_attention_bytes(t, b, q_heads, kv_heads, 32, 32)
+        assert (n == 0) == refused
+    s = seqs(B=B, T=T, q_start=None if one else P)
+    assert g.lib().qmv_kv_attention(kv(kv_heads=kv_heads, head_dim=32), s, P, 32 * q_heads, q_heads, 0.1, 0,
+                                    2 * P, 3 * P, None) == SHAPE
+
+
+def test_new_pages_need_a_number():
+    for n in (None, 0, -1):
+        with pytest.raises(ValueError):
+            g.KVCache(None, 16, 1, 32, n_pages=n)
