@@ -59,6 +59,7 @@ constexpr float NO_KEY = -1e30f;   // reference of a row that has seen no positi
 
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef float f4 __attribute__((ext_vector_type(4)));
+typedef float f2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 
 template <int N> struct Words { uint32_t w[N]; };
@@ -132,8 +133,8 @@ struct Split {
 };
 __device__ __forceinline__ Split two_parts(float a, float b) {
     Split s;
-    s.h = half2v{(_Float16)a, (_Float16)b};
-    s.l = half2v{(_Float16)(a - (float)s.h[0]), (_Float16)(b - (float)s.h[1])};
+    s.h = __builtin_convertvector(f2{a, b}, half2v);
+    s.l = __builtin_convertvector(f2{a - (float)s.h[0], b - (float)s.h[1]}, half2v);
     return s;
 }
 // s d, split again: what the rounded product of the first part leaves is exact in the f16 fma,
@@ -363,8 +364,14 @@ __device__ __forceinline__ void stage_value_scales(Words<NB> dv, int live, int l
 // two tiles at a time.  The values' sums run over the even
 // tiles, move across, and go on over the odd tiles, which is the order of the
 // sums in every variant.
+//
+// What bounds it: with few rows the loads' latency and the VALU, half busy (131072 positions, 42 us,
+// 3.6 TB/s), with many the VALU (about 1700 instructions a wave and run, a third of them unpacking,
+// beside 128 matrix instructions: 70 % busy on four chunks of 256 tokens, 172 us).  So three waves a
+// SIMD: the rows' two parts, the same for the four waves, wait in LDS, and a wave's sums take the
+// place of its scales (32 sequences of 301..8191: 54 us, 60 with the rows in registers, two waves).
 template <int NB, bool PACK>
-__global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a, Plan plan) {
+__global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void k_attn(AttnArgs a, Plan plan) {
     const KvArgs& kv = a.kv;
     constexpr int D = 32 * NB, SUB = sub_of(NB), SEG = seg_of(NB), TILES = SUB / 16;
     constexpr int ROWS = PACK ? 8 : 16;           // rows of a tile
@@ -372,11 +379,19 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
     constexpr int NBP = NB < 4 ? NB : 4;          // blocks joined at a time
     constexpr int LD = 32 * NBP + 4;
     constexpr int PER_ROW = 64 * WAVES / ROWS;    // threads that join a row
-    __shared__ __align__(16) uint32_t s_dk[WAVES][NB][SUB / 2];  // [block][position] fp16
-    __shared__ __align__(16) uint32_t s_dv[WAVES][NB][SUB / 2];
-    __shared__ __align__(16) float s_ev[WAVES][SUB], s_down[WAVES][SUB];
-    __shared__ __align__(16) float s_o[WAVES][ROWS * LD];
-    __shared__ float s_r[WAVES][ROWS], s_l[WAVES][ROWS];
+    // A wave's own part: the scales of its run ([block][position], fp16), which nobody else reads,
+    // and in their place, once it is done with them, its sums of the run for all to join.
+    struct Scales {
+        uint32_t dk[NB][SUB / 2], dv[NB][SUB / 2];
+        float ev[SUB], down[SUB];
+    };
+    union Own {
+        Scales s;
+        float o[ROWS * LD];
+    };
+    __shared__ __align__(16) Own s_own[WAVES];
+    __shared__ __align__(16) float s_r[ROWS][WAVES], s_l[ROWS][WAVES];
+    __shared__ __align__(16) uint4 s_q[2 * NB][64];  // the rows' two parts, the same for every wave
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int n = lane & (ROWS - 1), par = PACK ? (lane >> 3) & 1 : 0, g = lane >> 4;
@@ -454,14 +469,23 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
     };
     fetch_pages(seg0);
 
-    half8 qh[NB], ql[NB];
     float factor;
     int pos;
-    prepare_q<NB>(a, s, head, G, first + n, rows, g, qh, ql, factor, pos, [&] {
-        fetch_scales(seg0);
-        fetch_keys();
-        fetch_pages(seg0 + 1);
-    });
+    {
+        half8 qh[NB], ql[NB];
+        prepare_q<NB>(a, s, head, G, first + n, rows, g, qh, ql, factor, pos, [&] {
+            fetch_scales(seg0);
+            fetch_keys();
+            fetch_pages(seg0 + 1);
+        });
+#pragma unroll
+        for (int bb = 0; bb < NB; bb++)
+            if ((bb & (WAVES - 1)) == wave) {
+                __builtin_memcpy(&s_q[2 * bb][lane], &qh[bb], 16);
+                __builtin_memcpy(&s_q[2 * bb + 1][lane], &ql[bb], 16);
+            }
+    }
+    __syncthreads();
 
     // the joined state: thread (row tid / PER_ROW, part tid % PER_ROW) holds its share of every
     // NBP blocks
@@ -470,11 +494,15 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
     float O[SHARE], L = 0.0f, RR = NO_KEY;
 #pragma unroll
     for (int i = 0; i < SHARE; i++) O[i] = 0.0f;
+    const auto row_of = [&](int i) {  // row i of the tile among all rows of the call
+        return (int64_t)(s.q0 + (first + i) / G) * a.Hq + head * G + (first + i) % G;
+    };
     const Unpack unpack;
-    const uint32_t dk_at = lds_at(&s_dk[wave][0][8 * par + 2 * g]);
-    const uint32_t dv_at = lds_at(&s_dv[wave][0][8 * par + 2 * g]);
-    const uint32_t ev_at = lds_at(&s_ev[wave][16 * par + 4 * g]);
-    const uint32_t down_at = lds_at(&s_down[wave][16 * par + 4 * g]);
+    const uint32_t q_at = lds_at(&s_q[0][lane]);
+    const uint32_t dk_at = lds_at(&s_own[wave].s.dk[0][8 * par + 2 * g]);
+    const uint32_t dv_at = lds_at(&s_own[wave].s.dv[0][8 * par + 2 * g]);
+    const uint32_t ev_at = lds_at(&s_own[wave].s.ev[16 * par + 4 * g]);
+    const uint32_t down_at = lds_at(&s_own[wave].s.down[16 * par + 4 * g]);
 
     for (int seg = seg0; seg < seg1; seg++) {
         const int t0 = seg * SEG + wave * SUB;
@@ -488,55 +516,63 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
             if (TILES == 8 || lane < 8 * TILES) {
                 const int u = lane >> 3, t = t0 + 16 * u + 2 * (lane & 7);
                 const int live = ((here >> u) & 1) ? s.len - t : 0;
-                stage_key_scales<NB>(dk, live, lane, s_dk[wave]);
-                stage_value_sizes<NB>(dv, live, lane, s_ev[wave]);
-                stage_value_scales<NB>(dv, live, lane, s_dv[wave], s_down[wave]);
+                stage_key_scales<NB>(dk, live, lane, s_own[wave].s.dk);
+                stage_value_sizes<NB>(dv, live, lane, s_own[wave].s.ev);
+                stage_value_scales<NB>(dv, live, lane, s_own[wave].s.dv, s_own[wave].s.down);
             }
             wave_sync();
 
             // scores: sc[U][i] of row n at position t0 + 16 u + 4g + i, u the slot's tile
-            // (the block scales of a lane's four positions are read from LDS one step ahead of use,
-            // here and below: the scheduler left to itself waits for each)
+            // (the rows' parts and the block scales of a lane's four positions are read from LDS one
+            // step ahead of use, here and below: the scheduler left to itself waits for each)
             f4 sc[SLOTS];
             const auto scales = [&](uint32_t from, int U, int bb) {
                 return lds_read<u2>(from + 4 * (bb * (SUB / 2) + 8 * (PACK ? 2 * U : U)));
             };
-            u2 dn[NB];
+            half8 qhn, qln;
+            u2 dn[2];
+            const auto ahead = [&](int P, int bb) {
+                qhn = lds_read<half8>(q_at + 2048 * bb);
+                qln = lds_read<half8>(q_at + 2048 * bb + 1024);
+                dn[0] = scales(dk_at, PACK ? P : 2 * P, bb);
+                if constexpr (!PACK) dn[1] = scales(dk_at, 2 * P + 1, bb);
+            };
+            ahead(0, 0);
 #pragma unroll
-            for (int bb = 0; bb < NB; bb++) dn[bb] = scales(dk_at, 0, bb);
-#pragma unroll
-            for (int U = 0; U < SLOTS; U++) {
-                f4 z = {0, 0, 0, 0};
-                u2 dc[NB];
-#pragma unroll
-                for (int bb = 0; bb < NB; bb++) dc[bb] = dn[bb];
-                if (U + 1 < SLOTS) {
-#pragma unroll
-                    for (int bb = 0; bb < NB; bb++) dn[bb] = scales(dk_at, U + 1, bb);
-                }
-                __builtin_amdgcn_sched_barrier(0);
+            for (int P = 0; P < TILES / 2; P++) {
+                f4 z[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
                 for (int bb = 0; bb < NB; bb++) {
-                    const u2 d = dc[bb];
-                    f4 acc[PACK ? 2 : 1];
+                    const half8 qh = qhn, ql = qln;
+                    const u2 d[2] = {dn[0], dn[1]};
+                    if (bb + 1 < NB) ahead(P, bb + 1);
+                    else if (P + 1 < TILES / 2) ahead(P + 1, 0);
+                    __builtin_amdgcn_sched_barrier(0);
+                    f4 acc[2];
 #pragma unroll
-                    for (int h = 0; h < (PACK ? 2 : 1); h++) {
-                        const uint32_t w = cw[PACK ? 2 * U + h : U].w[bb], v = w >> 8;
+                    for (int h = 0; h < 2; h++) {
+                        const uint32_t w = cw[2 * P + h].w[bb], v = w >> 8;
                         const half8 ko =
                             operand(unpack.low(w), unpack.high(w), unpack.low(v), unpack.high(v));
-                        acc[h] = mfma(ko, ql[bb], f4{0, 0, 0, 0});
-                        acc[h] = mfma(ko, qh[bb], acc[h]);
+                        acc[h] = mfma(ko, ql, f4{0, 0, 0, 0});
+                        acc[h] = mfma(ko, qh, acc[h]);
                     }
 #pragma unroll
-                    for (int i = 0; i < 4; i++)
-                        z[i] = __builtin_fmaf((float)half_of(d[i >> 1], i & 1),
-                                              PACK && par ? acc[PACK ? 1 : 0][i] : acc[0][i], z[i]);
+                    for (int h = 0; h < (PACK ? 1 : 2); h++)
+#pragma unroll
+                        for (int i = 0; i < 4; i++)
+                            z[h][i] = __builtin_fmaf((float)half_of(d[h][i >> 1], i & 1),
+                                                     PACK && par ? acc[1][i] : acc[h][i], z[h][i]);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
                 // in base 2, relative to the size of the position's values
-                const f4 e = lds_read<f4>(ev_at + 4 * 16 * (PACK ? 2 * U : U));
 #pragma unroll
-                for (int i = 0; i < 4; i++) sc[U][i] = __builtin_fmaf(z[i], factor, e[i]);
-                __builtin_amdgcn_sched_barrier(0);
+                for (int h = 0; h < (PACK ? 1 : 2); h++) {
+                    const f4 e = lds_read<f4>(ev_at + 4 * 16 * (2 * P + h));
+                    const int U = PACK ? P : 2 * P + h;
+#pragma unroll
+                    for (int i = 0; i < 4; i++) sc[U][i] = __builtin_fmaf(z[h][i], factor, e[i]);
+                }
             }
             // the values' codes take the keys' registers and arrive during the softmax
 #pragma unroll
@@ -666,12 +702,12 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
         fetch_pages(seg + 2);
 
         // join the waves' parts of the segment, then the segment to the state
+        wave_sync();  // the sums take the place of the scales
         if (lane < ROWS) {
-            s_r[wave][n] = r;
-            s_l[wave][n] = l;
+            s_r[n][wave] = r;
+            s_l[n][wave] = l;
         }
-        bool has[WAVES];
-        float sr = NO_KEY, sl = 0.0f;
+        f4 rw, lw;
         Join jw[WAVES], jn{1.0f, 0.0f};
 #pragma unroll
         for (int b0 = 0; b0 < NB; b0 += NBP) {
@@ -680,61 +716,61 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 3 : 2) void k_attn(AttnArgs a
 #pragma unroll
                 for (int bb = 0; bb < nbp; bb++) {
                     const f4 x = o[2 * (b0 + bb)], y = o[2 * (b0 + bb) + 1];
-                    float* to = &s_o[wave][n * LD + 32 * bb + 8 * g];
+                    float* to = &s_own[wave].o[n * LD + 32 * bb + 8 * g];
                     *reinterpret_cast<f4*>(to) = f4{x[0], y[0], x[1], y[1]};
                     *reinterpret_cast<f4*>(to + 4) = f4{x[2], y[2], x[3], y[3]};
                 }
             }
             __syncthreads();
+            // without branches, so that all reads are in flight at once; a run without keys for the
+            // row has the factors 1 and 0 or 1, and -0 in the place of its sums adds nothing at all
+            const int per = 32 * nbp / PER_ROW, o0 = 32 * b0 / PER_ROW;
+            float part[WAVES][32 * NBP / PER_ROW], v[32 * NBP / PER_ROW];
             if (b0 == 0) {
+                rw = *reinterpret_cast<const f4*>(s_r[jr]);
+                lw = *reinterpret_cast<const f4*>(s_l[jr]);
+            }
+#pragma unroll
+            for (int w = 0; w < WAVES; w++)
+#pragma unroll
+                for (int i = 0; i < per; i++) part[w][i] = s_own[w].o[jr * LD + jp * per + i];
+            __builtin_amdgcn_sched_barrier(0);
+            if (b0 == 0) {
+                float sr = NO_KEY, sl = 0.0f;
 #pragma unroll
                 for (int w = 0; w < WAVES; w++) {
-                    const float rw = s_r[w][jr];
-                    has[w] = rw != NO_KEY;
-                    if (has[w]) {
-                        jw[w] = join(sr, rw);
-                        sl = joined(sl, s_l[w][jr], jw[w]);
-                    }
+                    jw[w] = join(sr, rw[w]);
+                    sl = joined(sl, lw[w], jw[w]);
                 }
                 if (plan.splits == 1) {
                     jn = join(RR, sr);
                     L = joined(L, sl, jn);
+                } else if (jp == 0 && first + jr < rows) {
+                    float* rl = part_rl(a, row_of(jr), plan.segs, seg);
+                    rl[0] = sr;
+                    rl[1] = sl;
                 }
             }
-            const int per = 32 * nbp / PER_ROW, o0 = 32 * b0 / PER_ROW;
-            float v[32 * NBP / PER_ROW];
 #pragma unroll
             for (int i = 0; i < per; i++) v[i] = 0.0f;
 #pragma unroll
             for (int w = 0; w < WAVES; w++)
-                if (has[w]) {
 #pragma unroll
-                    for (int i = 0; i < per; i++) v[i] = joined(v[i], s_o[w][jr * LD + jp * per + i], jw[w]);
-                }
+                for (int i = 0; i < per; i++)
+                    v[i] = joined(v[i], rw[w] != NO_KEY ? part[w][i] : -0.0f, jw[w]);
             if (plan.splits == 1) {
 #pragma unroll
                 for (int i = 0; i < per; i++) O[o0 + i] = joined(O[o0 + i], v[i], jn);
-            } else {
-                const int rr = first + jr;
-                if (rr < rows) {
-                    const int64_t row = (int64_t)(s.q0 + rr / G) * a.Hq + head * G + rr % G;
-                    float* to = part_o(a, row, plan.segs, seg) + 32 * b0 + jp * per;
+            } else if (first + jr < rows) {
+                float* to = part_o(a, row_of(jr), plan.segs, seg) + 32 * b0 + jp * per;
 #pragma unroll
-                    for (int i = 0; i < per; i++) to[i] = v[i];
-                    if (b0 == 0 && jp == 0) {
-                        float* rl = part_rl(a, row, plan.segs, seg);
-                        rl[0] = sr;
-                        rl[1] = sl;
-                    }
-                }
+                for (int i = 0; i < per; i++) to[i] = v[i];
             }
             __syncthreads();
         }
     }
-    if (plan.splits > 1) return;
-    const int rr = first + jr;
-    if (rr >= rows) return;
-    float* out = a.out + ((int64_t)(s.q0 + rr / G) * a.Hq + head * G + rr % G) * D;
+    if (plan.splits > 1 || first + jr >= rows) return;
+    float* out = a.out + row_of(jr) * D;
 #pragma unroll
     for (int b0 = 0; b0 < NB; b0 += NBP) {
         const int per = 32 * (NB - b0 < NBP ? NB - b0 : NBP) / PER_ROW, o0 = 32 * b0 / PER_ROW;
@@ -1160,17 +1196,17 @@ Plan plan_of(bool one, int64_t T, int64_t B, int Hq, int Hkv, int nb, int64_t ma
     // Packed tiles of 8 rows where the sequences of a call have that few per key/value head on
     // average; 64 rows a workgroup where that many fill them and there are four per CU, as long
     // and short ones have to even out (a 2048-token prompt with a window of 1024, 32 heads on 8:
-    // 120 us, 182 in tiles of 16; four chunks of 256 tokens on prefixes of up to 3750, with half as
-    // many workgroups, 206 against 171); else tiles of 16.
+    // 118 us, 168 in tiles of 16; four chunks of 256 tokens on prefixes of up to 3750, with half as
+    // many workgroups, 201 against 172); else tiles of 16.
     p.pack = nb <= 4 && (one ? G <= 8 : T * G <= 8 * B);
     p.wide = nb <= 4 && !one && T * G >= 64 * B && (T * G / 64 + B) * Hkv >= 1024;
     const int64_t tr = p.wide ? 64 : p.pack ? 8 : 16;
     p.tiles = (int32_t)(one ? B * ((G + tr - 1) / tr) : T * G / tr + B);
     p.segs = (int32_t)((max_len + seg_of(nb) - 1) / seg_of(nb));
-    // One sequence: as many workgroups as run at once (two per CU), each with several segments,
-    // so that the loads ahead work and the prologue is paid once (131072 positions, 32 heads on 8: 42
-    // us, and 44 with twice as many).  Several sequences differ in length: four times as many, which
-    // even out (32 of 301..8191: 60 us, and 68 with as many as for one).
+    // One sequence: two workgroups per CU, all of which run at once, each with several segments, so
+    // that the loads ahead work and the prologue is paid once (131072 positions, 32 heads on 8: 42 us,
+    // and 44 with three or four per CU).  Several sequences differ in length: four times as many, which
+    // even out (32 of 301..8191: 54 us, and 68 with as many as for one).
     const int64_t groups = (int64_t)p.tiles * Hkv, want = B == 1 ? 512 : 2048;
     int64_t splits = groups >= 512 ? 1 : (want + groups - 1) / groups;
     if (splits > p.segs) splits = p.segs;
