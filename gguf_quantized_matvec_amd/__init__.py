@@ -605,6 +605,14 @@ def _on(t, dtype, what, device):
     raise ValueError(f"{what} must be on {device}, got {t.device}")
 
 
+def _new(t, like, shape, dtype, what):
+    """(t, its address); a new tensor on like's device if t is None."""
+    if t is not None:
+        return t, _on(t, dtype, what, like.device)
+    t = like.new_empty(shape, dtype=dtype)
+    return t, t.data_ptr()
+
+
 def _add_rmsnorm(q8k, x, w, eps, res, h, y, xq, stream):
     import torch
     f32 = torch.float32
@@ -627,11 +635,10 @@ def _add_rmsnorm(q8k, x, w, eps, res, h, y, xq, stream):
     yp = None if y is None else _on(y, f32, "y", dev)
 
     def call(s):
-        q = torch.empty(n, dtype=torch.uint8, device=dev) if xq is None else xq
-        out = torch.empty(x.shape, dtype=f32, device=dev) if h is None and res is not None else h
+        q, qp = _new(xq, x, n, torch.uint8, "xq")
+        out, hp = (None, None) if res is None else _new(h, x, x.shape, f32, "h")
         (qmv_add_rmsnorm_q8_k if q8k else qmv_add_rmsnorm_q8_0)(
-            xp, rp, wp, eps, rows, K, None if out is None else _on(out, f32, "h", dev), yp,
-            _on(q, torch.uint8, "xq", dev), s)
+            xp, rp, wp, eps, rows, K, hp, yp, qp, s)
         return out, q
 
     return _on_device(dev, stream, call)
@@ -748,9 +755,8 @@ def kv_append(cache: KVCache, batch: KVBatch, q, k, v, freq=None, halves: bool =
         rot, fp = 2 * freq.numel(), _on(freq, torch.float64, "freq", dev)
 
     def call(s):
-        out = torch.empty(q.shape, dtype=torch.float32, device=dev) if q_out is None else q_out
-        qmv_kv_append(cache.c, batch.c, qp, qs, heads, kp, ks, vp, vs, fp, rot, int(halves),
-                      _on(out, torch.float32, "q_out", dev), s)
+        out, op = _new(q_out, q, q.shape, torch.float32, "q_out")
+        qmv_kv_append(cache.c, batch.c, qp, qs, heads, kp, ks, vp, vs, fp, rot, int(halves), op, s)
         return out
 
     return _on_device(dev, stream, call)
@@ -766,10 +772,9 @@ def kv_read(cache: KVCache, batch: KVBatch, k=None, v=None, stream=None):
             raise ValueError(f"{what} must be {shape}, got {tuple(t.shape)}")
 
     def call(s):
-        ko = torch.empty(shape, dtype=torch.float32, device=dev) if k is None else k
-        vo = torch.empty(shape, dtype=torch.float32, device=dev) if v is None else v
-        qmv_kv_read(cache.c, batch.c, _on(ko, torch.float32, "k", dev),
-                    _on(vo, torch.float32, "v", dev), s)
+        ko, kp = _new(k, cache.pages, shape, torch.float32, "k")
+        vo, vp = _new(v, cache.pages, shape, torch.float32, "v")
+        qmv_kv_read(cache.c, batch.c, kp, vp, s)
         return ko, vo
 
     return _on_device(dev, stream, call)
@@ -790,10 +795,9 @@ def kv_attention(cache: KVCache, batch: KVBatch, q, scale: float, window: int = 
         raise ValueError(f"work must hold {n} bytes, got {work.numel()}")
 
     def call(s):
-        o = torch.empty(q.shape, dtype=torch.float32, device=dev) if out is None else out
-        ws = torch.empty(max(n, 16), dtype=torch.uint8, device=dev) if work is None else work
-        qmv_kv_attention(cache.c, batch.c, qp, qs, heads, scale, window,
-                         _on(o, torch.float32, "out", dev), _on(ws, torch.uint8, "work", dev), s)
+        o, op = _new(out, q, q.shape, torch.float32, "out")
+        ws, wp = _new(work, q, max(n, 16), torch.uint8, "work")
+        qmv_kv_attention(cache.c, batch.c, qp, qs, heads, scale, window, op, wp, s)
         return o
 
     return _on_device(dev, stream, call)
