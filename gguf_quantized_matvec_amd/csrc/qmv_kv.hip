@@ -33,8 +33,11 @@ namespace {
 // to a rounding border decides a 4-bit code), rounded once to f32.
 //
 // A thread needs its elements' partners: within its 8 when pairs are adjacent,
-// 8 others when they are halves apart, loaded a second time.  VEC: 16-byte loads
-// and stores (aligned rows, partners in whole eights).
+// 8 others when they are halves apart (HALVES), loaded a second time.  VEC:
+// 16-byte loads and stores (aligned rows, partners in whole eights).
+// Bound by its bytes: 4117 rows of 32 heads on 8 of 128 elements, 178 MB, take 43
+// us (4.1 TB/s; a copy reaches 5.2), 45 and 55 with a row's heads on two and three
+// workgroups; more waves a SIMD do not help.
 template <bool VEC>
 __device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
     if constexpr (VEC) {
@@ -81,7 +84,7 @@ __device__ __forceinline__ _Float16 quantise8(const float (&x)[8], int g, uint32
     return bad ? (_Float16)__builtin_nanf("") : (_Float16)d;
 }
 
-template <bool VEC>
+template <bool VEC, bool HALVES>
 __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a, int passes) {
     const KvArgs& kv = a.kv;
     __shared__ double turn[2][128];
@@ -91,7 +94,7 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a, int passes) {
     const int units = a.Hq + 2 * kv.Hkv;
     const int half = a.rot >> 1;
     int apart = 0;
-    if (a.halves && 8 * w < a.rot) apart = 8 * w < half ? half : -half;
+    if (HALVES && 8 * w < a.rot) apart = 8 * w < half ? half : -half;
     // a pass's elements and their partners, loaded a pass ahead, and the first before anything else
     float x[8], p[8];
     const auto fetch = [&](int pass) {
@@ -102,7 +105,7 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a, int passes) {
                          : is_v ? a.v + (int64_t)t * a.v_stride + (int64_t)(u - a.Hq - kv.Hkv) * D
                                 : a.k + (int64_t)t * a.k_stride + (int64_t)(u - a.Hq) * D;
         load8<VEC>(src + 8 * w, x);
-        if (a.halves && !is_v) {
+        if (HALVES && !is_v) {
             if constexpr (VEC) {
                 load8<true>(src + 8 * w + apart, p);
             } else {
@@ -129,14 +132,16 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a, int passes) {
     const int page = page_of(kv, b, pos);
     __syncthreads();
     const int bb = w >> 2, g = w & 3;
-    double c[8], n[8];  // y[e] = x[e] c[e] + partner[e] n[e]
+    // y[e] = x[e] c + partner[e] (-s or s); adjacent pairs share c and s
+    constexpr int TURNS = HALVES ? 8 : 4;
+    double c[TURNS], sn[TURNS];
 #pragma unroll
-    for (int e = 0; e < 8; e++) {
-        const int i = 8 * w + e;
-        const int j = a.halves ? (i < half ? i : i - half) : i >> 1;
-        const bool turned = i < a.rot, second = a.halves ? i >= half : i & 1;
-        c[e] = turned ? turn[0][j] : 1.0;
-        n[e] = turned ? (second ? turn[1][j] : -turn[1][j]) : 0.0;
+    for (int k = 0; k < TURNS; k++) {
+        const int i = 8 * w + (HALVES ? k : 2 * k);
+        const int j = HALVES ? (i < half ? i : i - half) : i >> 1;
+        const bool turned = i < a.rot;
+        c[k] = turned ? turn[0][j] : 1.0;
+        sn[k] = turned ? (HALVES && i < half ? -turn[1][j] : turn[1][j]) : 0.0;
     }
     const int off = pos & ((1 << kv.log2p) - 1);
     const int64_t page_codes = (int64_t)(16 * kv.nb) << kv.log2p;
@@ -147,11 +152,13 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a, int passes) {
         float y[8];
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-            const float q = a.halves ? p[e] : x[e ^ 1];
-            y[e] = is_v || 8 * w + e >= a.rot ? x[e] : (float)((double)x[e] * c[e] + (double)q * n[e]);
+            const float q = HALVES ? p[e] : x[e ^ 1];
+            const int k = HALVES ? e : e >> 1;
+            const double s = HALVES || (e & 1) ? sn[k] : -sn[k];
+            y[e] = is_v || 8 * w + e >= a.rot ? x[e] : (float)((double)x[e] * c[k] + (double)q * s);
         }
         fetch(pass + 1);
-        if (a.halves) __syncthreads();  // q in place: partners are read before any is written
+        if constexpr (HALVES) __syncthreads();  // q in place: partners are read before any is written
         if (live && is_q) {
             float* dst = a.q_out + ((int64_t)t * a.Hq + u) * D + 8 * w;
             if constexpr (VEC) {
@@ -233,8 +240,9 @@ int launch_kv_append(const AppendArgs& a, hipStream_t s) {
                      (a.q_stride | a.k_stride | a.v_stride) % 4 == 0 &&
                      (!a.halves || a.rot % 16 == 0);
     const dim3 grid((unsigned)a.kv.T, (unsigned)((all + passes - 1) / passes));
-    if (vec) hipLaunchKernelGGL(k_kv_append<true>, grid, dim3(256), 0, s, a, passes);
-    else hipLaunchKernelGGL(k_kv_append<false>, grid, dim3(256), 0, s, a, passes);
+    const auto kernel = a.halves ? vec ? k_kv_append<true, true> : k_kv_append<false, true>
+                                 : vec ? k_kv_append<true, false> : k_kv_append<false, false>;
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a, passes);
     return (int)hipGetLastError();
 }
 
