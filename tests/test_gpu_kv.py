@@ -533,3 +533,102 @@ def test_many_rows_see_nan_where_it_is(g):
     got = g.kv_attention(g.KVCache(dev(raw), page, h, d), c.batch(g), q, 0.125, window=100)
     assert torch.equal(got[:300], clean[:300]) and torch.equal(got[400:], clean[400:])
     assert torch.all(torch.isnan(got[300:400]))
+
+
+@pytest.mark.parametrize("d,rot,halves,extra", [(64, 64, False, 1), (64, 64, True, 3), (96, 24, True, 4), (128, 72, True, 2),
+                                                (256, 6, False, 1), (32, 32, True, 1)])
+def test_append_rows_of_any_alignment(g, d, rot, halves, extra):
+    """Rows that start anywhere (no 16-byte loads) and rotations that end inside eight elements."""
+    hq, hkv, page, n = 6, 3, 16, 21
+    c = Case([n + 4], [n], page, hkv, d, 21)
+    width = (hq + 2 * hkv) * d + extra
+    both = dev(c.rng.standard_normal((n, width)).astype(np.float32))
+    q, k, v = both[:, :hq * d], both[:, hq * d:(hq + hkv) * d], both[:, (hq + hkv) * d:(hq + 2 * hkv) * d]
+    freq = 10000.0 ** (-np.arange(0, rot, 2) / rot)
+    cache = g.KVCache(None, page, hkv, d, n_pages=c.n_pages)
+    out = g.kv_append(cache, c.batch(g), q, k, v, dev(freq), halves=halves)
+    rk, rv = (x.cpu().numpy().reshape(n, hkv, d) for x in g.kv_read(cache, c.batch(g)))
+    q64, k64 = (rotate(x.cpu().numpy().reshape(n, -1, d), c.pos, freq, halves) for x in (q, k))
+    # one rounding to f32 of sums of two f64 products of values below 8
+    assert np.all(np.abs(out.cpu().numpy().reshape(q64.shape) - q64) <= 2.0 ** -24 * np.abs(q64) + 2.0 ** -47)
+    assert np.array_equal(rk, q4_value(*q4_0(k64.astype(np.float32))).astype(np.float32))
+    assert np.array_equal(rv, q4_value(*q4_0(v.cpu().numpy().reshape(n, hkv, d))).astype(np.float32))
+
+
+@pytest.mark.parametrize("halves", [False, True])
+def test_append_in_place_of_many_rows(g, halves):
+    """Rows enough for a workgroup to take all heads of one, with q rotated where it stands: as in
+    calls of few rows into another tensor."""
+    hq, hkv, d, page, n = 32, 8, 128, 64, 700
+    rng = np.random.default_rng(22)
+    q, k, v = (dev(rng.standard_normal((n, h * d)).astype(np.float32)) for h in (hq, hkv, hkv))
+    freq, table = dev(10000.0 ** (-np.arange(0, d, 2) / d)), dev(rng.permutation(11).reshape(1, 11).astype(np.int32))
+    few = g.KVCache(torch.zeros(11 * hkv * page * 144, dtype=torch.uint8, device="cuda"), page, hkv, d)
+    many = g.KVCache(torch.zeros_like(few.pages), page, hkv, d)
+
+    def batch(lo, hi):
+        return g.KVBatch(table, dev(np.array([hi], np.int32)), dev(np.array([0, hi - lo], np.int32)), hi - lo, 704)
+
+    parts = [g.kv_append(few, batch(i, i + 100), q[i:i + 100], k[i:i + 100], v[i:i + 100], freq, halves=halves)
+             for i in range(0, n, 100)]
+    assert g.kv_append(many, batch(0, n), q, k, v, freq, halves=halves, q_out=q) is q
+    assert torch.equal(q, torch.cat(parts)) and torch.equal(few.pages, many.pages)
+
+
+def test_many_sequences(g):
+    """More sequences than a wave looks at a time, some without rows, in one call: each as alone;
+    q as a part of wider rows."""
+    hq, hkv, d, page, B = 6, 2, 64, 16, 200
+    rng = np.random.default_rng(23)
+    ns = [int(x) for x in rng.choice([0, 1, 1, 2, 5, 19], B)]
+    lens = [n + int(x) for n, x in zip(ns, rng.choice([0, 3, 15, 40, 530], B))]
+    c = Case(lens, ns, page, hkv, d, 24, spare_rows=2)
+    raw, ks, vs = filled(c, hq)
+    wide = dev((1.5 * c.rng.standard_normal((c.T, hq * d + 8))).astype(np.float32))
+    q = wide[:, 4:4 + hq * d]
+    cache = g.KVCache(dev(raw), page, hkv, d)
+    out = torch.full((c.T, hq * d), 7.0, device="cuda")
+    g.kv_attention(cache, c.batch(g), q, 0.125, out=out)
+    assert torch.all(out[c.rows:] == 7.0)
+    check(c, out.cpu().numpy(), q.cpu().numpy(), ks, vs, hq, 0.125, 0)
+    k, v = (dev(c.rng.standard_normal((c.T, hkv * d)).astype(np.float32)) for _ in range(2))
+    qr = torch.full((c.T, hq * d), 7.0, device="cuda")
+    g.kv_append(cache, c.batch(g), q, k, v, q_out=qr)
+    assert torch.equal(qr[:c.rows], q[:c.rows]) and torch.all(qr[c.rows:] == 7.0)
+    rk, rv = g.kv_read(cache, c.batch(g))
+    assert np.array_equal(rk[:c.rows].cpu().numpy(), q4_value(*q4_0(k[:c.rows].cpu().numpy())).astype(np.float32))
+    assert np.array_equal(rv[:c.rows].cpu().numpy(), q4_value(*q4_0(v[:c.rows].cpu().numpy())).astype(np.float32))
+
+
+def test_capture_of_a_long_prompt(g):
+    """64 rows a workgroup, captured; tables and starts change between the replays, and two calls run
+    at once on two streams, each with a workspace of its own."""
+    h, d, page, n = 64, 64, 32, 512
+    c = Case([n, n], [n, n], page, h, d, 25)
+    raw, _, _ = filled(c, h)
+    cache = g.KVCache(dev(raw), page, h, d)
+    q = dev(c.rng.standard_normal((c.T, h * d)).astype(np.float32))
+    table, lens, starts = dev(c.table), dev(np.array(c.lens, np.int32)), dev(c.starts)
+    batch = g.KVBatch(table, lens, starts, c.T, n)
+    out = torch.empty_like(q)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        g.kv_attention(cache, batch, q, 0.125, out=out)
+    one = g.KVBatch(table[:1].contiguous(), lens[:1].contiguous(), max_len=n)
+    side = torch.cuda.Stream()
+    for step in range(6):
+        starts.copy_(dev(np.array([0, 512 - 70 * step, 1024 - 100 * step], np.int32)))
+        lens.copy_(dev(np.array([512 - step, 512], np.int32)))
+        out.fill_(7.0)
+        want = torch.full_like(q, 7.0)
+        side.wait_stream(torch.cuda.current_stream())
+        graph.replay()
+        g.kv_attention(cache, batch, q, 0.125, out=want, stream=side)
+        with torch.cuda.stream(side):
+            again = g.kv_attention(cache, one, q[:1].contiguous(), 0.125)
+        torch.cuda.current_stream().wait_stream(side)
+        if step % 2:
+            torch.cuda.synchronize()
+        assert torch.equal(out, want), step
+        assert torch.equal(again, g.kv_attention(cache, one, q[:1].contiguous(), 0.125)), step
