@@ -605,11 +605,16 @@ def _on(t, dtype, what, device):
     raise ValueError(f"{what} must be on {device}, got {t.device}")
 
 
-def _new(t, like, shape, dtype, what):
-    """(t, its address); a new tensor on like's device if t is None."""
+def _new(t, like, dtype, what, shape=None):
+    """(t, its address); if t is None a new tensor on like's device, of like's shape and type or
+    of the given ones."""
+    import torch
     if t is not None:
         return t, _on(t, dtype, what, like.device)
-    t = like.new_empty(shape, dtype=dtype)
+    if shape is None:
+        t = torch.empty_like(like, memory_format=torch.contiguous_format)
+    else:
+        t = like.new_empty(shape, dtype=dtype)
     return t, t.data_ptr()
 
 
@@ -635,8 +640,8 @@ def _add_rmsnorm(q8k, x, w, eps, res, h, y, xq, stream):
     yp = None if y is None else _on(y, f32, "y", dev)
 
     def call(s):
-        q, qp = _new(xq, x, n, torch.uint8, "xq")
-        out, hp = (None, None) if res is None else _new(h, x, x.shape, f32, "h")
+        q, qp = _new(xq, x, torch.uint8, "xq", n)
+        out, hp = (None, None) if res is None else _new(h, x, f32, "h")
         (qmv_add_rmsnorm_q8_k if q8k else qmv_add_rmsnorm_q8_0)(
             xp, rp, wp, eps, rows, K, hp, yp, qp, s)
         return out, q
@@ -755,7 +760,7 @@ def kv_append(cache: KVCache, batch: KVBatch, q, k, v, freq=None, halves: bool =
         rot, fp = 2 * freq.numel(), _on(freq, torch.float64, "freq", dev)
 
     def call(s):
-        out, op = _new(q_out, q, q.shape, torch.float32, "q_out")
+        out, op = _new(q_out, q, torch.float32, "q_out")
         qmv_kv_append(cache.c, batch.c, qp, qs, heads, kp, ks, vp, vs, fp, rot, int(halves), op, s)
         return out
 
@@ -772,8 +777,8 @@ def kv_read(cache: KVCache, batch: KVBatch, k=None, v=None, stream=None):
             raise ValueError(f"{what} must be {shape}, got {tuple(t.shape)}")
 
     def call(s):
-        ko, kp = _new(k, cache.pages, shape, torch.float32, "k")
-        vo, vp = _new(v, cache.pages, shape, torch.float32, "v")
+        ko, kp = _new(k, cache.pages, torch.float32, "k", shape)
+        vo, vp = _new(v, ko, torch.float32, "v")
         qmv_kv_read(cache.c, batch.c, kp, vp, s)
         return ko, vo
 
@@ -795,8 +800,8 @@ def kv_attention(cache: KVCache, batch: KVBatch, q, scale: float, window: int = 
         raise ValueError(f"work must hold {n} bytes, got {work.numel()}")
 
     def call(s):
-        o, op = _new(out, q, q.shape, torch.float32, "out")
-        ws, wp = _new(work, q, max(n, 16), torch.uint8, "work")
+        o, op = _new(out, q, torch.float32, "out")
+        ws, wp = _new(work, q, torch.uint8, "work", n)
         qmv_kv_attention(cache.c, batch.c, qp, qs, heads, scale, window, op, wp, s)
         return o
 
