@@ -113,9 +113,6 @@ __device__ __forceinline__ _Float16 half_of(uint32_t w, int i) {
     return h;
 }
 
-// p0 d0 and p1 d1, each as the sum of two f16 numbers: what the first leaves is
-// exact in the fma and rounded once more.  (The empty asm statements keep
-// each number one v_fma_mixlo or v_fma_mixhi.)
 __device__ __forceinline__ half2v halves(uint32_t w) {
     half2v h;
     __builtin_memcpy(&h, &w, 4);
