@@ -297,7 +297,8 @@ __device__ __forceinline__ void stage_key_scales(Words<NB> dk, int live, int lan
     keep_live<NB>(dk, live);
 #pragma unroll
     for (int i = 0; i < NB; i++)
-        to[i][lane] = half_bits(dk.w[i >> 1], i & 1) | half_bits(dk.w[(NB + i) >> 1], (NB + i) & 1) << 16;
+        to[i][lane] = __builtin_amdgcn_perm(dk.w[(NB + i) >> 1], dk.w[i >> 1],
+                                            ((NB + i) & 1 ? 0x07060000u : 0x05040000u) | (i & 1 ? 0x0302u : 0x0100u));
 }
 // The exponent that bounds the largest scale of a position's values, max_b |dv|
 // < 2^ev.  A position with an infinite or NaN scale gets ev = inf, which turns
@@ -336,6 +337,8 @@ __device__ __forceinline__ void stage_value_scales(Words<NB> dv, int live, int l
                                                    uint32_t (*to)[sub_of(NB) / 2], float* down) {
     keep_live<NB>(dv, live);
     const Sizes z = sizes_of<NB>(dv);
+    // bytes 0..3 are the lane's own, 4..7 the other's: even lanes take both low halves
+    const uint32_t pick = lane & 1 ? 0x03020706u : 0x05040100u;
     float f[2];
 #pragma unroll
     for (int i = 0; i < 2; i++) {
@@ -349,8 +352,8 @@ __device__ __forceinline__ void stage_value_scales(Words<NB> dv, int live, int l
         v[1] = z.bad[1] ? (_Float16)0.0f : (_Float16)((float)v[1] * f[1]);
         // the lanes of positions 0, 1 and 2, 3 exchange to words of positions 0, 2 and 1, 3, the
         // order of the code words
-        const uint32_t own = word(v), other = dpp_bits<DPP_XOR1>(own);
-        to[i][lane] = lane & 1 ? (other >> 16) | (own & 0xFFFF0000u) : (own & 0xFFFFu) | (other << 16);
+        const uint32_t own = word(v);
+        to[i][lane] = __builtin_amdgcn_perm(dpp_bits<DPP_XOR1>(own), own, pick);
     }
 }
 
@@ -362,11 +365,11 @@ __device__ __forceinline__ void stage_value_scales(Words<NB> dv, int live, int l
 // tiles, move across, and go on over the odd tiles, which is the order of the
 // sums in every variant.
 //
-// What bounds it: with few rows the loads' latency and the VALU, 58 % busy (131072 positions, 42 us,
-// 3.6 TB/s), with many the VALU (about 1700 instructions a wave and run, a third of them unpacking,
-// beside 128 matrix instructions: 75 % busy on four chunks of 256 tokens, 170 us).  So three waves a
+// What bounds it: with few rows the loads' latency and the VALU, 58 % busy (131072 positions, 41 us,
+// 3.7 TB/s), with many the VALU (about 1700 instructions a wave and run, a third of them unpacking,
+// beside 128 matrix instructions: 75 % busy on four chunks of 256 tokens, 164 us).  So three waves a
 // SIMD: the rows' two parts, the same for the four waves, wait in LDS, and a wave's sums take the
-// place of its scales (32 sequences of 301..8191: 54 us, 60 with the rows in registers, two waves).
+// place of its scales (32 sequences of 301..8191: 53 us, 60 with the rows in registers, two waves).
 template <int NB, bool PACK>
 __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void k_attn(AttnArgs a, Plan plan) {
     const KvArgs& kv = a.kv;
@@ -460,9 +463,13 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void k_attn(AttnArgs a
         dv = load_words<NB>(hd + ((int64_t)(2 * NB) << kv.log2p));
         lane_k = works(seg) ? (lane & 15) * (16 * NB) + g * (4 * NB) : 0;
     };
+    // (an offset that is seen to be 32 bits wide where it is used stays beside the tile's address, which
+    // all lanes share, in the load; otherwise every load adds the two first)
     const auto fetch_keys = [&] {
+        uint32_t off = lane_k;
+        asm("" : "+v"(off));
 #pragma unroll
-        for (int u = 0; u < TILES; u++) cw[u] = load_words<NB>(tile_codes(u) + lane_k);
+        for (int u = 0; u < TILES; u++) cw[u] = load_words<NB>(tile_codes(u) + off);
     };
     fetch_pages(seg0);
 
@@ -538,6 +545,16 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void k_attn(AttnArgs a
 #pragma unroll
             for (int P = 0; P < TILES / 2; P++) {
                 f4 z[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+                f4 accp[2];  // a step's results are used in the next one, behind its products
+                u2 dp[2];
+                const auto take = [&] {
+#pragma unroll
+                    for (int h = 0; h < (PACK ? 1 : 2); h++)
+#pragma unroll
+                        for (int i = 0; i < 4; i++)
+                            z[h][i] = __builtin_fmaf((float)half_of(dp[h][i >> 1], i & 1),
+                                                     PACK && par ? accp[1][i] : accp[h][i], z[h][i]);
+                };
 #pragma unroll
                 for (int bb = 0; bb < NB; bb++) {
                     const half8 qh = qhn, ql = qln;
@@ -545,23 +562,27 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void k_attn(AttnArgs a
                     if (bb + 1 < NB) ahead(P, bb + 1);
                     else if (P + 1 < TILES / 2) ahead(P + 1, 0);
                     __builtin_amdgcn_sched_barrier(0);
-                    f4 acc[2];
+                    half8 ko[2];
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
                         const uint32_t w = cw[2 * P + h].w[bb], v = w >> 8;
-                        const half8 ko =
-                            operand(unpack.low(w), unpack.high(w), unpack.low(v), unpack.high(v));
-                        acc[h] = mfma(ko, ql, f4{0, 0, 0, 0});
-                        acc[h] = mfma(ko, qh, acc[h]);
+                        ko[h] = operand(unpack.low(w), unpack.high(w), unpack.low(v), unpack.high(v));
                     }
+                    __builtin_amdgcn_sched_barrier(0);
+                    f4 acc[2];
 #pragma unroll
-                    for (int h = 0; h < (PACK ? 1 : 2); h++)
+                    for (int h = 0; h < 2; h++) acc[h] = mfma(ko[h], ql, f4{0, 0, 0, 0});
 #pragma unroll
-                        for (int i = 0; i < 4; i++)
-                            z[h][i] = __builtin_fmaf((float)half_of(d[h][i >> 1], i & 1),
-                                                     PACK && par ? acc[1][i] : acc[h][i], z[h][i]);
+                    for (int h = 0; h < 2; h++) acc[h] = mfma(ko[h], qh, acc[h]);
+                    if (bb) take();
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        accp[h] = acc[h];
+                        dp[h] = d[h];
+                    }
                     __builtin_amdgcn_sched_barrier(0);
                 }
+                take();
                 // in base 2, relative to the size of the position's values
 #pragma unroll
                 for (int h = 0; h < (PACK ? 1 : 2); h++) {
@@ -572,9 +593,11 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void k_attn(AttnArgs a
                 }
             }
             // the values' codes take the keys' registers and arrive during the softmax
+            uint32_t lane_v = lane * (4 * NB);
+            asm("" : "+v"(lane_v));
 #pragma unroll
             for (int u = 0; u < TILES; u++)
-                cw[u] = load_words<NB>(tile_codes(u) + codes + lane * (4 * NB));
+                cw[u] = load_words<NB>(tile_codes(u) + codes + lane_v);
 
             // weights
             if (masked) {
@@ -1194,17 +1217,17 @@ Plan plan_of(bool one, int64_t T, int64_t B, int Hq, int Hkv, int nb, int64_t ma
     // Packed tiles of 8 rows where the sequences of a call have that few per key/value head on
     // average; 64 rows a workgroup where that many fill them and there are four per CU, as long
     // and short ones have to even out (a 2048-token prompt with a window of 1024, 32 heads on 8:
-    // 118 us, 168 in tiles of 16; four chunks of 256 tokens on prefixes of up to 3750, with half as
-    // many workgroups, 201 against 170); else tiles of 16.
+    // 116 us, 168 in tiles of 16; four chunks of 256 tokens on prefixes of up to 3750, with half as
+    // many workgroups, 201 against 164); else tiles of 16.
     p.pack = nb <= 4 && (one ? G <= 8 : T * G <= 8 * B);
     p.wide = nb <= 4 && !one && T * G >= 64 * B && (T * G / 64 + B) * Hkv >= 1024;
     const int64_t tr = p.wide ? 64 : p.pack ? 8 : 16;
     p.tiles = (int32_t)(one ? B * ((G + tr - 1) / tr) : T * G / tr + B);
     p.segs = (int32_t)((max_len + seg_of(nb) - 1) / seg_of(nb));
     // One sequence: two workgroups per CU, all of which run at once, each with several segments, so
-    // that the loads ahead work and the prologue is paid once (131072 positions, 32 heads on 8: 42 us,
-    // and 44 with three or four per CU).  Several sequences differ in length: four times as many, which
-    // even out (32 of 301..8191: 54 us, and 68 with as many as for one).
+    // that the loads ahead work and the prologue is paid once (131072 positions, 32 heads on 8: 41 us,
+    // and 43 with three or four per CU).  Several sequences differ in length: four times as many, which
+    // even out (32 of 301..8191: 53 us, and 68 with as many as for one).
     const int64_t groups = (int64_t)p.tiles * Hkv, want = B == 1 ? 512 : 2048;
     int64_t splits = groups >= 512 ? 1 : (want + groups - 1) / groups;
     if (splits > p.segs) splits = p.segs;
