@@ -365,9 +365,9 @@ __device__ __forceinline__ void stage_value_scales(Words<NB> dv, int live, int l
 // tiles, move across, and go on over the odd tiles, which is the order of the
 // sums in every variant.
 //
-// What bounds it: with few rows the loads' latency and the VALU, 58 % busy (131072 positions, 41 us,
-// 3.7 TB/s), with many the VALU (about 1700 instructions a wave and run, a third of them unpacking,
-// beside 128 matrix instructions: 75 % busy on four chunks of 256 tokens, 164 us).  So three waves a
+// What bounds it: with few rows the loads' latency and the VALU, 57 % busy (131072 positions, 41 us,
+// 3.7 TB/s), with many the VALU (about 1650 instructions a wave and run, a third of them unpacking,
+// beside 128 matrix instructions: 77 % busy on four chunks of 256 tokens, 163 us).  So three waves a
 // SIMD: the rows' two parts, the same for the four waves, wait in LDS, and a wave's sums take the
 // place of its scales (32 sequences of 301..8191: 53 us, 60 with the rows in registers, two waves).
 template <int NB, bool PACK>
@@ -806,7 +806,7 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void k_attn(AttnArgs a
 // scores need) are replaced while values are worked on, and values while scores
 // are, from words loaded a run ahead; two barriers a run.  Every wave joins its
 // runs to segments and its segments to its state itself, in the steps of k_attn.
-// 250 registers, so two waves a SIMD: VALU 59 %, LDS 33 %, matrix cores 23 % busy.
+// 250 registers, so two waves a SIMD: VALU 62 %, LDS 34 %, matrix cores 24 % busy.
 template <int NB>
 __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_wide(AttnArgs a, Plan plan) {
     static_assert(sub_of(NB) == 128 && WAVES == 4, "a wave unpacks two tiles of keys and a pair of values");
@@ -1217,8 +1217,8 @@ Plan plan_of(bool one, int64_t T, int64_t B, int Hq, int Hkv, int nb, int64_t ma
     // Packed tiles of 8 rows where the sequences of a call have that few per key/value head on
     // average; 64 rows a workgroup where that many fill them and there are four per CU, as long
     // and short ones have to even out (a 2048-token prompt with a window of 1024, 32 heads on 8:
-    // 116 us, 168 in tiles of 16; four chunks of 256 tokens on prefixes of up to 3750, with half as
-    // many workgroups, 201 against 164); else tiles of 16.
+    // 114 us, 168 in tiles of 16; four chunks of 256 tokens on prefixes of up to 3750, with half as
+    // many workgroups, 201 against 163); else tiles of 16.
     p.pack = nb <= 4 && (one ? G <= 8 : T * G <= 8 * B);
     p.wide = nb <= 4 && !one && T * G >= 64 * B && (T * G / 64 + B) * Hkv >= 1024;
     const int64_t tr = p.wide ? 64 : p.pack ? 8 : 16;
