@@ -296,9 +296,14 @@ __device__ __forceinline__ void stage_key_scales(Words<NB> dk, int live, int lan
                                                  uint32_t (*to)[sub_of(NB) / 2]) {
     keep_live<NB>(dk, live);
 #pragma unroll
-    for (int i = 0; i < NB; i++)
-        to[i][lane] = __builtin_amdgcn_perm(dk.w[(NB + i) >> 1], dk.w[i >> 1],
-                                            ((NB + i) & 1 ? 0x07060000u : 0x05040000u) | (i & 1 ? 0x0302u : 0x0100u));
+    for (int i = 0; i < NB; i++) {
+        const half2v d = halves(__builtin_amdgcn_perm(
+            dk.w[(NB + i) >> 1], dk.w[i >> 1],
+            ((NB + i) & 1 ? 0x07060000u : 0x05040000u) | (i & 1 ? 0x0302u : 0x0100u)));
+        // an infinite scale becomes NaN, as it would times a code of 8 (times the block's sum it would
+        // be a score of -inf as well, a key of no weight)
+        to[i][lane] = word(__builtin_elementwise_fma(d, half2v{0, 0}, d));
+    }
 }
 // The exponent that bounds the largest scale of a position's values, max_b |dv|
 // < 2^ev.  A position with an infinite or NaN scale gets ev = inf, which turns

@@ -482,7 +482,8 @@ size_t qmv_kv_attention_bytes(int64_t T, int64_t B, int q_heads, int kv_heads, i
  * the positions it sees alone: not on the other rows, on how a prompt is cut
  * into calls, on the pages' order or on max_len.  A row that sees a position
  * with a non-finite scale, or whose q is not finite, is NaN throughout; what
- * a row does not see, uninitialised pages included, does not reach it. */
+ * a row does not see, uninitialised pages included, does not reach it.
+ * scale * q and the scores have to fit f32. */
 int qmv_kv_attention(const qmv_kv* kv, const qmv_kv_batch* seqs, const float* q, int64_t q_stride,
                      int q_heads, float scale, int64_t window, float* out, void* work,
                      void* stream);

@@ -632,3 +632,22 @@ def test_capture_of_a_long_prompt(g):
             torch.cuda.synchronize()
         assert torch.equal(out, want), step
         assert torch.equal(again, g.kv_attention(cache, one, q[:1].contiguous(), 0.125)), step
+
+
+@pytest.mark.parametrize("d,hq,hkv,n,where", [(64, 4, 2, 5, "k"), (128, 16, 1, 40, "k"), (64, 64, 64, 1000, "k"),
+                                              (64, 4, 2, 5, "v"), (128, 16, 1, 40, "v"), (160, 2, 2, 40, "k")])
+@pytest.mark.parametrize("bits", [0x7C00, 0xFC00, 0x7E00])
+def test_a_scale_that_is_not_finite(g, d, hq, hkv, n, where, bits):
+    """An infinite or NaN scale of one block of one token: the rows that see it are NaN throughout, the
+    others as without it."""
+    page, at = 32, n - 3
+    c = Case([n + 70], [n], page, hkv, d, 26)
+    raw, _, _ = filled(c, hq)
+    q = dev(c.rng.standard_normal((n, hq * d)).astype(np.float32))
+    clean = g.kv_attention(g.KVCache(dev(raw), page, hkv, d), c.batch(g), q, 0.125)
+    cells, p = c.cells(raw), 70 + at
+    byte = page * (32 if where == "k" else 34) * c.nb + ((p % page) * c.nb + c.nb - 1) * 2
+    cells[c.table[0, p // page], :, byte:byte + 2] = np.array([bits], np.uint16).view(np.uint8)
+    got = g.kv_attention(g.KVCache(dev(raw), page, hkv, d), c.batch(g), q, 0.125)
+    assert torch.equal(got[:at], clean[:at])
+    assert torch.all(torch.isnan(got[at:]))
