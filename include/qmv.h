@@ -384,8 +384,8 @@ int qmv_launch_noalloc(int type, const void* w, int64_t N, int64_t K, const floa
  * [rows][K] receives the sum and may be x or res itself.  y [rows][K], if not
  * NULL, receives y before its quantisation; it, xq and w overlap nothing
  * else.  Values that are not finite (a row of zeros with eps 0 among them) are
- * not checked, as by the quantisers.  The order of every sum depends on K alone: a row's bits do not
- * depend on the rows beside it. */
+ * not checked, as by the quantisers.  The order of every sum depends on K
+ * alone: a row's bits do not depend on the rows beside it. */
 int qmv_add_rmsnorm_q8_0(const float* x, const float* res, const float* w, float eps,
                          int64_t rows, int64_t K, float* h, float* y, void* xq, void* stream);
 int qmv_add_rmsnorm_q8_k(const float* x, const float* res, const float* w, float eps,
