@@ -24,7 +24,7 @@ EXPORTS = ("qmv_act_bytes", "quantize_act_q8_0", "qmv_launch", "qmv_launch_group
            "qmv_launch_gateup_swiglu", "qmv_launch_gateup_swiglu_q8", "qmv_act_bytes_q8k", "quantize_act_q8_k", "qmv_launch_q8k",
            "qmv_launch_gateup_swiglu_q8k", "qmv_launch_group_q8k", "qmm_launch_q8k", "qmv_partials_q8k_launch", "qmv_prepared_bytes", "qmv_prepare",
            "qmm_launch_q8k_prepared", "qmm_partials_q8k_prepared_launch", "qmv_add_rmsnorm_q8_0", "qmv_add_rmsnorm_q8_k",
-           "qmv_kv_bytes", "qmv_kv_append", "qmv_kv_read", "qmv_kv_attention_bytes", "qmv_kv_attention", "qmv_strerror")
+           "qmv_kv_bytes", "qmv_kv_append", "qmv_kv_read", "qmv_kv_attention_bytes", "qmv_kv_attention_rows", "qmv_kv_attention", "qmv_strerror")
 MAX_BATCH = 16
 MAX_GROUP = 8
 
@@ -101,13 +101,15 @@ def lib() -> ctypes.CDLL:
         L.qmv_kv_read.argtypes = [KV, KB, P, P, P]
         L.qmv_kv_attention_bytes.argtypes = [I64, I64, I, I, I, I64]
         L.qmv_kv_attention_bytes.restype = ctypes.c_size_t
+        L.qmv_kv_attention_rows.argtypes = [I64, I64, I, I, I, I, I64]
         L.qmv_kv_attention.argtypes = [KV, KB, P, I64, I, F, I64, P, P, P]
         for f in ("quantize_act_q8_0", "qmv_launch", "qmv_launch_group", "qmm_launch",
                   "qmv_partials_launch", "qmm_partials_launch", "qmv_launch_noalloc",
                   "qmv_launch_gateup_swiglu", "qmv_launch_gateup_swiglu_q8", "quantize_act_q8_k", "qmv_launch_q8k",
                   "qmv_launch_gateup_swiglu_q8k", "qmv_launch_group_q8k", "qmm_launch_q8k", "qmv_partials_q8k_launch", "qmv_prepare",
                   "qmm_launch_q8k_prepared", "qmm_partials_q8k_prepared_launch", "qmv_add_rmsnorm_q8_0",
-                  "qmv_add_rmsnorm_q8_k", "qmv_kv_append", "qmv_kv_read", "qmv_kv_attention"):
+                  "qmv_add_rmsnorm_q8_k", "qmv_kv_append", "qmv_kv_read", "qmv_kv_attention_rows",
+                  "qmv_kv_attention"):
             getattr(L, f).restype = I
         L.qmv_strerror.argtypes = [I]
         L.qmv_strerror.restype = ctypes.c_char_p
@@ -267,6 +269,11 @@ def qmv_kv_read(kv: KvStruct, seqs: KvBatchStruct, k: int, v: int, stream: int =
 def qmv_kv_attention_bytes(T: int, B: int, q_heads: int, kv_heads: int, head_dim: int,
                            max_len: int) -> int:
     return int(lib().qmv_kv_attention_bytes(T, B, q_heads, kv_heads, head_dim, max_len))
+
+
+def qmv_kv_attention_rows(T: int, B: int, starts: bool, q_heads: int, kv_heads: int, head_dim: int,
+                          max_len: int) -> int:
+    return int(lib().qmv_kv_attention_rows(T, B, int(starts), q_heads, kv_heads, head_dim, max_len))
 
 
 def qmv_kv_attention(kv: KvStruct, seqs: KvBatchStruct, q: int, q_stride: int, q_heads: int,

@@ -1285,6 +1285,11 @@ int64_t kv_attention_bytes(int64_t T, int64_t B, int Hq, int Hkv, int nb, int64_
     return split ? T * Hq * p.segs * (32 * nb + 2) * 4 : 16;
 }
 
+int kv_attention_rows(int64_t T, int64_t B, bool starts, int Hq, int Hkv, int nb, int64_t max_len) {
+    const Plan p = plan_of(!starts, T, B, Hq, Hkv, nb, max_len);
+    return p.wide ? 64 : p.pack ? 8 : 16;
+}
+
 int launch_kv_attention(const AttnArgs& a, hipStream_t s) {
     const Plan p = plan_of(!a.kv.q_start, a.kv.T, a.kv.B, a.Hq, a.kv.Hkv, a.kv.nb, a.kv.max_len);
     int rc;

@@ -51,6 +51,8 @@ int launch_kv_append(const AppendArgs& a, hipStream_t s);
 int launch_kv_read(const KvArgs& kv, float* k, float* v, hipStream_t s);
 // Bytes of work that launch_kv_attention uses for these arguments.
 int64_t kv_attention_bytes(int64_t T, int64_t B, int Hq, int Hkv, int nb, int64_t max_len);
+// Rows of a workgroup in such a call (starts: it has q_start).
+int kv_attention_rows(int64_t T, int64_t B, bool starts, int Hq, int Hkv, int nb, int64_t max_len);
 int launch_kv_attention(const AttnArgs& a, hipStream_t s);
 
 }  // namespace qmv

@@ -76,6 +76,13 @@ bool tiles_ok(int64_t T, int64_t B, int64_t q_heads, int64_t kv_heads) {
     return T * q_heads / 8 + B * kv_heads < (1 << 24);
 }
 
+bool attention_shape_ok(int64_t T, int64_t B, int q_heads, int kv_heads, int head_dim,
+                        int64_t max_len) {
+    return cache_shape_ok(1, 16, kv_heads, head_dim) && q_heads_ok(q_heads, kv_heads) && B >= 1 &&
+           B <= QMV_KV_MAX_ROWS && T >= 1 && T <= QMV_KV_MAX_ROWS && max_len >= 1 &&
+           max_len <= QMV_KV_MAX_LEN && tiles_ok(T, B, q_heads, kv_heads);
+}
+
 }  // namespace
 
 extern "C" {
@@ -136,11 +143,15 @@ int qmv_kv_read(const qmv_kv* kv, const qmv_kv_batch* seqs, float* k, float* v, 
 
 size_t qmv_kv_attention_bytes(int64_t T, int64_t B, int q_heads, int kv_heads, int head_dim,
                               int64_t max_len) {
-    if (!cache_shape_ok(1, 16, kv_heads, head_dim) || !q_heads_ok(q_heads, kv_heads) || B < 1 ||
-        B > QMV_KV_MAX_ROWS || T < 1 || T > QMV_KV_MAX_ROWS || max_len < 1 ||
-        max_len > QMV_KV_MAX_LEN || !tiles_ok(T, B, q_heads, kv_heads))
-        return 0;
+    if (!attention_shape_ok(T, B, q_heads, kv_heads, head_dim, max_len)) return 0;
     return (size_t)qmv::kv_attention_bytes(T, B, q_heads, kv_heads, head_dim / 32, max_len);
+}
+
+int qmv_kv_attention_rows(int64_t T, int64_t B, int starts, int q_heads, int kv_heads,
+                          int head_dim, int64_t max_len) {
+    if (!attention_shape_ok(T, B, q_heads, kv_heads, head_dim, max_len) || (!starts && T != B))
+        return 0;
+    return qmv::kv_attention_rows(T, B, starts != 0, q_heads, kv_heads, head_dim / 32, max_len);
 }
 
 int qmv_kv_attention(const qmv_kv* kv, const qmv_kv_batch* seqs, const float* q, int64_t q_stride,

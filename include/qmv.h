@@ -469,6 +469,12 @@ int qmv_kv_read(const qmv_kv* kv, const qmv_kv_batch* seqs, float* k, float* v, 
 size_t qmv_kv_attention_bytes(int64_t T, int64_t B, int q_heads, int kv_heads, int head_dim,
                               int64_t max_len);
 
+/* Test hook: the rows of a workgroup (8, 16 or 64) in a call of this shape,
+ * which names the kernel that it runs; 0 for an invalid shape.  starts: whether
+ * the call has q_start. */
+int qmv_kv_attention_rows(int64_t T, int64_t B, int starts, int q_heads, int kv_heads,
+                          int head_dim, int64_t max_len);
+
 /* Causal attention over the cache: for each row (at position p) and query
  * head, out = sum_t softmax_t(scale * q . k[t]) v[t] over the sequence's
  * positions t with p - window < t <= p (window 0: all t <= p); 0 for a row

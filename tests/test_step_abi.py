@@ -202,3 +202,20 @@ def test_new_pages_need_a_number():
     for n in (None, 0, -1):
         with pytest.raises(ValueError):
             g.KVCache(None, 16, 1, 32, n_pages=n)
+
+
+def test_attention_rows_of_invalid_shapes():
+    f = g.qmv_kv_attention_rows
+    for bad in [(0, 1, True, 4, 2, 64, 9), (1, 0, True, 4, 2, 64, 9), (1, 1, True, 3, 2, 64, 9), (1, 1, True, 4, 2, 48, 9),
+                (1, 1, True, 4, 2, 64, 0), (2, 1, False, 4, 2, 64, 9), (1 << 20, 1 << 20, True, 32, 32, 64, 9)]:
+        assert f(*bad) == 0
+    assert f(1, 1, False, 4, 2, 64, 9) == 8
+
+
+def test_the_choice_of_an_attention_kernel():
+    """Few rows a key/value head: 8 rows a workgroup, never for heads beyond 128 elements."""
+    rows = g.qmv_kv_attention_rows
+    assert rows(1, 1, False, 32, 8, 128, 100) == 8 and rows(1, 1, False, 32, 2, 128, 100) == 16
+    assert rows(1, 1, False, 32, 8, 160, 100) == 16 and rows(1 << 14, 1, True, 32, 8, 256, 1 << 14) == 16
+    assert rows(64, 64, True, 8, 1, 64, 100) == 8 and rows(65, 64, True, 8, 1, 64, 100) == 16
+    assert rows(2048, 1, True, 32, 8, 128, 2048) == 64 and rows(1024, 4, True, 32, 8, 128, 4096) == 16
