@@ -55,7 +55,9 @@ constexpr int WAVES = 4;
 // SIMD.  And of a segment.
 constexpr int sub_of(int nb) { return nb <= 4 ? 128 : 64; }
 constexpr int seg_of(int nb) { return WAVES * sub_of(nb); }
-constexpr float NO_KEY = -1e30f;   // reference of a row that has seen no position
+// Reference of a row that has seen no position: below every score (their size stays under 2^127), so
+// that joining a part to it never takes it for the larger.
+constexpr float NO_KEY = -3.402823466e38f;
 
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef float f4 __attribute__((ext_vector_type(4)));

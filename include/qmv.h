@@ -490,7 +490,7 @@ int qmv_kv_attention_rows(int64_t T, int64_t B, int starts, int q_heads, int kv_
  * into calls, on the pages' order or on max_len.  A row that sees a position
  * with a non-finite scale, or whose q is not finite, is NaN throughout; what
  * a row does not see, uninitialised pages included, does not reach it.
- * scale * q and the scores have to fit f32. */
+ * scale * q and the scores have to stay below 2^126 in size. */
 int qmv_kv_attention(const qmv_kv* kv, const qmv_kv_batch* seqs, const float* q, int64_t q_stride,
                      int q_heads, float scale, int64_t window, float* out, void* work,
                      void* stream);

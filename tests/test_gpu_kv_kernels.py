@@ -3,7 +3,7 @@ which kernel they run."""
 import numpy as np
 import pytest
 
-from step_ref import attention
+from step_ref import attention, encode_page, q4_0, q4_value
 from test_gpu_kv import Case, bound, dev, filled
 
 pytestmark = pytest.mark.gpu
@@ -75,3 +75,73 @@ def test_64_rows_a_workgroup(g, d, hq, hkv, window):
         sees &= c.pos < 400 + window
     sees = torch.from_numpy(sees).cuda()
     assert torch.all(torch.isnan(got[:c.rows][sees])) and torch.equal(got[:c.rows][~sees], out[:c.rows][~sees])
+
+
+# a shape of every kernel: lens, rows of each, page, q heads, kv heads, d, rows a workgroup, split over positions
+KERNELS = [
+    ([200], [1], 16, 4, 1, 64, 8, False),
+    ([2000], [1], 16, 4, 1, 128, 8, True),
+    ([90], [25], 16, 2, 1, 96, 16, False),
+    ([900], [3], 16, 16, 1, 32, 16, True),
+    ([200], [3], 32, 3, 1, 160, 16, False),
+    ([700], [2], 32, 2, 2, 256, 16, True),
+    ([530], [512], 64, 128, 128, 64, 64, False),
+]
+
+
+def shaped(g, kernel, seed):
+    """The Case of a shape, whose kernel and split are as it says."""
+    lens, ns, page, hq, hkv, d, rows, split = kernel
+    print(kernel, flush=True)
+    assert g.qmv_kv_attention_rows(sum(ns), len(ns), True, hq, hkv, d, max(lens)) == rows
+    assert (g.qmv_kv_attention_bytes(sum(ns), len(ns), hq, hkv, d, max(lens)) > 16) == split
+    return Case(lens, ns, page, hkv, d, seed), page, hq, hkv, d
+
+
+def built(c, kc, kd, vc, vd):
+    """The pages of one sequence's tokens [L, hkv, nb, 32] and scales [L, hkv, nb]; -> raw, K, V."""
+    cells = np.zeros((c.n_pages, c.hkv, c.head_bytes), np.uint8)
+    L = c.lens[0]
+    for j in range(-(-L // c.page)):
+        t = slice(j * c.page, min(L, (j + 1) * c.page))
+        pad = [(0, c.page - (t.stop - t.start))]
+        for h in range(c.hkv):
+            k, v = (np.pad(x[t, h], pad + [(0, 0)] * 2) for x in (kc, vc))
+            a, b = (np.pad(x[t, h], pad + [(0, 0)]) for x in (kd, vd))
+            cells[c.table[0, j], h] = encode_page(k, a, v, b, c.page, c.nb)
+    return cells.reshape(-1), q4_value(kc, kd), q4_value(vc, vd)
+
+
+# up to both ends of f32
+SIZES = [1e12, 1e20, 5e29, 1e30, 3e30, 1e31, 1e34, 4e37]
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_of_any_size(g, kernel, sign):
+    """Keys all alike but one, which is twice as long: with positive scores it takes all the weight,
+    with negative ones it has none and the others share it, however large the scores are.  Every
+    weight is then exact, and so is its product with a value, so that only the sums round: partial
+    sums of at most 64 terms and runs of 512 keys, each by half a step of sum p |v|."""
+    c, page, hq, hkv, d = shaped(g, kernel, 32)
+    L, n, twice = c.lens[0], c.ns[0], c.lens[0] // 3
+    k, v = c.rng.standard_normal((1, hkv, d)), c.rng.standard_normal((L, hkv, c.nb, 32))
+    kc, kd = (np.repeat(x, L, 0) for x in q4_0(k.astype(np.float32)))
+    kd[twice] *= 2
+    v = v.clip(-2.9, 2.9)
+    v[..., 7] = 3.0  # one scale for all
+    vc, vd = q4_0(v.reshape(L, hkv, d).astype(np.float32))
+    raw, ks, vs = built(c, kc, kd, vc, vd)
+    cache, batch = g.KVCache(dev(raw), page, hkv, d), c.batch(g)
+    unit = ks[0] / (ks[0] ** 2).sum(-1, keepdims=True)  # [hkv, d]: a score of 1
+    per = n * hq
+    sizes = np.resize(SIZES, -(-len(SIZES) // per) * per).reshape(-1, n, hq)
+    for size in sizes[:3] if per >= len(SIZES) else sizes:
+        q = (sign * size[..., None] * np.repeat(unit, hq // hkv, 0)).astype(np.float32)
+        got = g.kv_attention(cache, batch, dev(q.reshape(n, -1)), 1.0).cpu().numpy().reshape(n, hq, d)
+        for j in range(n):
+            seen = np.arange(c.pos[j] + 1)
+            seen = seen[seen == twice] if sign > 0 and c.pos[j] >= twice else seen[seen != twice]
+            want, mean = vs[seen].mean(0), np.abs(vs[seen]).mean(0)
+            lim = np.repeat((80 + L / 512) * 2.0 ** -24 * mean, hq // hkv, 0)
+            assert np.all(np.abs(got[j] - np.repeat(want, hq // hkv, 0)) <= lim), (j, size[j])
