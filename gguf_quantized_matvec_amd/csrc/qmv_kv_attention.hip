@@ -203,6 +203,14 @@ __device__ __forceinline__ float joined(float o, float part, Join j) {
     return __builtin_fmaf(o, j.a, part * j.b);
 }
 
+// The reference of a run of scores whose largest is top: the weights relative to it reach 2^14.  From
+// 2^25 on 14 may be no multiple of top's step, and the difference rounded to 16, whose weight is
+// beyond f16: top itself then, with weights up to 1 (scores there are steps of 4 or more apart).
+__device__ __forceinline__ float reference(float top) {
+    const float r = top > -INFINITY ? top - 14.0f : 0.0f;
+    return top - r > 15.0f ? top : r;
+}
+
 __device__ __forceinline__ float result(float o, float l) { return l == 0.0f ? 0.0f : o / l; }
 
 // The sequence b and its first row of row tile `tile` of ROWS rows; false if
@@ -627,7 +635,7 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void k_attn(AttnArgs a
                 for (int i = 0; i < 4; i++) top = fmaxf(top, sc[U][i]);
             if constexpr (PACK) top = fmaxf(top, across8(top));
             top = max_rows(top);
-            const float ref = top > -INFINITY ? top - 14.0f : 0.0f;
+            const float ref = reference(top);
             float sum[2] = {0.0f, 0.0f};  // over the even and the odd tiles
             Split p[SLOTS][2];            // positions 0, 2 and 1, 3
 #pragma unroll
@@ -1025,7 +1033,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_wide(AttnArgs a, Plan pl
 #pragma unroll
                 for (int i = 0; i < 4; i++) top = fmaxf(top, sc[u][i]);
             top = max_rows(top);
-            const float ref = top > -INFINITY ? top - 14.0f : 0.0f;
+            const float ref = reference(top);
             float sum[2] = {0.0f, 0.0f};  // over the even and the odd tiles
 #pragma unroll
             for (int u = 0; u < TILES; u++) {

@@ -112,8 +112,9 @@ def built(c, kc, kd, vc, vd):
     return cells.reshape(-1), q4_value(kc, kd), q4_value(vc, vd)
 
 
-# up to both ends of f32
-SIZES = [1e12, 1e20, 5e29, 1e30, 3e30, 1e31, 1e34, 4e37]
+# around the places where 14 is no multiple of a score's step, and up to both ends of f32
+SIZES = [x * 2.0 ** e for e in range(23, 31) for x in (1.0, 1.13, 1.37, 1.61, 1.89)] + [
+    1e12, 1e20, 5e29, 1e30, 3e30, 1e31, 1e34, 4e37]
 
 
 @pytest.mark.parametrize("kernel", KERNELS)
