@@ -35,7 +35,8 @@
 // scales as dv 2^-e: the products, which are split into two f16 numbers, then
 // fill f16's range from the top, keep 22 bits down to 2^-17 of the largest term
 // and are off by 2^-39 of it below, whatever the size of the values.  The sum
-// of the weights is that of p 2^-e, in f32.
+// of the weights is that of p 2^-e, in f32.  Blocks far below the largest of
+// their position: exact_sums.
 //
 // Built with -ffp-contract=off: every float operation is the one written.
 #include <hip/hip_runtime.h>
@@ -59,7 +60,12 @@ constexpr int seg_of(int nb) { return WAVES * sub_of(nb); }
 // that joining a part to it never takes it for the larger.
 constexpr float NO_KEY = -3.402823466e38f;
 
+// A block of values whose scale is this far below the largest of its position has its sums done
+// apart (exact_sums).
+constexpr float SMALL = 1.0f / 256;
+
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bfloat8 __attribute__((ext_vector_type(8)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 typedef float f2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u2 __attribute__((ext_vector_type(2)));
@@ -170,6 +176,110 @@ __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// The sums of values over a run for one block, from weights times scales with all their 24 bits, and
+// whether the lane's row takes them.  The products' two f16 parts lose what lies 2^-39 below the
+// largest product of all blocks, which is much of a block whose scales are far below the others':
+// a row that sees a SMALL scale of the block takes these sums instead, three bf16 numbers a weight,
+// which have f32's range.  (Where it sees none, a block keeps what is 2^-30 of its own largest
+// product.)  The choice depends on what the row sees alone, so its bits still do.
+//
+// Few models need it, if any, so it is made for few registers rather than for speed: everything is
+// loaded and the scores are computed once more, in the same steps (parts(b): the rows' two parts).
+// Calls that do not need it take 1 % longer with it, in k_attn_wide 3 %; calls that need it for one
+// block of every position 2.3 to 2.9 times as long (32 sequences of 301..8191: 133 us for 57).
+struct Exact {
+    f4 sum[2];  // even elements, odd elements
+    bool taken;
+};
+// The upper halves of two numbers' bits: bf16 numbers.
+__device__ __forceinline__ uint32_t upper(float a, float b) {
+    return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+}
+__device__ __forceinline__ uint32_t as_bf16(uint32_t w) {  // of two small whole f16 numbers
+    return upper((float)half_of(w, 0), (float)half_of(w, 1));
+}
+// At the end of a branch that few runs take, so that behind it the others wait for their own loads
+// only (4 % of k_attn_wide).
+__device__ __forceinline__ void all_arrived() { __builtin_amdgcn_s_waitcnt(0); }
+
+template <int NB, class F>
+__device__ __forceinline__ Exact exact_sums(const AttnArgs& a, const Unpack& unpack,
+                                            const int32_t* table, int len, int head, int t0, int bb,
+                                            float factor, float ref, int pos, int lane, F&& parts) {
+    constexpr int TILES = sub_of(NB) / 16;
+    const KvArgs& kv = a.kv;
+    Exact r = {};
+    bool small = false;
+    asm volatile("" : "+v"(lane));  // (nothing of this before the loop of the runs)
+    const int n = lane & 15, g = lane >> 4;
+#pragma nounroll
+    for (int t = t0; t < t0 + 16 * TILES; t += 16) {  // a tile in half of a product, zeros in the other
+        int page = t < len ? table[t >> kv.log2p] : -1;
+        const bool ok = page >= 0 && (int64_t)page < kv.n_pages;
+        page = ok ? page : 0;
+        const uint8_t* hd = head_of(kv, page, head);
+        const int off = t & ((1 << kv.log2p) - 1);
+        const int64_t codes = (int64_t)(16 * NB) << kv.log2p, scales = (int64_t)(2 * NB) << kv.log2p;
+        const Words<NB> kw = load_words<NB>(hd + (off + n) * (16 * NB) + g * (4 * NB));
+        const uint8_t* sc = hd + 2 * codes + (off + 4 * g) * (2 * NB);
+        const Words<2 * NB> dk = load_words<2 * NB>(sc);
+        f4 z = {0, 0, 0, 0};
+#pragma unroll
+        for (int b = 0; b < NB; b++) {
+            half8 qh, ql;
+            parts(b, qh, ql);
+            const uint32_t w = kw.w[b], v = w >> 8;
+            const half8 ko = operand(unpack.low(w), unpack.high(w), unpack.low(v), unpack.high(v));
+            const f4 acc = mfma(ko, qh, mfma(ko, ql, f4{0, 0, 0, 0}));
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                z[i] = __builtin_fmaf((float)half_of(dk.w[(i * NB + b) >> 1], (i * NB + b) & 1), acc[i],
+                                      z[i]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        const Words<2 * NB> dv = load_words<2 * NB>(sc + scales);
+        const uint16_t* dvb = reinterpret_cast<const uint16_t*>(sc + scales) + bb;
+        const uint32_t vw =
+            *reinterpret_cast<const uint32_t*>(hd + codes + off * (16 * NB) + lane * (4 * NB) + 4 * bb);
+        float x[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int b = 0; b < NB; b++) {
+                const uint32_t m = half_bits(dv.w[(i * NB + b) >> 1], (i * NB + b) & 1) & 0x7FFFu;
+                top = m > top ? m : top;
+            }
+            const int e = (int)(top >> 10) - 14, at = t + 4 * g + i;
+            const bool bad = top >= 0x7C00u;
+            const float down = bad ? 0.0f : __uint_as_float((uint32_t)(127 - e) << 23);
+            const float d = bad ? 0.0f : half_value(dvb[i * NB]);
+            const bool seen = ok && at <= pos && (!a.window || at > pos - a.window);
+            const float s = __builtin_fmaf(z[i], factor, bad ? INFINITY : (float)e);
+            const float p = seen ? exp2_raw(s - ref) : 0.0f;
+            small |= p > 0.0f && fabsf(d) * down < SMALL;
+            x[i] = p * down * d;
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        const uint4 ev = make_uint4(as_bf16(unpack.low(vw)), as_bf16(unpack.low(vw >> 8)), 0, 0);
+        const uint4 od = make_uint4(as_bf16(unpack.high(vw)), as_bf16(unpack.high(vw >> 8)), 0, 0);
+#pragma unroll
+        for (int m = 0; m < 3; m++) {  // 8 bits each, cut off so that what is left is exact
+            const uint4 part = make_uint4(upper(x[0], x[2]), upper(x[1], x[3]), 0, 0);
+            bfloat8 e, o, w;
+            __builtin_memcpy(&e, &ev, 16);
+            __builtin_memcpy(&o, &od, 16);
+            __builtin_memcpy(&w, &part, 16);
+            r.sum[0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e, w, r.sum[0], 0, 0, 0);
+            r.sum[1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(o, w, r.sum[1], 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 4; i++) x[i] -= __uint_as_float(__float_as_uint(x[i]) & 0xFFFF0000u);
+        }
+    }
+    r.taken = (__ballot(small) >> n) & 0x0001000100010001ull;
+    return r;
 }
 
 // The launch: `tiles` row tiles (per key/value head), `splits` workgroups each
@@ -322,6 +432,9 @@ __device__ __forceinline__ void stage_key_scales(Words<NB> dk, int live, int lan
 struct Sizes {
     int e[2];
     bool bad[2];
+    __device__ __forceinline__ float down(int i) const {  // 2^-e
+        return bad[i] ? 0.0f : __uint_as_float((uint32_t)(127 - e[i]) << 23);
+    }
 };
 template <int NB>
 __device__ __forceinline__ Sizes sizes_of(const Words<NB>& dv) {
@@ -357,7 +470,7 @@ __device__ __forceinline__ void stage_value_scales(Words<NB> dv, int live, int l
     float f[2];
 #pragma unroll
     for (int i = 0; i < 2; i++) {
-        f[i] = z.bad[i] ? 0.0f : __uint_as_float((uint32_t)(127 - z.e[i]) << 23);
+        f[i] = z.down(i);
         down[2 * lane + i] = f[i];
     }
 #pragma unroll
@@ -370,6 +483,44 @@ __device__ __forceinline__ void stage_value_scales(Words<NB> dv, int live, int l
         const uint32_t own = word(v);
         to[i][lane] = __builtin_amdgcn_perm(dpp_bits<DPP_XOR1>(own), own, pick);
     }
+}
+// Whether a scale of the lane's live positions is SMALL beside the largest of its position.
+template <int NB>
+__device__ __forceinline__ bool some_small(Words<NB> dv, int live) {
+    keep_live<NB>(dv, live);
+    const Sizes z = sizes_of<NB>(dv);
+    uint32_t least[2] = {0x7FFF, 0x7FFF};
+#pragma unroll
+    for (int i = 0; i < 2 * NB; i++) {
+        const uint32_t m = half_bits(dv.w[i >> 1], i & 1) & 0x7FFFu;
+        least[i / NB] = m < least[i / NB] ? m : least[i / NB];
+    }
+    bool small = false;
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+        small |= live > i && !z.bad[i] && half_value((uint16_t)least[i]) * z.down(i) < SMALL;
+    return small;
+}
+// The blocks (bits) of a run in which some position's scale is SMALL and some other's is not 0, from the
+// scales of two positions a lane; `live` 0 for lanes without any.
+template <int NB>
+__device__ __forceinline__ uint32_t blocks_apart(Words<NB> dv, int live) {
+    keep_live<NB>(dv, live);
+    const Sizes z = sizes_of<NB>(dv);
+    uint32_t blocks = 0;
+#pragma unroll
+    for (int i = 0; i < NB; i++) {
+        const float v[2] = {fabsf((float)half_of(dv.w[i >> 1], i & 1)),
+                            fabsf((float)half_of(dv.w[(NB + i) >> 1], (NB + i) & 1))};
+        bool small = false, some = false;
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+            small |= live > j && !z.bad[j] && v[j] * z.down(j) < SMALL;
+            some |= !z.bad[j] && v[j] > 0.0f;
+        }
+        if (__ballot(small) && __ballot(some)) blocks |= 1u << i;
+    }
+    return blocks;
 }
 
 // PACK: at most 8 rows share a key/value head in the tile.  The 16 columns of
@@ -532,13 +683,18 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void k_attn(AttnArgs a
             const bool masked = t0 + SUB > pos_lo + 1 || (a.window && t0 <= pos_hi - a.window) ||
                                 there != (1u << TILES) - 1;
             const uint32_t here = there;
+            const int mine = t0 + 16 * (lane >> 3) + 2 * (lane & 7);
+            const int live = ((here >> (lane >> 3)) & 1) ? s.len - mine : 0;
+            bool small = false;
             if (TILES == 8 || lane < 8 * TILES) {
-                const int u = lane >> 3, t = t0 + 16 * u + 2 * (lane & 7);
-                const int live = ((here >> u) & 1) ? s.len - t : 0;
                 stage_key_scales<NB>(dk, live, lane, s_own[wave].s.dk);
                 stage_value_sizes<NB>(dv, live, lane, s_own[wave].s.ev);
                 stage_value_scales<NB>(dv, live, lane, s_own[wave].s.dv, s_own[wave].s.down);
+                small = some_small<NB>(dv, live);
             }
+            uint32_t apart = 0;
+            if (__ballot(small)) apart = blocks_apart<NB>(dv, live);
+            apart = uniform(apart);
             wave_sync();
 
             // scores: sc[U][i] of row n at position t0 + 16 u + 4g + i, u the slot's tile
@@ -731,6 +887,19 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void k_attn(AttnArgs a
                     }
                 }
             }
+#pragma nounroll
+            for (; apart; apart &= apart - 1) {
+                const int bb = __builtin_ctz(apart);
+                const Exact x = exact_sums<NB>(a, unpack, table, s.len, head, t0, bb, factor, ref, pos, lane,
+                                               [&](int b, half8& qh, half8& ql) {
+                                                   qh = lds_read<half8>(q_at + 2048 * b);
+                                                   ql = lds_read<half8>(q_at + 2048 * b + 1024);
+                                               });
+#pragma unroll
+                for (int i = 0; i < 2 * NB; i++)
+                    if (x.taken && bb == i / 2) o[i] = x.sum[i & 1];
+                all_arrived();
+            }
         }
         fetch_scales(seg + 1);
         fetch_keys();
@@ -821,7 +990,7 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void k_attn(AttnArgs a
 // scores need) are replaced while values are worked on, and values while scores
 // are, from words loaded a run ahead; two barriers a run.  Every wave joins its
 // runs to segments and its segments to its state itself, in the steps of k_attn.
-// 250 registers, so two waves a SIMD: VALU 62 %, LDS 34 %, matrix cores 24 % busy.
+// 256 registers, so two waves a SIMD: VALU 62 %, LDS 34 %, matrix cores 24 % busy.
 template <int NB>
 __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_wide(AttnArgs a, Plan plan) {
     static_assert(sub_of(NB) == 128 && WAVES == 4, "a wave unpacks two tiles of keys and a pair of values");
@@ -834,6 +1003,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_wide(AttnArgs a, Plan pl
     uint32_t (*s_dv)[SUB / 2] = s_dk + NB;
     float* s_ev = reinterpret_cast<float*>(s_dv + NB);
     float* s_down = s_ev + SUB;
+    uint32_t* s_apart = reinterpret_cast<uint32_t*>(s_down + SUB);  // blocks, of the values in LDS
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int n = lane & 15, g = lane >> 4;
@@ -870,7 +1040,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_wide(AttnArgs a, Plan pl
         if (sub < sub1 && lane < TILES && t < s.len) pg = table[t >> kv.log2p];
     };
     // the wave's share: tiles 2w, 2w + 1 of keys, pair w of values, wave 0 the keys' and wave 1 the
-    // values' scales; fetch_keys notes which tiles have a page and where all of them lie
+    // values' scales, wave 2 these too, to find the blocks apart; fetch_keys notes which tiles have a
+    // page and where all of them lie
     uint32_t at_lo = 0, at_hi = 0;
     const auto tile_codes = [&](int u) {
         return kv.pages + ((uint32_t)__builtin_amdgcn_readlane(at_lo, u) |
@@ -888,7 +1059,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_wide(AttnArgs a, Plan pl
 #pragma unroll
         for (int i = 0; i < 2; i++)
             kw[i] = load_words<NB>(tile_codes(2 * wave + i) + n * (16 * NB) + g * (4 * NB));
-        if (wave < 2) {
+        if (wave < 3) {
             const int u = lane >> 3, t = t0 + 16 * u + 2 * (lane & 7);
             dd = load_words<NB>(head_of(kv, __shfl(p, u), head) + 2 * codes +
                                 ((int64_t)(wave ? 2 * NB : 0) << kv.log2p) +
@@ -926,6 +1097,12 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_wide(AttnArgs a, Plan pl
             to[1][lane] = make_uint4(unpack.high(w0), unpack.high(v0), unpack.high(w1), unpack.high(v1));
         }
         if (wave == 1) stage_value_scales<NB>(dd, live_of(sub, have), lane, s_dv, s_down);
+        if (wave == 2) {
+            const int live = live_of(sub, have);
+            uint32_t apart = 0;
+            if (__ballot(some_small<NB>(dd, live))) apart = blocks_apart<NB>(dd, live);
+            if (lane == 0) *s_apart = apart;
+        }
     };
     const uint32_t k_at = lds_at(&s_k[0][lane]), v_at = lds_at(&s_v[0][lane]);
     const uint32_t dk_at = lds_at(&s_dk[0][2 * g]), dv_at = lds_at(&s_dv[0][2 * g]);
@@ -1015,6 +1192,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_wide(AttnArgs a, Plan pl
         __syncthreads();  // every wave is done with the keys
         Split p[TILES][2];  // weights of positions 0, 2 and 1, 3 of each four
         Join js{1.0f, 0.0f};
+        uint32_t apart = *s_apart;
+        float ref = 0.0f;
         if (work) {
             if (masked) {
                 const int rel = pos - t0 - 4 * g;
@@ -1033,7 +1212,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_wide(AttnArgs a, Plan pl
 #pragma unroll
                 for (int i = 0; i < 4; i++) top = fmaxf(top, sc[u][i]);
             top = max_rows(top);
-            const float ref = reference(top);
+            ref = reference(top);
             float sum[2] = {0.0f, 0.0f};  // over the even and the odd tiles
 #pragma unroll
             for (int u = 0; u < TILES; u++) {
@@ -1067,6 +1246,18 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_wide(AttnArgs a, Plan pl
                 n0 = lds_read<u2>(dv_at + 4 * (bb * (SUB / 2) + 8 * u));
                 n1 = lds_read<u2>(dv_at + 4 * (bb * (SUB / 2) + 8 * u + 16));
             };
+            // (the segment's state, to which exact sums are joined below, waits in memory, as the
+            // registers are full; the compiler must not see through it and keep it in them)
+            float before[8 * NB];
+            apart = uniform(apart);
+            if (apart) {
+                float* to = before;
+                asm volatile("" : "+v"(to));
+#pragma unroll
+                for (int i = 0; i < 8 * NB; i++) to[i] = os[i >> 2][i & 3];
+                asm volatile("" : : "v"(to) : "memory");
+                all_arrived();
+            }
             next(0, 0);
 #pragma unroll
             for (int bb = 0; bb < NB; bb++) {
@@ -1095,6 +1286,25 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_wide(AttnArgs a, Plan pl
                     os[2 * bb][i] = joined(os[2 * bb][i], o0[i], js);
                     os[2 * bb + 1][i] = joined(os[2 * bb + 1][i], o1[i], js);
                 }
+            }
+#pragma nounroll
+            for (; apart; apart &= apart - 1) {
+                const int bb = __builtin_ctz(apart);
+                const float* from = before;
+                asm volatile("" : "+v"(from) : : "memory");
+                const Exact x = exact_sums<NB>(a, unpack, table, s.len, head, t0, bb, factor, ref, pos, lane,
+                                               [&](int b, half8& h, half8& l) {
+                                                   h = qh[b];
+                                                   l = ql[b];
+                                               });
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const float y = joined(from[8 * bb + i], x.sum[i >> 2][i & 3], js);
+#pragma unroll
+                    for (int b = 0; b < NB; b++)
+                        if (x.taken && bb == b) os[2 * b + (i >> 2)][i & 3] = y;
+                }
+                all_arrived();
             }
         }
         __syncthreads();  // every wave is done with the values
@@ -1126,7 +1336,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_wide(AttnArgs a, Plan pl
     }
 }
 
-template <int NB> constexpr int wide_lds() { return 2 * 8 * NB * 1024 + 2 * NB * 256 + 2 * 512; }
+template <int NB> constexpr int wide_lds() { return 2 * 8 * NB * 1024 + 2 * NB * 256 + 2 * 512 + 16; }
 
 // Joins the segments of a row in ascending order, as k_attn does when it has
 // them all: one workgroup per row, query head and W elements (all, or 32 where

@@ -146,3 +146,98 @@ def test_scores_of_any_size(g, kernel, sign):
             want, mean = vs[seen].mean(0), np.abs(vs[seen]).mean(0)
             lim = np.repeat((80 + L / 512) * 2.0 ** -24 * mean, hq // hkv, 0)
             assert np.all(np.abs(got[j] - np.repeat(want, hq // hkv, 0)) <= lim), (j, size[j])
+
+
+def block_bound(c, q, ks, vs, hq, scale, got, row, floor):
+    """Checks a row (or some of its heads) by its blocks: the f32 computation of `bound`, and `floor`
+    of the largest p max |v| of the element's own block a key."""
+    heads = np.arange(hq) if hq <= 8 else np.sort(c.rng.choice(hq, 4, replace=False))
+    L, d = c.pos[row] + 1, c.d
+    for h in heads:
+        k, v, x = ks[:L, h * c.hkv // hq], vs[:L, h * c.hkv // hq], q[row, h].astype(np.float64)
+        s = k @ x * scale
+        p = np.exp(s - s.max())
+        p /= p.sum()
+        pv = p @ np.abs(v)
+        most = (p[:, None] * np.abs(v).reshape(L, c.nb, 32).max(-1)).max(0).repeat(32)
+        delta = (d + 8) * 2.0 ** -24 * (np.abs(k) @ np.abs(x)).max() * scale + 2.0 ** -21
+        lim = (2 * delta + (80 + L / 512) * 2.0 ** -24) * pv + L * floor * most
+        err = np.abs(got[row, h] - p @ v)
+        assert np.all(err <= lim), (row, h, (err / np.maximum(lim, 1e-300)).reshape(c.nb, 32).max(-1))
+
+
+# exponents of a block's scale, relative to the head's largest
+STEPS = np.array([0, 0, -1, -3, -6, -7, -8, -9, -14, -20, -25, -30, -33])
+
+
+def scales_of(c, how, L):
+    """Value scales [L, hkv, nb] and, for some, the key that the queries look for."""
+    shape = (L, c.hkv, c.nb)
+    e, look = np.zeros(shape), None
+    if how == "blocks":      # every token alike, a size for each block
+        e += STEPS[(5 + 3 * np.arange(c.nb)) % len(STEPS)]
+        e[..., 0] = 0
+    elif how == "tokens":    # every block of every token for itself, zeros among them
+        e = c.rng.choice(np.append(STEPS, -99), shape)
+    elif how == "looked at":  # one token takes nearly all the weight, and has a block as small as can be
+        look = L // 2
+        e[look, :, c.nb - 1] = -33
+        e[look + 1, :, c.nb - 1] = -99
+    elif how == "nothing":   # a block of zeros in every token, and tokens of zeros
+        e[..., c.nb - 1] = -99
+        e[::3] = -99
+    d = np.where(e == -99, 0.0, np.ldexp(600 * (1 + c.rng.random(shape)), e.astype(int)))
+    return (d * c.rng.choice([-1, 1], shape)).astype(np.float16), look
+
+
+def case_of(g, kernel, how, seed):
+    c, page, hq, hkv, d = shaped(g, kernel, seed)
+    L, n = c.lens[0], c.ns[0]
+    kc, kd = q4_0(c.rng.standard_normal((L, hkv, d)).astype(np.float32))
+    vd, look = scales_of(c, how, L)
+    vc = c.rng.integers(0, 16, (L, hkv, c.nb, 32))
+    vc[..., 3] = 0  # a code of -8 in every block
+    q = 2 * c.rng.standard_normal((n, hq, d))
+    if look is not None:  # a score of about 40 there
+        k = np.repeat(q4_value(kc, kd)[look], hq // hkv, 0)
+        q = q * 0.5 + 40 * d ** 0.5 * k / (k ** 2).sum(-1, keepdims=True)
+    return c, page, hq, hkv, d, kc, kd, vc, vd, q.astype(np.float32)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("how", ["blocks", "tokens", "looked at", "nothing"])
+def test_value_scales_of_a_head_apart(g, kernel, how):
+    """Blocks of one head whose scales are far apart: each keeps the accuracy of an f32 computation of
+    its own sums.  Where all scales that a row sees in a run are within 2^-8 of the largest of their
+    token, weight times scale is held as two f16 numbers in a unit where the run's largest is 2^13 at
+    least, and the block's at that token 2^5: the two are off by at most 2^-24 (half of f16's smallest
+    step, once for the weight and once for the product), and meet codes of at most 8 as the block's
+    own largest does, so a key adds at most 2^-29 of it.  Elsewhere nothing is lost but f32 roundings."""
+    c, page, hq, hkv, d, kc, kd, vc, vd, q = case_of(g, kernel, how, 33)
+    raw, ks, vs = built(c, kc, kd, vc, vd)
+    n, scale = c.ns[0], float(np.float32(d ** -0.5))
+    got = g.kv_attention(g.KVCache(dev(raw), page, hkv, d), c.batch(g), dev(q.reshape(n, -1)), scale)
+    got = got.cpu().numpy().reshape(n, hq, d)
+    for row in range(n) if n < 30 else c.rng.choice(n, 12, replace=False):
+        block_bound(c, q, ks, vs, hq, scale, got, row, 2.0 ** -29)
+
+
+@pytest.mark.parametrize("kernel", [k for k in KERNELS if k[1][0] > 1] + [([400], [160], 32, 8, 2, 128, 16, False)])
+def test_scales_apart_change_no_row_that_does_not_see_them(g, kernel):
+    """Bit for bit: rows before such a token as without it, and all rows as in calls of one row."""
+    c, page, hq, hkv, d, kc, kd, vc, vd, q = case_of(g, kernel, "tokens", 34)
+    L, n, scale = c.lens[0], c.ns[0], d ** -0.5
+    from_ = L - n // 2
+    vd[:from_] = (c.rng.random(vd[:from_].shape) + 1).astype(np.float16)
+    plain = vd.copy()
+    plain[from_:] = 1
+    qd, batch = dev(q.reshape(n, -1)), c.batch(g)
+    with_, without = (g.kv_attention(g.KVCache(dev(built(c, kc, kd, vc, x)[0]), page, hkv, d), batch, qd, scale)
+                      for x in (vd, plain))
+    rows = from_ - (L - n)
+    assert torch.equal(with_[:rows], without[:rows])
+    assert not torch.equal(with_[rows:], without[rows:])
+    cache, table = g.KVCache(dev(built(c, kc, kd, vc, vd)[0]), page, hkv, d), dev(c.table)
+    for j in range(n) if n < 30 else c.rng.choice(n, 12, replace=False):
+        one = g.KVBatch(table, dev(np.array([L - n + j + 1], np.int32)), max_len=int(L))
+        assert torch.equal(g.kv_attention(cache, one, qd[j:j + 1], scale)[0], with_[j]), j
