@@ -28,8 +28,9 @@ struct Seq {
 __device__ __forceinline__ Seq seq_of(const KvArgs& kv, int b) {
     Seq s;
     s.q0 = kv.q_start ? kv.q_start[b] : b;
-    s.n = kv.q_start ? kv.q_start[b + 1] - s.q0 : 1;
-    if (s.q0 < 0 || s.n < 0 || s.n > kv.T - s.q0) s.q0 = s.n = 0;
+    const int end = kv.q_start ? kv.q_start[b + 1] : b + 1;
+    if (s.q0 < 0 || end < s.q0 || end > kv.T) s.q0 = s.n = 0;
+    else s.n = end - s.q0;
     const int64_t most = kv.table_stride << kv.log2p;
     int len = kv.lens[b];
     if (len > kv.max_len) len = kv.max_len;
