@@ -587,21 +587,23 @@ def _on_device(device, stream, call):
     of the current device, without a context (these calls take microseconds)."""
     import torch
     if stream is None and torch.cuda.current_device() == device.index:
-        return call(torch.cuda.current_stream().cuda_stream if _raw_stream is None
-                    else _raw_stream(device.index))
+        return call((_raw_stream or _find_raw_stream())(device.index))
     with _On(device, stream) as handle:
         return call(handle)
 
 
+# device index -> the handle of its current stream; looked up by the first call,
+# since importing this package does not import torch
+_raw_stream = None
+
+
 def _find_raw_stream():
     import torch
-    return getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-try:
-    _raw_stream = _find_raw_stream()  # the handle without a Stream object around it
-except ImportError:
-    _raw_stream = None
+    global _raw_stream
+    # the handle without a Stream object around it, where torch gives it
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return _raw_stream
 
 
 def _on(t, dtype, what, device):

@@ -2,6 +2,8 @@
 check runs on the host before anything is enqueued)."""
 import ctypes
 import os
+import subprocess
+import sys
 
 import pytest
 
@@ -219,3 +221,15 @@ def test_the_choice_of_an_attention_kernel():
     assert rows(1, 1, False, 32, 8, 160, 100) == 16 and rows(1 << 14, 1, True, 32, 8, 256, 1 << 14) == 16
     assert rows(64, 64, True, 8, 1, 64, 100) == 8 and rows(65, 64, True, 8, 1, 64, 100) == 16
     assert rows(2048, 1, True, 32, 8, 128, 2048) == 64 and rows(1024, 4, True, 32, 8, 128, 4096) == 16
+
+
+def test_importing_the_package_does_not_import_torch():
+    """The ctypes layer has no need of torch, and works where torch is missing or broken."""
+    code = ("import sys; sys.modules['torch'] = None; import gguf_quantized_matvec_amd as g; "
+            "assert sys.modules['torch'] is None; print(g.qmv_kv_bytes(1, 16, 1, 32))")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and r.stdout.strip() == str(16 * 36), r.stderr
+    code = "import sys, gguf_quantized_matvec_amd; assert 'torch' not in sys.modules"
+    assert subprocess.run([sys.executable, "-c", code], cwd=os.path.dirname(os.path.dirname(
+        os.path.abspath(__file__)))).returncode == 0
