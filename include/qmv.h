@@ -484,15 +484,17 @@ int qmv_kv_attention_rows(int64_t T, int64_t B, int starts, int q_heads, int kv_
  * 16-byte aligned; work: qmv_kv_attention_bytes(T, B, ...) bytes, 16-byte
  * aligned, used by one call at a time; out and work overlap nothing else;
  * 0 < scale <= 1e6; T * q_heads / 8 + B * kv_heads < 2^24.
- * The products keep 22 bits of q (but not less than 2^-40 of the row's largest
+ * The products keep 22 bits of q (but not less than 2^-39 of the row's largest
  * element of the head) and of the weights times the values' scales (but not
  * less than 2^-29 of the largest such term of the same 32 elements); sums are
  * f32: an element has the accuracy of an f32 computation of its sum, however
  * far apart the scales of a head's blocks are.  A row's bits depend on its q and on
  * the positions it sees alone: not on the other rows, on how a prompt is cut
  * into calls, on the pages' order or on max_len.  A row that sees a position
- * with a non-finite scale, or whose q is not finite, is NaN throughout; what
- * a row does not see, uninitialised pages included, does not reach it.
+ * with a non-finite scale, or that sees any position and has a q that is not
+ * finite, is NaN throughout (a row here is a query's head: its other heads are
+ * not affected); what a row does not see, uninitialised pages included, does
+ * not reach it.
  * scale * q and the scores have to stay below 2^126 in size. */
 int qmv_kv_attention(const qmv_kv* kv, const qmv_kv_batch* seqs, const float* q, int64_t q_stride,
                      int q_heads, float scale, int64_t window, float* out, void* work,

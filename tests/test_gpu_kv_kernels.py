@@ -241,3 +241,53 @@ def test_scales_apart_change_no_row_that_does_not_see_them(g, kernel):
     for j in range(n) if n < 30 else c.rng.choice(n, 12, replace=False):
         one = g.KVBatch(table, dev(np.array([L - n + j + 1], np.int32)), max_len=int(L))
         assert torch.equal(g.kv_attention(cache, one, qd[j:j + 1], scale)[0], with_[j]), j
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_q_that_is_not_finite(g, kernel):
+    """A query's head with a NaN or an infinity is NaN throughout, its other heads and the other rows
+    are as without it."""
+    c, page, hq, hkv, d = shaped(g, kernel, 35)
+    n = c.ns[0]
+    raw, _, _ = filled(c, hq)
+    cache, batch = g.KVCache(dev(raw), page, hkv, d), c.batch(g)
+    q = c.rng.standard_normal((n, hq, d)).astype(np.float32)
+    clean = g.kv_attention(cache, batch, dev(q.reshape(n, -1)), 0.1).view(n, hq, d)
+    spoilt = c.rng.random((n, hq)) < 0.3
+    spoilt[0, 0] = True
+    for j, h in np.argwhere(spoilt):
+        q[j, h, c.rng.integers(d)] = c.rng.choice([np.nan, np.inf, -np.inf])
+    got = g.kv_attention(cache, batch, dev(q.reshape(n, -1)), 0.1).view(n, hq, d)
+    spoilt = torch.from_numpy(spoilt).cuda()
+    assert torch.all(torch.isnan(got[spoilt])) and torch.equal(got[~spoilt], clean[~spoilt])
+
+
+def test_q_that_is_not_finite_and_sees_nothing(g):
+    """More rows than tokens: the first see no position and are 0 whatever they hold."""
+    c = Case([3], [7], 16, 2, 64, 36)
+    raw, _, _ = filled(c, 4)
+    q = dev(np.full((7, 4 * 64), np.nan, np.float32))
+    got = g.kv_attention(g.KVCache(dev(raw), 16, 2, 64), c.batch(g), q, 0.125)
+    assert torch.all(got[:4] == 0) and torch.all(torch.isnan(got[4:]))
+
+
+@pytest.mark.parametrize("kernel", KERNELS[:-1])
+@pytest.mark.parametrize("apart", [6, 12, 18])
+def test_q_of_sizes_apart(g, kernel, apart):
+    """The first block of q 2^apart times the others, that of the keys as much smaller.  Two f16
+    parts of q in a unit where the head's largest element is 2^14 at least are off by at most half of
+    f16's smallest step, 2^-25: 2^-39 of that element, times the sum of the key's sizes."""
+    c, page, hq, hkv, d = shaped(g, kernel, 37)
+    L, n, scale = c.lens[0], c.ns[0], float(np.float32(d ** -0.5))
+    kc, kd = q4_0(c.rng.standard_normal((L, hkv, d)).astype(np.float32))
+    kd[..., 0] *= np.float16(2.0 ** -apart)
+    vc, vd = q4_0(c.rng.standard_normal((L, hkv, d)).astype(np.float32))
+    raw, ks, vs = built(c, kc, kd, vc, vd)
+    q = c.rng.standard_normal((n, hq, d)).astype(np.float32)
+    q[..., :32] *= np.float32(2.0 ** apart)
+    got = g.kv_attention(g.KVCache(dev(raw), page, hkv, d), c.batch(g), dev(q.reshape(n, -1)), scale)
+    got = got.cpu().numpy().reshape(n, hq, d)
+    want, amax, pv, pmax = attention(q, ks, vs, c.pos, scale)
+    size = np.abs(ks).sum(-1).max(0).repeat(hq // hkv)
+    lost = 2.0 ** -39 * np.abs(q).max(-1) * size * scale
+    assert np.all(np.abs(got - want) <= bound(d, L, amax, pv, pmax) + 2 * lost[..., None] * pv)
