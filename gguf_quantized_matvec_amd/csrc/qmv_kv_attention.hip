@@ -531,11 +531,13 @@ __device__ __forceinline__ uint32_t blocks_apart(Words<NB> dv, int live) {
 // tiles, move across, and go on over the odd tiles, which is the order of the
 // sums in every variant.
 //
-// What bounds it: with few rows the loads' latency and the VALU, 57 % busy (131072 positions, 41 us,
-// 3.7 TB/s), with many the VALU (about 1650 instructions a wave and run, a third of them unpacking,
-// beside 128 matrix instructions: 77 % busy on four chunks of 256 tokens, 163 us).  So three waves a
-// SIMD: the rows' two parts, the same for the four waves, wait in LDS, and a wave's sums take the
-// place of its scales (32 sequences of 301..8191: 53 us, 60 with the rows in registers, two waves).
+// What bounds it: with few rows the loads' latency and the VALU, 56 % busy (131072 positions, 46 us
+// with the join), with many the VALU (about 1700 instructions a wave and run, a third of them
+// unpacking, beside 128 matrix instructions: 78 % busy on four chunks of 256 tokens, 142 us).  So three
+// waves a SIMD: the rows' two parts, the same for the four waves, wait in LDS, and a wave's sums take
+// the place of its scales (32 sequences of 301..8191: 57 us with the join, an eighth more with the rows
+// in registers and two waves).  With 16 rows and 128 elements ten registers are spilled, nearly all
+// before the loop of the runs.
 template <int NB, bool PACK>
 __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void k_attn(AttnArgs a, Plan plan) {
     const KvArgs& kv = a.kv;
@@ -990,7 +992,7 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void k_attn(AttnArgs a
 // scores need) are replaced while values are worked on, and values while scores
 // are, from words loaded a run ahead; two barriers a run.  Every wave joins its
 // runs to segments and its segments to its state itself, in the steps of k_attn.
-// 256 registers, so two waves a SIMD: VALU 62 %, LDS 34 %, matrix cores 24 % busy.
+// 256 registers, so two waves a SIMD: VALU 60 %, LDS 32 %, matrix cores 23 % busy.
 template <int NB>
 __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_wide(AttnArgs a, Plan plan) {
     static_assert(sub_of(NB) == 128 && WAVES == 4, "a wave unpacks two tiles of keys and a pair of values");
@@ -1441,18 +1443,25 @@ Plan plan_of(bool one, int64_t T, int64_t B, int Hq, int Hkv, int nb, int64_t ma
     Plan p;
     // Packed tiles of 8 rows where the sequences of a call have that few per key/value head on
     // average; 64 rows a workgroup where that many fill them and there are four per CU, as long
-    // and short ones have to even out (a 2048-token prompt with a window of 1024, 32 heads on 8:
-    // 114 us, 168 in tiles of 16; four chunks of 256 tokens on prefixes of up to 3750, with half as
-    // many workgroups, 201 against 163); else tiles of 16.
+    // and short ones have to even out; else tiles of 16.  32 heads on 8 of 128, 64 rows against 16: a
+    // prompt of 2048 tokens (1032 workgroups of 64 rows) 129 against 155 us, two of 1024 132 against
+    // 158; four chunks of 256 on prefixes of up to 3750 (536) 187 against 146, six (800) 232 against 208,
+    // eight (1064) 280 against 276.  Prompts without prefixes gain earlier (1536 tokens, 776: 76 against
+    // 100 us; 1024, 520: 50 against 58), which the numbers of rows do not tell from the chunks.
     p.pack = nb <= 4 && (one ? G <= 8 : T * G <= 8 * B);
     p.wide = nb <= 4 && !one && T * G >= 64 * B && (T * G / 64 + B) * Hkv >= 1024;
     const int64_t tr = p.wide ? 64 : p.pack ? 8 : 16;
     p.tiles = (int32_t)(one ? B * ((G + tr - 1) / tr) : T * G / tr + B);
     p.segs = (int32_t)((max_len + seg_of(nb) - 1) / seg_of(nb));
     // One sequence: two workgroups per CU, all of which run at once, each with several segments, so
-    // that the loads ahead work and the prologue is paid once (131072 positions, 32 heads on 8: 41 us,
-    // and 43 with three or four per CU).  Several sequences differ in length: four times as many, which
-    // even out (32 of 301..8191: 53 us, and 68 with as many as for one).
+    // that the loads ahead work and the prologue is paid once (131072 positions, 32 heads on 8: 46.7 us,
+    // 47.2 with three per CU, 45.2 with four).  Several sequences differ in length: four times as many,
+    // which even out (32 of 301..8191: 57 us, 67 with half as many, 71 with as many as for one).  From
+    // 512 tiles on no split: 64 sequences of 301..8191 110 us, 121 split in four, 104 in eight; 96 134
+    // without, 138 in three, 143 in six; 64 of 1..2000 31 without, 43 with; but 63 of 301..8191, which
+    // are split in four, 119, in eight 102.
+    // All that goes by max_len, the bound, as the lengths are not known here: 32 sequences of 301..8191
+    // take 60 us with 8191 and 173 with 131072, where each head is one workgroup's.
     const int64_t groups = (int64_t)p.tiles * Hkv, want = B == 1 ? 512 : 2048;
     int64_t splits = groups >= 512 ? 1 : (want + groups - 1) / groups;
     if (splits > p.segs) splits = p.segs;

@@ -423,8 +423,10 @@ typedef struct qmv_kv {
  * positions.  q_start NULL: one row a sequence, T == B.  Rows from
  * q_start[B] on belong to no sequence and are left alone, outputs included.
  * A length of 0 is a sequence without tokens.  max_len (1..2^30, at most
- * table_stride * page_tokens) bounds the lengths, and sizes the launch and the
- * workspace.  1 <= B, T <= QMV_KV_MAX_ROWS.
+ * table_stride * page_tokens) bounds the lengths, and sizes the launch, its
+ * split over the chip and the workspace: a bound far above the lengths costs
+ * time (three times as much for 32 sequences of up to 8191 tokens under one of
+ * 131072).  1 <= B, T <= QMV_KV_MAX_ROWS.
  * These contents are not checked on the host.  Whatever they hold, nothing
  * outside the described buffers is touched: a length is cut to max_len, a
  * page number out of range holds no token (an append drops it, attention does
