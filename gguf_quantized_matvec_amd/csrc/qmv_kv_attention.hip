@@ -63,6 +63,7 @@ constexpr float NO_KEY = -3.402823466e38f;
 // A block of values whose scale is this far below the largest of its position has its sums done
 // apart (exact_sums).
 constexpr float SMALL = 1.0f / 256;
+constexpr uint16_t SMALL_BITS = (15 - 8) << 10;  // as f16
 
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bfloat8 __attribute__((ext_vector_type(8)));
@@ -123,6 +124,12 @@ __device__ __forceinline__ _Float16 half_of(uint32_t w, int i) {
 
 __device__ __forceinline__ half2v halves(uint32_t w) {
     half2v h;
+    __builtin_memcpy(&h, &w, 4);
+    return h;
+}
+typedef uint16_t ushort2v __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ ushort2v ushorts(uint32_t w) {
+    ushort2v h;
     __builtin_memcpy(&h, &w, 4);
     return h;
 }
@@ -187,8 +194,8 @@ __device__ __forceinline__ void wave_sync() {
 //
 // Few models need it, if any, so it is made for few registers rather than for speed: everything is
 // loaded and the scores are computed once more, in the same steps (parts(b): the rows' two parts).
-// Calls that do not need it take 1 % longer with it, in k_attn_wide 3 %; calls that need it for one
-// block of every position 2.3 to 2.9 times as long (32 sequences of 301..8191: 133 us for 57).
+// Calls that do not need it take as long as without it, in k_attn_wide 3 % longer; calls that need it
+// for one block of every position 2.3 to 2.9 times as long (32 sequences of 301..8191: 133 us for 57).
 struct Exact {
     f4 sum[2];  // even elements, odd elements
     bool taken;
@@ -459,9 +466,10 @@ __device__ __forceinline__ void stage_value_sizes(Words<NB> dv, int live, int la
 #pragma unroll
     for (int i = 0; i < 2; i++) ev[2 * lane + i] = z.bad[i] ? INFINITY : (float)z.e[i];
 }
-// The values' scales as dv 2^-ev, below 1, and 2^-ev.
+// The values' scales as dv 2^-ev, below 1, and 2^-ev.  True if a scale of the lane's live positions
+// is SMALL beside the largest of its position.
 template <int NB>
-__device__ __forceinline__ void stage_value_scales(Words<NB> dv, int live, int lane,
+__device__ __forceinline__ bool stage_value_scales(Words<NB> dv, int live, int lane,
                                                    uint32_t (*to)[sub_of(NB) / 2], float* down) {
     keep_live<NB>(dv, live);
     const Sizes z = sizes_of<NB>(dv);
@@ -473,6 +481,7 @@ __device__ __forceinline__ void stage_value_scales(Words<NB> dv, int live, int l
         f[i] = z.down(i);
         down[2 * lane + i] = f[i];
     }
+    ushort2v least = {0x7FFF, 0x7FFF};
 #pragma unroll
     for (int i = 0; i < NB; i++) {
         half2v v = {half_of(dv.w[i >> 1], i & 1), half_of(dv.w[(NB + i) >> 1], (NB + i) & 1)};
@@ -481,25 +490,11 @@ __device__ __forceinline__ void stage_value_scales(Words<NB> dv, int live, int l
         // the lanes of positions 0, 1 and 2, 3 exchange to words of positions 0, 2 and 1, 3, the
         // order of the code words
         const uint32_t own = word(v);
+        least = __builtin_elementwise_min(least, ushorts(own & 0x7FFF7FFFu));
         to[i][lane] = __builtin_amdgcn_perm(dpp_bits<DPP_XOR1>(own), own, pick);
     }
-}
-// Whether a scale of the lane's live positions is SMALL beside the largest of its position.
-template <int NB>
-__device__ __forceinline__ bool some_small(Words<NB> dv, int live) {
-    keep_live<NB>(dv, live);
-    const Sizes z = sizes_of<NB>(dv);
-    uint32_t least[2] = {0x7FFF, 0x7FFF};
-#pragma unroll
-    for (int i = 0; i < 2 * NB; i++) {
-        const uint32_t m = half_bits(dv.w[i >> 1], i & 1) & 0x7FFFu;
-        least[i / NB] = m < least[i / NB] ? m : least[i / NB];
-    }
-    bool small = false;
-#pragma unroll
-    for (int i = 0; i < 2; i++)
-        small |= live > i && !z.bad[i] && half_value((uint16_t)least[i]) * z.down(i) < SMALL;
-    return small;
+    return (live > 0 && !z.bad[0] && least[0] < SMALL_BITS) ||
+           (live > 1 && !z.bad[1] && least[1] < SMALL_BITS);
 }
 // The blocks (bits) of a run in which some position's scale is SMALL and some other's is not 0, from the
 // scales of two positions a lane; `live` 0 for lanes without any.
@@ -691,8 +686,7 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void k_attn(AttnArgs a
             if (TILES == 8 || lane < 8 * TILES) {
                 stage_key_scales<NB>(dk, live, lane, s_own[wave].s.dk);
                 stage_value_sizes<NB>(dv, live, lane, s_own[wave].s.ev);
-                stage_value_scales<NB>(dv, live, lane, s_own[wave].s.dv, s_own[wave].s.down);
-                small = some_small<NB>(dv, live);
+                small = stage_value_scales<NB>(dv, live, lane, s_own[wave].s.dv, s_own[wave].s.down);
             }
             uint32_t apart = 0;
             if (__ballot(small)) apart = blocks_apart<NB>(dv, live);
@@ -1042,8 +1036,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_wide(AttnArgs a, Plan pl
         if (sub < sub1 && lane < TILES && t < s.len) pg = table[t >> kv.log2p];
     };
     // the wave's share: tiles 2w, 2w + 1 of keys, pair w of values, wave 0 the keys' and wave 1 the
-    // values' scales, wave 2 these too, to find the blocks apart; fetch_keys notes which tiles have a
-    // page and where all of them lie
+    // values' scales; fetch_keys notes which tiles have a page and where all of them lie
     uint32_t at_lo = 0, at_hi = 0;
     const auto tile_codes = [&](int u) {
         return kv.pages + ((uint32_t)__builtin_amdgcn_readlane(at_lo, u) |
@@ -1061,7 +1054,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_wide(AttnArgs a, Plan pl
 #pragma unroll
         for (int i = 0; i < 2; i++)
             kw[i] = load_words<NB>(tile_codes(2 * wave + i) + n * (16 * NB) + g * (4 * NB));
-        if (wave < 3) {
+        if (wave < 2) {
             const int u = lane >> 3, t = t0 + 16 * u + 2 * (lane & 7);
             dd = load_words<NB>(head_of(kv, __shfl(p, u), head) + 2 * codes +
                                 ((int64_t)(wave ? 2 * NB : 0) << kv.log2p) +
@@ -1098,11 +1091,11 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_wide(AttnArgs a, Plan pl
             to[0][lane] = make_uint4(unpack.low(w0), unpack.low(v0), unpack.low(w1), unpack.low(v1));
             to[1][lane] = make_uint4(unpack.high(w0), unpack.high(v0), unpack.high(w1), unpack.high(v1));
         }
-        if (wave == 1) stage_value_scales<NB>(dd, live_of(sub, have), lane, s_dv, s_down);
-        if (wave == 2) {
+        if (wave == 1) {
             const int live = live_of(sub, have);
             uint32_t apart = 0;
-            if (__ballot(some_small<NB>(dd, live))) apart = blocks_apart<NB>(dd, live);
+            if (__ballot(stage_value_scales<NB>(dd, live, lane, s_dv, s_down)))
+                apart = blocks_apart<NB>(dd, live);
             if (lane == 0) *s_apart = apart;
         }
     };
