@@ -526,9 +526,9 @@ __device__ __forceinline__ uint32_t blocks_apart(Words<NB> dv, int live) {
 // tiles, move across, and go on over the odd tiles, which is the order of the
 // sums in every variant.
 //
-// What bounds it: with few rows the loads' latency and the VALU, 56 % busy (131072 positions, 46 us
-// with the join), with many the VALU (about 1700 instructions a wave and run, a third of them
-// unpacking, beside 128 matrix instructions: 78 % busy on four chunks of 256 tokens, 142 us).  So three
+// What bounds it: with few rows the loads' latency and the VALU, 58 % busy (131072 positions, 46 us
+// with the join), with many the VALU (about 1670 instructions a wave and run, a third of them
+// unpacking, beside 128 matrix instructions: 77 % busy on four chunks of 256 tokens, 142 us).  So three
 // waves a SIMD: the rows' two parts, the same for the four waves, wait in LDS, and a wave's sums take
 // the place of its scales (32 sequences of 301..8191: 57 us with the join, an eighth more with the rows
 // in registers and two waves).  With 16 rows and 128 elements ten registers are spilled, nearly all
@@ -986,7 +986,7 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void k_attn(AttnArgs a
 // scores need) are replaced while values are worked on, and values while scores
 // are, from words loaded a run ahead; two barriers a run.  Every wave joins its
 // runs to segments and its segments to its state itself, in the steps of k_attn.
-// 256 registers, so two waves a SIMD: VALU 60 %, LDS 32 %, matrix cores 23 % busy.
+// 256 registers, so two waves a SIMD: VALU 59 %, LDS 32 %, matrix cores 23 % busy.
 template <int NB>
 __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_wide(AttnArgs a, Plan plan) {
     static_assert(sub_of(NB) == 128 && WAVES == 4, "a wave unpacks two tiles of keys and a pair of values");
