@@ -148,13 +148,14 @@ def test_scores_of_any_size(g, kernel, sign):
             assert np.all(np.abs(got[j] - np.repeat(want, hq // hkv, 0)) <= lim), (j, size[j])
 
 
-def block_bound(c, q, ks, vs, hq, scale, got, row, floor):
+def block_bound(c, q, ks, vs, hq, scale, got, row, floor, seen=slice(None)):
     """Checks a row (or some of its heads) by its blocks: the f32 computation of `bound`, and `floor`
     of the largest p max |v| of the element's own block a key."""
     heads = np.arange(hq) if hq <= 8 else np.sort(c.rng.choice(hq, 4, replace=False))
-    L, d = c.pos[row] + 1, c.d
+    d = c.d
     for h in heads:
-        k, v, x = ks[:L, h * c.hkv // hq], vs[:L, h * c.hkv // hq], q[row, h].astype(np.float64)
+        k, v = (y[:c.pos[row] + 1, h * c.hkv // hq][seen] for y in (ks, vs))
+        L, x = len(k), q[row, h].astype(np.float64)
         s = k @ x * scale
         p = np.exp(s - s.max())
         p /= p.sum()
@@ -291,3 +292,33 @@ def test_q_of_sizes_apart(g, kernel, apart):
     size = np.abs(ks).sum(-1).max(0).repeat(hq // hkv)
     lost = 2.0 ** -39 * np.abs(q).max(-1) * size * scale
     assert np.all(np.abs(got - want) <= bound(d, L, amax, pv, pmax) + 2 * lost[..., None] * pv)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("window", [0, 60])
+def test_value_scales_apart_behind_masks(g, kernel, window):
+    """The same with a window, a hole in the table, and scales that are not finite where no row looks:
+    against the definition, and bit for bit as alone."""
+    c, page, hq, hkv, d, kc, kd, vc, vd, q = case_of(g, kernel, "tokens", 38)
+    L, n, scale = c.lens[0], c.ns[0], float(np.float32(d ** -0.5))
+    hole = (L - 40) // page  # a page that rows with a window of 60 see
+    raw, ks, vs = built(c, kc, kd, vc, vd)
+    cells = c.cells(raw)
+    cells[c.table[0, hole]] = 0xFF  # NaN scales
+    cells[c.spare] = 0xFF
+    c.table[0, hole] = -1
+    table = dev(c.table)
+    cache, qd = g.KVCache(dev(raw), page, hkv, d), dev(q.reshape(n, -1))
+    out = g.kv_attention(cache, c.batch(g), qd, scale, window=window)
+    got = out.cpu().numpy().reshape(n, hq, d)
+    for row in range(n) if n < 30 else c.rng.choice(n, 12, replace=False):
+        t = np.arange(c.pos[row] + 1)
+        seen = t // page != hole
+        if window:
+            seen &= t > c.pos[row] - window
+        if seen.any():
+            block_bound(c, q, ks, vs, hq, scale, got, row, 2.0 ** -29, seen)
+        else:
+            assert np.all(got[row] == 0)
+        one = g.KVBatch(table, dev(np.array([c.pos[row] + 1], np.int32)), max_len=int(L))
+        assert torch.equal(g.kv_attention(cache, one, qd[row:row + 1], scale, window=window)[0], out[row]), row
