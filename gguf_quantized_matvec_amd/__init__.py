@@ -24,9 +24,11 @@ EXPORTS = ("qmv_act_bytes", "quantize_act_q8_0", "qmv_launch", "qmv_launch_group
            "qmv_launch_gateup_swiglu", "qmv_launch_gateup_swiglu_q8", "qmv_act_bytes_q8k", "quantize_act_q8_k", "qmv_launch_q8k",
            "qmv_launch_gateup_swiglu_q8k", "qmv_launch_group_q8k", "qmm_launch_q8k", "qmv_partials_q8k_launch", "qmv_prepared_bytes", "qmv_prepare",
            "qmm_launch_q8k_prepared", "qmm_partials_q8k_prepared_launch", "qmv_add_rmsnorm_q8_0", "qmv_add_rmsnorm_q8_k",
-           "qmv_kv_bytes", "qmv_kv_append", "qmv_kv_read", "qmv_kv_attention_bytes", "qmv_kv_attention_rows", "qmv_kv_attention", "qmv_strerror")
+           "qmv_kv_bytes", "qmv_kv_append", "qmv_kv_read", "qmv_kv_attention_bytes", "qmv_kv_attention_rows", "qmv_kv_attention",
+           "qmv_moe_route", "qmv_moe_gateup_bytes", "qmv_moe_gateup_swiglu", "qmv_moe_down_bytes", "qmv_moe_down", "qmv_strerror")
 MAX_BATCH = 16
 MAX_GROUP = 8
+MOE_SCORES = {"softmax": 0, "sigmoid": 1}
 
 
 class Gemv(ctypes.Structure):
@@ -103,13 +105,19 @@ def lib() -> ctypes.CDLL:
         L.qmv_kv_attention_bytes.restype = ctypes.c_size_t
         L.qmv_kv_attention_rows.argtypes = [I64, I64, I, I, I, I, I64]
         L.qmv_kv_attention.argtypes = [KV, KB, P, I64, I, F, I64, P, P, P]
+        L.qmv_moe_route.argtypes = [P, I64, I64, I, P, I, I, I, I, I, F, P, P, P]
+        for f in ("qmv_moe_gateup_bytes", "qmv_moe_down_bytes"):
+            getattr(L, f).argtypes = [I64, I, I64, I64, I64]
+            getattr(L, f).restype = ctypes.c_size_t
+        L.qmv_moe_gateup_swiglu.argtypes = [I, P, P, I64, I64, I64, P, I64, I, P, P, P, P, P]
+        L.qmv_moe_down.argtypes = [I, P, I64, I64, I64, P, P, I64, I, P, P, P, P, P]
         for f in ("quantize_act_q8_0", "qmv_launch", "qmv_launch_group", "qmm_launch",
                   "qmv_partials_launch", "qmm_partials_launch", "qmv_launch_noalloc",
                   "qmv_launch_gateup_swiglu", "qmv_launch_gateup_swiglu_q8", "quantize_act_q8_k", "qmv_launch_q8k",
                   "qmv_launch_gateup_swiglu_q8k", "qmv_launch_group_q8k", "qmm_launch_q8k", "qmv_partials_q8k_launch", "qmv_prepare",
                   "qmm_launch_q8k_prepared", "qmm_partials_q8k_prepared_launch", "qmv_add_rmsnorm_q8_0",
                   "qmv_add_rmsnorm_q8_k", "qmv_kv_append", "qmv_kv_read", "qmv_kv_attention_rows",
-                  "qmv_kv_attention"):
+                  "qmv_kv_attention", "qmv_moe_route", "qmv_moe_gateup_swiglu", "qmv_moe_down"):
             getattr(L, f).restype = I
         L.qmv_strerror.argtypes = [I]
         L.qmv_strerror.restype = ctypes.c_char_p
@@ -280,6 +288,33 @@ def qmv_kv_attention(kv: KvStruct, seqs: KvBatchStruct, q: int, q_stride: int, q
                      scale: float, window: int, out: int, work: int, stream: int = 0) -> None:
     _check(lib().qmv_kv_attention(kv, seqs, q, q_stride, q_heads, scale, window, out, work, stream),
            "qmv_kv_attention")
+
+
+def qmv_moe_route(logits: int, T: int, E: int, score: int, bias, groups: int, top_groups: int,
+                  group_top: int, top: int, renorm: int, scale: float, idx: int, weight: int,
+                  stream: int = 0) -> None:
+    _check(lib().qmv_moe_route(logits, T, E, score, bias, groups, top_groups, group_top, top, renorm,
+                               scale, idx, weight, stream), "qmv_moe_route")
+
+
+def qmv_moe_gateup_bytes(T: int, top: int, E: int, N: int, K: int) -> int:
+    return int(lib().qmv_moe_gateup_bytes(T, top, E, N, K))
+
+
+def qmv_moe_gateup_swiglu(type: int, w_gate: int, w_up: int, E: int, N: int, K: int, idx: int, T: int,
+                          top: int, x, xq, h: int, work: int, stream: int = 0) -> None:
+    _check(lib().qmv_moe_gateup_swiglu(type, w_gate, w_up, E, N, K, idx, T, top, x, xq, h, work,
+                                       stream), "qmv_moe_gateup_swiglu")
+
+
+def qmv_moe_down_bytes(T: int, top: int, E: int, N: int, K: int) -> int:
+    return int(lib().qmv_moe_down_bytes(T, top, E, N, K))
+
+
+def qmv_moe_down(type: int, w: int, E: int, N: int, K: int, idx: int, weight: int, T: int, top: int,
+                 h, hq, y: int, work: int, stream: int = 0) -> None:
+    _check(lib().qmv_moe_down(type, w, E, N, K, idx, weight, T, top, h, hq, y, work, stream),
+           "qmv_moe_down")
 
 
 def qmv_strerror(code: int) -> str:
@@ -813,5 +848,129 @@ def kv_attention(cache: KVCache, batch: KVBatch, q, scale: float, window: int = 
         ws, wp = _new(work, q, torch.uint8, "work", n)
         qmv_kv_attention(cache.c, batch.c, qp, qs, heads, scale, window, op, wp, s)
         return o
+
+    return _on_device(dev, stream, call)
+
+
+# ------------------------------------------------------ mixture of experts --
+
+def moe_route(logits, top: int, score: str = "softmax", bias=None, groups: int = 1, top_groups: int = 1,
+              group_top: int = 1, renorm: bool = True, scale: float = 1.0, idx=None, weight=None,
+              stream=None):
+    """(idx int32, weight f32), both [T, top]: the experts that the tokens of logits [T, E] go to and
+    their weights, as qmv_moe_route describes them (a slot without an expert: -1 and 0)."""
+    import torch
+    f32 = torch.float32
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [T, E], got {tuple(logits.shape)}")
+    if score not in MOE_SCORES:
+        raise ValueError(f"score must be one of {sorted(MOE_SCORES)}, got {score!r}")
+    T, E = logits.shape
+    lp = _dev(logits, f32, "logits")
+    dev = logits.device
+    bp = None
+    if bias is not None:
+        if bias.shape != (E,):
+            raise ValueError(f"bias must be [{E}], got {tuple(bias.shape)}")
+        bp = _on(bias, f32, "bias", dev)
+    for t, what in ((idx, "idx"), (weight, "weight")):
+        if t is not None and t.shape != (T, top):
+            raise ValueError(f"{what} must be [{T}, {top}], got {tuple(t.shape)}")
+
+    def call(s):
+        i, ip = _new(idx, logits, torch.int32, "idx", (T, top))
+        w, wp = _new(weight, logits, f32, "weight", (T, top))
+        qmv_moe_route(lp, T, E, MOE_SCORES[score], bp, groups, top_groups, group_top, top, int(renorm),
+                      scale, ip, wp, s)
+        return i, w
+
+    return _on_device(dev, stream, call)
+
+
+def _experts(type, w, N, K, what):
+    """(address, number) of the matrices of an expert tensor."""
+    import torch
+    p = _dev(w, torch.uint8, what)
+    one = N * row_bytes(type, K)
+    if one <= 0 or w.numel() == 0 or w.numel() % one:
+        raise ValueError(f"{what} must be whole {N} x {K} matrices of {one} bytes, got {w.numel()} bytes")
+    return p, w.numel() // one
+
+
+def _pairs(idx, dev):
+    import torch
+    if idx.dim() != 2:
+        raise ValueError(f"idx must be [T, top], got {tuple(idx.shape)}")
+    return (_on(idx, torch.int32, "idx", dev), *idx.shape)
+
+
+def _rows_or_blocks(x, xq, rows, K, what, dev):
+    """Addresses of f32 rows or of their Q8_0 blocks, one of the two None."""
+    import torch
+    if (x is None) == (xq is None):
+        raise ValueError(f"give {what} or {what}q, one of them")
+    if x is not None:
+        if x.numel() != rows * K or x.shape[-1] != K:
+            raise ValueError(f"{what} must hold {rows} rows of {K}, got {tuple(x.shape)}")
+        return _on(x, torch.float32, what, dev), None
+    if xq.numel() < rows * (K // 32) * 34:
+        raise ValueError(f"{what}q must hold {rows * (K // 32) * 34} bytes, got {xq.numel()}")
+    return None, _on(xq, torch.uint8, what + "q", dev)
+
+
+def _moe_work(work, n):
+    if n == 0:
+        raise ValueError("bad shape of a mixture of experts: see the limits in qmv.h")
+    if work is not None and work.numel() < n:
+        raise ValueError(f"work must hold {n} bytes, got {work.numel()}")
+
+
+def moe_gateup_swiglu(type: int, w_gate, w_up, N: int, K: int, idx, x=None, xq=None, h=None, work=None,
+                      stream=None):
+    """h [T, top, N] f32 = silu(Wg[e] x) * (Wu[e] x) for the experts e of idx int32 [T, top]: w_gate
+    and w_up hold E matrices N x K each; x f32 [T, K], or xq with the rows' Q8_0 blocks."""
+    import torch
+    gp, E = _experts(type, w_gate, N, K, "w_gate")
+    dev = w_gate.device
+    if w_up.numel() != w_gate.numel():
+        raise ValueError(f"w_up must hold {w_gate.numel()} bytes as w_gate does, got {w_up.numel()}")
+    up = _on(w_up, torch.uint8, "w_up", dev)
+    ip, T, top = _pairs(idx, dev)
+    xp, qp = _rows_or_blocks(x, xq, T, K, "x", dev)
+    if h is not None and h.numel() != T * top * N:
+        raise ValueError(f"h must hold {T * top} rows of {N}, got {tuple(h.shape)}")
+    n = qmv_moe_gateup_bytes(T, top, E, N, K)
+    _moe_work(work, n)
+
+    def call(s):
+        out, hp = _new(h, w_gate, torch.float32, "h", (T, top, N))
+        ws, wp = _new(work, w_gate, torch.uint8, "work", n)
+        qmv_moe_gateup_swiglu(type, gp, up, E, N, K, ip, T, top, xp, qp, hp, wp, s)
+        return out
+
+    return _on_device(dev, stream, call)
+
+
+def moe_down(type: int, w, N: int, K: int, idx, weight, h=None, hq=None, y=None, work=None, stream=None):
+    """y [T, N] f32 = sum over the slots of weight * (W[e] h) for the experts e of idx int32 [T, top]:
+    w holds E matrices N x K; weight f32 [T, top]; h f32 [T, top, K], or hq with the rows' Q8_0 blocks."""
+    import torch
+    wp, E = _experts(type, w, N, K, "w")
+    dev = w.device
+    ip, T, top = _pairs(idx, dev)
+    if weight.shape != idx.shape:
+        raise ValueError(f"weight must have idx's shape {tuple(idx.shape)}, got {tuple(weight.shape)}")
+    sp = _on(weight, torch.float32, "weight", dev)
+    hp, qp = _rows_or_blocks(h, hq, T * top, K, "h", dev)
+    if y is not None and y.shape != (T, N):
+        raise ValueError(f"y must be [{T}, {N}], got {tuple(y.shape)}")
+    n = qmv_moe_down_bytes(T, top, E, N, K)
+    _moe_work(work, n)
+
+    def call(s):
+        out, yp = _new(y, w, torch.float32, "y", (T, N))
+        ws, kp = _new(work, w, torch.uint8, "work", n)
+        qmv_moe_down(type, wp, E, N, K, ip, sp, T, top, hp, qp, yp, kp, s)
+        return out
 
     return _on_device(dev, stream, call)

@@ -1,0 +1,770 @@
+// Experts' products for up to 16 rows of an expert at a time, for gfx950: the
+// multiply of qmv_launch (GGUF block weights x Q8_0 activations, integer block
+// dots, one f32 term a 32-element block, chunks of 8 blocks added in ascending
+// order; include/qmv.h), with the weights of the expert that each pair names.
+// Every pair's result is bit-identical to qmv_launch on that expert's matrix.
+//
+// An item is up to R = 4 NI pairs of one expert.  A workgroup of 8 waves takes
+// an item and 8 / KS tiles of 16 weight rows; KS waves share a tile and take
+// its 256-element chunks in turn.  A wave fetches the 16 rows' bytes of a
+// chunk as 16-byte pieces into registers, two chunks ahead (the gate's and the
+// up's of a pair), lays them into its slice of LDS, and lane (nn = l % 16,
+// kg = l / 16) decodes its quarter of each of weight row nn's blocks into an
+// operand of v_mfma_i32_16x16x32_i8.  Result element i of the lane is
+// activation row 4 kg + i of the instruction; the item's row j stands at
+// 4 (j % 4) + j / 4, so with NI rows a lane only the elements i < NI are
+// scaled: few rows cost few f32 terms.  The item's activations lie in LDS, a
+// segment of chunks at a time, shared by the 8 waves.
+//
+// Order inside a block does not matter (the integers are exact), so lane kg
+// takes bytes 4kg .. 4kg+3 of a 16-byte nibble block, low and high nibbles,
+// and the activations are laid out to match: no lane reads nibbles that it
+// does not use.
+//
+// Built with -ffp-contract=off: every float operation is the one written.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "qmv_moe.h"
+
+namespace qmv {
+namespace {
+
+constexpr int T_Q4_0 = 2, T_Q4_1 = 3, T_Q5_0 = 6, T_Q5_1 = 7, T_Q8_0 = 8, T_Q8_1 = 9,
+              T_Q4_K = 12, T_Q6_K = 14;
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+
+// QK, BB: elements and bytes of a block; CB: bytes of a chunk of 256 elements;
+// PPS: 16-byte pieces that cover a chunk at the worst alignment of its start.
+template <int FMT> struct Fmt;
+template <> struct Fmt<T_Q8_0> { static constexpr int QK = 32, BB = 34, CB = 272, PPS = 18; };
+template <> struct Fmt<T_Q4_0> { static constexpr int QK = 32, BB = 18, CB = 144, PPS = 10; };
+template <> struct Fmt<T_Q5_0> { static constexpr int QK = 32, BB = 22, CB = 176, PPS = 12; };
+template <> struct Fmt<T_Q4_1> { static constexpr int QK = 32, BB = 20, CB = 160, PPS = 11; };
+template <> struct Fmt<T_Q5_1> { static constexpr int QK = 32, BB = 24, CB = 192, PPS = 13; };
+template <> struct Fmt<T_Q8_1> { static constexpr int QK = 32, BB = 36, CB = 288, PPS = 19; };
+template <> struct Fmt<T_Q4_K> { static constexpr int QK = 256, BB = 144, CB = 144, PPS = 9; };
+template <> struct Fmt<T_Q6_K> { static constexpr int QK = 256, BB = 210, CB = 210, PPS = 14; };
+
+// The block term has a second part, a minimum times the activation codes' sum.
+template <int FMT> constexpr bool has_min() {
+    return FMT == T_Q4_K || FMT == T_Q4_1 || FMT == T_Q5_1;
+}
+// Blocks of 16 bytes of nibbles: element e < 16 the low one of byte e, e + 16 the high one.
+template <int FMT> constexpr bool nibble_block() {
+    return FMT == T_Q4_0 || FMT == T_Q4_1 || FMT == T_Q5_0 || FMT == T_Q5_1;
+}
+// Codes with an offset are formed as 16 (c - 8) and 8 (c - 16), whose int8
+// bits are a shift and a flipped top bit away; the factor leaves with the
+// activation scale, both exactly (powers of two).
+template <int FMT> constexpr float scale_back() {
+    return FMT == T_Q4_0 ? 1.0f / 16 : FMT == T_Q5_0 ? 1.0f / 8 : 1.0f;
+}
+template <int FMT> constexpr int pieces() { return (16 * Fmt<FMT>::PPS + 63) / 64; }
+template <int FMT> constexpr int row_stride() { return 16 * Fmt<FMT>::PPS + 16; }
+template <int FMT> constexpr int slice() { return 16 * row_stride<FMT>(); }
+
+constexpr int WAVES = 8;
+constexpr int SEG = 16;
+constexpr int ACT_STRIDE = 272;   // a row's 256 codes of a chunk, and 16 bytes so that rows differ in their banks
+
+__device__ __forceinline__ float half_bits(uint32_t h) {
+    const uint16_t u = (uint16_t)h;
+    _Float16 f;
+    __builtin_memcpy(&f, &u, 2);
+    return (float)f;
+}
+template <typename T> __device__ __forceinline__ T ld(const uint8_t* p) {
+    T v;
+    __builtin_memcpy(&v, p, sizeof(T));
+    return v;
+}
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// silu(g) u in f64 as t = exp(-g), s = g / (1 + t), s u, rounded once.
+__device__ __forceinline__ float swiglu(float g, float u) {
+    const double gd = (double)g;
+    const double s = gd / (1.0 + exp(-gd));
+    return (float)(s * (double)u);
+}
+
+// ----------------------------------------------------------- preparation ----
+// One launch before the product: workgroups 0 .. E sort the pairs (only beyond
+// MOE_SCAN pairs), the others quantise x to Q8_0 blocks.
+//
+// Workgroup e counts all pairs by expert, writes those of expert e in
+// ascending order to their place, and e's items: no workgroup waits for
+// another.  Its waves each take a run of the pairs, count and then write.
+struct PrepArgs {
+    const float* x;
+    uint8_t* blocks;
+    int64_t nblocks;     // Q8_0 blocks of x (0: nothing to quantise)
+    const int32_t* idx;
+    int32_t P, E, R;
+    int32_t planners;    // E + 1, or 0
+    int32_t* items;
+    int32_t* order;
+    int32_t* count;
+    bool a16;            // x is 16-byte aligned
+};
+constexpr int PREP = 512;
+
+__device__ __forceinline__ int key_of(int e, int E) { return (unsigned)e < (unsigned)E ? e : E; }
+
+__global__ __launch_bounds__(PREP) void k_moe_prep(PrepArgs a) {
+    __shared__ int hist[1025], seen[PREP / 64], sums[2][PREP / 64];
+    const int tid = threadIdx.x, lane = tid & 63, wv = uniform(tid >> 6);
+    if ((int)blockIdx.x < a.planners) {
+        const int E = a.E, P = a.P, e = blockIdx.x;
+        for (int i = tid; i <= E; i += PREP) hist[i] = 0;
+        __syncthreads();
+        const int run = ((P + PREP - 1) / PREP) * 64, lo = wv * run, hi = min(P, lo + run);
+        int mine = 0;
+        for (int p = lo; p < hi; p += 64) {
+            const int k = p + lane < hi ? key_of(a.idx[p + lane], E) : -1;
+            if (k >= 0) atomicAdd(&hist[k], 1);
+            mine += __popcll(__builtin_amdgcn_ballot_w64(k == e));
+        }
+        if (lane == 0) seen[wv] = mine;
+        __syncthreads();
+        // pairs and items of the experts below e (and, for the last, of all)
+        int before = 0, base = 0;
+        for (int i = tid; i < e; i += PREP) {
+            before += hist[i];
+            base += (hist[i] + a.R - 1) / a.R;
+        }
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            before += __shfl_xor(before, o);
+            base += __shfl_xor(base, o);
+        }
+        if (lane == 0) {
+            sums[0][wv] = before;
+            sums[1][wv] = base;
+        }
+        __syncthreads();
+        int start = 0, item = 0, at = 0;
+        for (int i = 0; i < PREP / 64; i++) {
+            start += sums[0][i];
+            item += sums[1][i];
+            if (i < wv) at += seen[i];
+        }
+        const int n = hist[e], items = (n + a.R - 1) / a.R;
+        at += start;
+        for (int p = lo; p < hi; p += 64) {
+            const bool is = p + lane < hi && key_of(a.idx[p + lane], E) == e;
+            const uint64_t m = __builtin_amdgcn_ballot_w64(is);
+            if (is) a.order[at + __popcll(m & ((1ull << lane) - 1))] = p + lane;
+            at += __popcll(m);
+        }
+        for (int i = tid; i < items; i += PREP)
+            reinterpret_cast<int4*>(a.items)[item + i] =
+                make_int4(e, start + i * a.R, min(a.R, n - i * a.R), 0);
+        if (e == E && tid == 0) *a.count = item + items;
+        return;
+    }
+    // eight lanes a block, four elements each
+    const int64_t b = (int64_t)((int)blockIdx.x - a.planners) * (PREP / 8) + (tid >> 3);
+    const int sub = tid & 7;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (b < a.nblocks) {
+        const float* xb = a.x + b * 32 + 4 * sub;
+        if (a.a16) {
+            const float4 f = *reinterpret_cast<const float4*>(xb);
+            v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; i++) v[i] = xb[i];
+        }
+    }
+    float amax = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
+    const float d = amax / 127.0f;
+    const float r = 1.0f / d, id = __builtin_isinf(r) ? 0.0f : r;
+    uint32_t c = 0;
+#pragma unroll
+    for (int i = 0; i < 4; i++) c |= ((uint32_t)(int)roundf(v[i] * id) & 0xFFu) << (8 * i);
+    if (b >= a.nblocks) return;
+    uint16_t* out = reinterpret_cast<uint16_t*>(a.blocks + b * 34);
+    out[1 + 2 * sub] = (uint16_t)c;
+    out[2 + 2 * sub] = (uint16_t)(c >> 16);
+    if (sub == 0) {
+        const _Float16 h = (_Float16)d;
+        __builtin_memcpy(out, &h, 2);
+    }
+}
+
+// --------------------------------------------------------------- product ----
+struct RowsArgs {
+    const uint8_t *w, *w2;
+    int64_t N, K, wbytes;    // wbytes: of all experts
+    int32_t E, P, per;
+    const int32_t* idx;
+    const uint8_t* blocks;   // Q8_0 blocks of the activation rows
+    const int32_t *items, *order, *count;
+    float* y;
+    int32_t ks;              // waves that share a tile: 1, 2, 4, 8
+    int32_t seg;             // chunks of activations in LDS at a time: SEG, or all if they are fewer
+    int32_t item0;           // the launch's first item
+};
+
+// One chunk of the 16 weight rows at rb (this lane's row) against the item's
+// rows: p[i] = the chunk's sum of row kg + 4 i, in the documented order.
+// ac: this lane's row of the activation codes (of the matrix operand); da, ca:
+// scales (times scale_back) and scale * code sum of row kg, 32 floats from one
+// row i to the next.  nbc: blocks of the chunk.
+template <int FMT, int NI>
+__device__ __forceinline__ void chunk_rows(const uint8_t* rb, const uint8_t* ac, const float* da,
+                                           const float* ca, int nbc, int kg, float (&p)[NI]) {
+    using F = Fmt<FMT>;
+    const v4i zero = {0, 0, 0, 0};
+    float dv[NI][8], cv[has_min<FMT>() ? NI : 1][8];
+#pragma unroll
+    for (int i = 0; i < NI; i++) {
+        const float4 a = *reinterpret_cast<const float4*>(da + 32 * i);
+        const float4 b = *reinterpret_cast<const float4*>(da + 32 * i + 4);
+        dv[i][0] = a.x; dv[i][1] = a.y; dv[i][2] = a.z; dv[i][3] = a.w;
+        dv[i][4] = b.x; dv[i][5] = b.y; dv[i][6] = b.z; dv[i][7] = b.w;
+        if constexpr (has_min<FMT>()) {
+            const float4 c = *reinterpret_cast<const float4*>(ca + 32 * i);
+            const float4 d = *reinterpret_cast<const float4*>(ca + 32 * i + 4);
+            cv[i][0] = c.x; cv[i][1] = c.y; cv[i][2] = c.z; cv[i][3] = c.w;
+            cv[i][4] = d.x; cv[i][5] = d.y; cv[i][6] = d.z; cv[i][7] = d.w;
+        }
+        p[i] = 0.0f;
+    }
+    // the superblock's fields
+    uint64_t q[4];
+    uint64_t qh[2];
+    uint4 hdr = make_uint4(0, 0, 0, 0);
+    float dw = 0.0f, dmin = 0.0f;
+    if constexpr (FMT == T_Q4_K) {
+        hdr = ld<uint4>(rb);
+        dw = half_bits(hdr.x & 0xFFFFu);
+        dmin = half_bits(hdr.x >> 16);
+#pragma unroll
+        for (int j = 0; j < 4; j++) q[j] = ld<uint64_t>(rb + 16 + 32 * j + 8 * kg);
+    } else if constexpr (FMT == T_Q6_K) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) q[j] = ld<uint64_t>(rb + 32 * j + 8 * kg);
+        qh[0] = ld<uint64_t>(rb + 128 + 8 * kg);
+        qh[1] = ld<uint64_t>(rb + 160 + 8 * kg);
+        hdr = ld<uint4>(rb + 192);
+        dw = half_bits(ld<uint16_t>(rb + 208));
+    }
+#pragma unroll
+    for (int b = 0; b < 8; b++) {
+        if (F::QK == 32 && b >= nbc) break;
+        const long a = *reinterpret_cast<const long*>(ac + 32 * b);
+        v4i I;
+        float mw = 0.0f;   // the minimum's factor: p += mw * ca
+        if constexpr (F::QK == 32) {
+            const uint8_t* blk = rb + F::BB * b;
+            dw = half_bits(ld<uint16_t>(blk));
+            uint64_t w;
+            if constexpr (FMT == T_Q8_0 || FMT == T_Q8_1) {
+                w = ld<uint64_t>(blk + (FMT == T_Q8_0 ? 2 : 4) + 8 * kg);
+            } else {
+                constexpr int QS = FMT == T_Q4_0 ? 2 : FMT == T_Q4_1 ? 4 : FMT == T_Q5_0 ? 6 : 8;
+                const uint32_t v = ld<uint32_t>(blk + QS + 4 * kg);
+                uint32_t lo, hi;
+                if constexpr (FMT == T_Q4_0) {
+                    lo = ((v << 4) & 0xF0F0F0F0u) ^ 0x80808080u;
+                    hi = (v & 0xF0F0F0F0u) ^ 0x80808080u;
+                } else if constexpr (FMT == T_Q4_1) {
+                    lo = v & 0x0F0F0F0Fu;
+                    hi = (v >> 4) & 0x0F0F0F0Fu;
+                } else {
+                    // fifth bits of elements 4kg .. 4kg+3 and 16 + 4kg ..: h * 0x204081 puts
+                    // bit j of a nibble h at bit 8 j (plus others, masked off), without carries
+                    const uint32_t h = ld<uint32_t>(blk + (FMT == T_Q5_0 ? 2 : 4)) >> (4 * kg);
+                    const uint32_t l5 = __umul24(h & 15u, 0x204081u) & 0x01010101u;
+                    const uint32_t h5 = __umul24((h >> 16) & 15u, 0x204081u) & 0x01010101u;
+                    if constexpr (FMT == T_Q5_0) {
+                        lo = (((v << 3) & 0x78787878u) | (l5 << 7)) ^ 0x80808080u;
+                        hi = (((v >> 1) & 0x78787878u) | (h5 << 7)) ^ 0x80808080u;
+                    } else {
+                        lo = (v & 0x0F0F0F0Fu) | (l5 << 4);
+                        hi = ((v >> 4) & 0x0F0F0F0Fu) | (h5 << 4);
+                    }
+                }
+                w = ((uint64_t)hi << 32) | lo;
+            }
+            if constexpr (has_min<FMT>()) mw = half_bits(ld<uint16_t>(blk + 2));
+            I = __builtin_amdgcn_mfma_i32_16x16x32_i8(a, (long)w, zero, 0, 0, 0);
+        } else if constexpr (FMT == T_Q4_K) {
+            const uint32_t s12[3] = {hdr.y, hdr.z, hdr.w};
+            auto byte = [&](int i) -> int { return (int)((s12[i >> 2] >> (8 * (i & 3))) & 0xFFu); };
+            int sc, mn;
+            if (b < 4) {
+                sc = byte(b) & 63;
+                mn = byte(b + 4) & 63;
+            } else {
+                sc = (byte(b + 4) & 15) | ((byte(b - 4) >> 6) << 4);
+                mn = (byte(b + 4) >> 4) | ((byte(b) >> 6) << 4);
+            }
+            mw = -(dmin * (float)mn);
+            const uint64_t raw = (b & 1) ? q[b >> 1] >> 4 : q[b >> 1];
+            I = __builtin_amdgcn_mfma_i32_16x16x32_i8(a, (long)(raw & 0x0F0F0F0F0F0F0F0Full), zero,
+                                                     0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < NI; i++) I[i] = __mul24(sc, I[i]);
+        } else {
+            const int h = b >> 2, kq = b & 3;
+            uint64_t ql = q[2 * h + (kq & 1)];
+            if (kq & 2) ql >>= 4;
+            const uint64_t q6 = (ql & 0x0F0F0F0F0F0F0F0Full) |
+                                (((qh[h] >> (2 * kq)) & 0x0303030303030303ull) << 4);
+            // q6 - 32 bytewise: no borrow leaves a byte whose top bit is set before
+            const uint64_t top = 0x8080808080808080ull;
+            const uint64_t w = ((q6 | top) - 0x2020202020202020ull) ^ top;
+            const uint32_t sc6[4] = {hdr.x, hdr.y, hdr.z, hdr.w};
+            const uint32_t sw = sc6[b >> 1] >> (16 * (b & 1));
+            const int s0 = (int8_t)(sw & 0xFF), s1 = (int8_t)((sw >> 8) & 0xFF);
+            // each half of the block has a scale of its own: two products, the other half's codes zero
+            const long lo = kg < 2 ? (long)w : 0, hi = kg < 2 ? 0 : (long)w;
+            const v4i I0 = __builtin_amdgcn_mfma_i32_16x16x32_i8(a, lo, zero, 0, 0, 0);
+            const v4i I1 = __builtin_amdgcn_mfma_i32_16x16x32_i8(a, hi, zero, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < NI; i++) I[i] = __mul24(s0, I0[i]) + __mul24(s1, I1[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < NI; i++) {
+            p[i] = fmaf((float)I[i], dw * dv[i][b], p[i]);
+            if constexpr (has_min<FMT>()) p[i] = fmaf(mw, cv[i][b], p[i]);
+        }
+    }
+}
+
+template <int FMT, bool PAIR, int NI, bool SCAN>
+__global__ __launch_bounds__(64 * WAVES, 4) void k_moe_rows(RowsArgs a) {
+    using F = Fmt<FMT>;
+    constexpr int R = 4 * NI, NP = pieces<FMT>(), MATS = PAIR ? 2 : 1;
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    int* pairs = reinterpret_cast<int*>(smem);    // [16] the item's pairs
+    const int tid = threadIdx.x, lane = tid & 63, wv = uniform(tid >> 6);
+    const int nn = lane & 15, kg = lane >> 4;
+
+    // the item: its expert and rows
+    int e = -1, rows = 0;
+    if constexpr (SCAN) {
+        const int key = lane < a.P ? key_of(a.idx[lane], a.E) : -1;
+        uint64_t left = __builtin_amdgcn_ballot_w64(lane < a.P);
+        int item = a.item0 + (int)blockIdx.y;
+        while (left) {
+            const int k = __builtin_amdgcn_readlane(key, (int)__builtin_ctzll(left));
+            const uint64_t m = __builtin_amdgcn_ballot_w64(key == k);
+            const int n = __popcll(m), items = (n + R - 1) / R;
+            if (item < items) {
+                e = k;
+                rows = min(R, n - item * R);
+                const int rank = __popcll(m & ((1ull << lane) - 1)) - item * R;
+                if (wv == 0 && key == k && rank >= 0 && rank < R) pairs[rank] = lane;
+                break;
+            }
+            item -= items;
+            left &= ~m;
+        }
+    } else if (a.item0 + (int)blockIdx.y < *a.count) {
+        const int4 it = reinterpret_cast<const int4*>(a.items)[a.item0 + (int)blockIdx.y];
+        e = uniform(it.x);
+        rows = uniform(it.z);
+        if (tid < rows) pairs[tid] = a.order[it.y + tid];
+    }
+    if (e < 0) return;
+    const int64_t N = a.N, K = a.K;
+    const int KS = a.ks, TW = WAVES / KS, ks = wv % KS, tw = wv / KS;
+    const int nb = (int)(K >> 5), C = (nb + 7) >> 3;
+    const int tiles = (int)((N + 15) >> 4);
+    if (e == a.E) {   // pairs without an expert
+        if constexpr (PAIR) {
+            __syncthreads();
+            const int64_t n0 = (int64_t)blockIdx.x * TW * 16;
+            const int width = (int)(N - n0 < TW * 16 ? N - n0 : TW * 16);
+            for (int i = tid; i < rows * width; i += 64 * WAVES) {
+                const int j = i / width;
+                a.y[pairs[j] * N + n0 + (i - j * width)] = 0.0f;
+            }
+        }
+        return;
+    }
+
+    // this wave's tile; a wave past the last one works on it too and stores nothing
+    const int tile_ = blockIdx.x * TW + tw;
+    const bool mine = tile_ < tiles;
+    const int64_t n0 = (int64_t)(mine ? tile_ : tiles - 1) * 16;
+    const int64_t Rb = (K / F::QK) * F::BB;
+    const int64_t tb = ((int64_t)e * N + n0) * Rb;
+    const uint32_t a0 = (uint32_t)(tb & 15);
+    const uint8_t* wt = a.w + (tb - a0);
+    const uint8_t* wt2 = PAIR ? a.w2 + (tb - a0) : wt;
+    const int64_t room = a.wbytes - (tb - a0) - 16;
+    const uint32_t lim = (uint32_t)(room < 0x7fffffff ? room : 0x7fffffff);
+    const bool tail = room < 16 * Rb + 16;          // pieces may reach past the last expert's end
+    const int last_row = (int)(N - 1 - n0 < 15 ? N - 1 - n0 : 15);
+    uint8_t* wl = smem + 64 + wv * slice<FMT>();
+    uint8_t* acts = smem + 64 + WAVES * slice<FMT>();
+    const int seg = a.seg;
+    float* dbuf = reinterpret_cast<float*>(acts + seg * R * ACT_STRIDE);    // [seg][R][8]
+    float* cbuf = dbuf + seg * R * 8;                                       // the same, with a minimum
+    float* pbuf = cbuf + (has_min<FMT>() ? seg * R * 8 : 0);                // [seg][TW][MATS][R][16], KS > 1
+
+    // 16-byte pieces: lane l's k-th is piece 64 k + l of the tile's rows
+    uint32_t rowoff[NP];
+    int pn[NP], pj[NP];
+#pragma unroll
+    for (int k = 0; k < NP; k++) {
+        const int p = min(64 * k + lane, 16 * F::PPS - 1);
+        pn[k] = p / F::PPS;
+        pj[k] = p - pn[k] * F::PPS;
+        rowoff[k] = a0 + (uint32_t)min(pn[k], last_row) * (uint32_t)Rb;
+    }
+    // a piece past the chunk's end is its last one again, one past the blob's
+    // end is moved back (staged bytewise)
+    auto piece = [&](int k, int c) -> uint32_t {
+        const uint32_t len = F::QK == 32 ? min(8, nb - 8 * c) * F::BB : F::CB;
+        const uint32_t s = rowoff[k] + (uint32_t)c * F::CB;
+        return min((s & ~15u) + 16 * pj[k], (s + len - 1) & ~15u);
+    };
+    auto fetch = [&](const uint8_t* base, int c, uint4 (&r)[NP]) {
+#pragma unroll
+        for (int k = 0; k < NP; k++)
+            __builtin_memcpy(&r[k], base + min(piece(k, c), lim), 16);
+    };
+    auto stage = [&](int c, const uint4 (&r)[NP]) {
+#pragma unroll
+        for (int k = 0; k < NP; k++)
+            if (64 * k + lane < 16 * F::PPS)
+                *reinterpret_cast<uint4*>(wl + pn[k] * row_stride<FMT>() + 16 * pj[k]) = r[k];
+        if (tail) {
+            // pieces that were moved back: their bytes to where they belong
+#pragma unroll
+            for (int k = 0; k < NP; k++) {
+                const uint32_t off = piece(k, c);
+                const uint32_t s = rowoff[k] + (uint32_t)c * F::CB;
+                if (off > lim) {
+                    uint8_t* to = wl + pn[k] * row_stride<FMT>() + (lim - (s & ~15u));
+                    uint16_t h[8];
+                    __builtin_memcpy(h, &r[k], 16);
+#pragma unroll
+                    for (int i = 0; i < 8; i++) __builtin_memcpy(to + 2 * i, &h[i], 2);
+                }
+            }
+        }
+        wave_sync();
+    };
+
+    // the wave's steps: its chunks ks, ks + KS, ...; of a pair first the gate's, then the up's
+    const int mychunks = (C - ks + KS - 1) / KS;   // may be 0
+    uint4 r0[NP], r1[NP];
+    if (mychunks > 0) fetch(wt, ks, r0);
+    if (PAIR ? mychunks > 0 : mychunks > 1) fetch(wt2, PAIR ? ks : ks + KS, r1);
+
+    float acc[MATS][NI];
+#pragma unroll
+    for (int m = 0; m < MATS; m++)
+#pragma unroll
+        for (int i = 0; i < NI; i++) acc[m][i] = 0.0f;
+    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // KS > 1: this thread's outputs tid + 512 q
+    const int outs = TW * MATS * R * 16;
+
+    // this lane's activation row of the matrix operand, and where its scales begin
+    const int arow = (nn >> 2) + ((nn & 3) < NI ? 4 * (nn & 3) : 0);
+
+    auto work = [&](int m, int c, int c0, const uint4 (&r)[NP]) {
+        stage(c, r);
+        const int cs = c - c0;
+        const uint32_t s = a0 + (uint32_t)min(nn, last_row) * (uint32_t)Rb + (uint32_t)c * F::CB;
+        const uint8_t* rb = wl + nn * row_stride<FMT>() + (s & 15);
+        const uint8_t* ac = acts + (cs * R + arow) * ACT_STRIDE + 8 * kg;
+        const float* da = dbuf + (cs * R + kg) * 8;
+        const float* ca = cbuf + (cs * R + kg) * 8;
+        float p[NI];
+        chunk_rows<FMT, NI>(rb, ac, da, ca, F::QK == 32 ? min(8, nb - 8 * c) : 8, kg, p);
+        wave_sync();
+        if (KS == 1) {
+#pragma unroll
+            for (int i = 0; i < NI; i++) acc[m][i] = acc[m][i] + p[i];
+        } else {
+            float* o = pbuf + cs * outs + ((tw * MATS + m) * R + kg) * 16 + nn;
+#pragma unroll
+            for (int i = 0; i < NI; i++) o[64 * i] = p[i];
+        }
+    };
+
+    int c = ks;
+    for (int c0 = 0; c0 < C; c0 += seg) {
+        const int c1 = min(C, c0 + seg);
+        __syncthreads();
+        // the segment's activations: a thread a block
+        {
+            const int nbs = min(nb, 8 * c1) - 8 * c0;
+            for (int i = tid; i < rows * nbs; i += 64 * WAVES) {
+                const int j = i / nbs, b = i - j * nbs;
+                const int64_t row = pairs[j] / a.per;
+                uint32_t v[9];
+                __builtin_memcpy(v, a.blocks + (row * nb + 8 * c0 + b) * 34, 34);
+                uint32_t q[8];
+#pragma unroll
+                for (int k = 0; k < 8; k++) q[k] = __builtin_amdgcn_alignbyte(k == 7 ? v[8] & 0xFFFFu : v[k + 1], v[k], 2);
+                const float d = half_bits(v[0] & 0xFFFFu);
+                uint4* to = reinterpret_cast<uint4*>(acts + ((b >> 3) * R + j) * ACT_STRIDE + 32 * (b & 7));
+                if constexpr (nibble_block<FMT>()) {
+                    to[0] = make_uint4(q[0], q[4], q[1], q[5]);
+                    to[1] = make_uint4(q[2], q[6], q[3], q[7]);
+                } else {
+                    to[0] = make_uint4(q[0], q[1], q[2], q[3]);
+                    to[1] = make_uint4(q[4], q[5], q[6], q[7]);
+                }
+                const int at = ((b >> 3) * R + j) * 8 + (b & 7);
+                dbuf[at] = d * scale_back<FMT>();
+                if constexpr (has_min<FMT>()) {
+                    int S = 0;
+#pragma unroll
+                    for (int k = 0; k < 8; k++) S = __builtin_amdgcn_sdot4((int)q[k], 0x01010101, S, false);
+                    cbuf[at] = d * (float)S;
+                }
+            }
+        }
+        __syncthreads();
+        if constexpr (PAIR) {
+            for (; c < c1; c += KS) {
+                work(0, c, c0, r0);
+                if (c + KS < C) fetch(wt, c + KS, r0);
+                work(1, c, c0, r1);
+                if (c + KS < C) fetch(wt2, c + KS, r1);
+            }
+        } else {
+            while (c < c1) {
+                work(0, c, c0, r0);
+                if (c + 2 * KS < C) fetch(wt, c + 2 * KS, r0);
+                c += KS;
+                if (c >= c1) break;   // only in the last segment: the others hold an even number of the wave's chunks
+                work(0, c, c0, r1);
+                if (c + 2 * KS < C) fetch(wt, c + 2 * KS, r1);
+                c += KS;
+            }
+        }
+        if (KS > 1) {
+            __syncthreads();
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const int o = tid + 64 * WAVES * q;
+                if (o < outs)
+                    for (int cs = 0; cs < c1 - c0; cs++) sum[q] = sum[q] + pbuf[cs * outs + o];
+            }
+        }
+    }
+
+    if (KS == 1) {
+        if (!mine) return;
+#pragma unroll
+        for (int i = 0; i < NI; i++) {
+            const int j = kg + 4 * i;
+            if (j < rows && nn <= last_row)
+                a.y[pairs[j] * N + n0 + nn] = PAIR ? swiglu(acc[0][i], acc[MATS - 1][i]) : acc[0][i];
+        }
+        return;
+    }
+    // output o = ((tile, matrix) R + row) 16 + weight row
+    if constexpr (PAIR) {
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            const int o = tid + 64 * WAVES * q;
+            if (o < outs) pbuf[o] = sum[q];
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+        const int o = tid + 64 * WAVES * q;
+        if (o >= outs) break;
+        const int n = o & 15, j = (o >> 4) % R, m = (o >> 4) / R;
+        const int64_t col = ((int64_t)blockIdx.x * TW + m / MATS) * 16 + n;
+        if (j < rows && col < N && (!PAIR || m % 2 == 0))
+            a.y[pairs[j] * N + col] = PAIR ? swiglu(sum[q], pbuf[o + R * 16]) : sum[q];
+    }
+}
+
+constexpr int64_t MOST_Y = 32768;
+
+// Raise a kernel's dynamic-LDS limit to the full 160 KB, once per kernel and device.
+int raise_lds_limit(const void* kernel, std::atomic<int> (&state)[64]) {
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess) return (int)hipErrorInvalidDevice;
+    std::atomic<int>* st = dev >= 0 && dev < 64 ? &state[dev] : nullptr;
+    if (st && st->load(std::memory_order_acquire) == 1) return 0;
+    const hipError_t rc =
+        hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+    if (rc != hipSuccess) return (int)rc;
+    if (st) st->store(1, std::memory_order_release);
+    return 0;
+}
+
+template <int FMT, bool PAIR, int NI, bool SCAN>
+int launch_rows(const MoeArgs& m, RowsArgs& a, hipStream_t s) {
+    using F = Fmt<FMT>;
+    constexpr int R = 4 * NI, MATS = PAIR ? 2 : 1;
+    const int64_t tiles = (a.N + 15) / 16, C = ((a.K >> 5) + 7) / 8;
+    a.wbytes = m.E * a.N * (a.K / F::QK) * F::BB;
+    const int64_t items = moe_most_items(m.P, m.E, R);
+    // waves that share a tile: enough waves to fill the chip
+    int ks = 1;
+    while (ks < 8 && 2 * ks <= C && tiles * items * ks * 2 <= 4096) ks *= 2;
+    a.ks = ks;
+    const int TW = WAVES / ks;
+    // a segment: as many chunks as leave a compute unit two workgroups, at
+    // least two a wave (the fetches run two ahead); 16 of them take at most
+    // 148 KB in any variant
+    auto lds_of = [&](int seg) {
+        return 64 + (size_t)WAVES * slice<FMT>() +
+               (size_t)seg * R * (ACT_STRIDE + 32 * (has_min<FMT>() ? 2 : 1)) +
+               (ks > 1 ? (size_t)seg * TW * MATS * R * 64 : 0);
+    };
+    int seg = SEG;
+    while (seg > 2 * ks && lds_of(seg) > 80 * 1024) seg /= 2;
+    a.seg = (int32_t)(C < seg ? C : seg);
+    const size_t lds = lds_of(a.seg);
+    static std::atomic<int> state[64];
+    const int rc = raise_lds_limit(reinterpret_cast<const void*>(&k_moe_rows<FMT, PAIR, NI, SCAN>), state);
+    if (rc) return rc;
+    for (int64_t at = 0; at < items; at += MOST_Y) {   // a grid's second dimension ends at 65535
+        a.item0 = (int32_t)at;
+        hipLaunchKernelGGL((k_moe_rows<FMT, PAIR, NI, SCAN>),
+                           dim3((unsigned)((tiles + TW - 1) / TW),
+                                (unsigned)(items - at < MOST_Y ? items - at : MOST_Y)),
+                           dim3(64 * WAVES), lds, s, a);
+        const int rc2 = (int)hipGetLastError();
+        if (rc2) return rc2;
+    }
+    return 0;
+}
+
+template <int FMT, bool PAIR> int launch_fmt(const MoeArgs& m, RowsArgs& a, hipStream_t s) {
+    const int R = moe_rows(m.P, m.top);
+    if (m.P <= MOE_SCAN)
+        return R == 4 ? launch_rows<FMT, PAIR, 1, true>(m, a, s)
+             : R == 8 ? launch_rows<FMT, PAIR, 2, true>(m, a, s)
+                      : launch_rows<FMT, PAIR, 4, true>(m, a, s);
+    return R == 4 ? launch_rows<FMT, PAIR, 1, false>(m, a, s)
+         : R == 8 ? launch_rows<FMT, PAIR, 2, false>(m, a, s)
+                  : launch_rows<FMT, PAIR, 4, false>(m, a, s);
+}
+
+template <int FMT> int launch_any(const MoeArgs& m, RowsArgs& a, hipStream_t s) {
+    return m.w2 ? launch_fmt<FMT, true>(m, a, s) : launch_fmt<FMT, false>(m, a, s);
+}
+
+// ----------------------------------------------------------- combination ----
+// y[t][n] = sum over the token's slots with an expert, ascending, of
+// weight * yp: one fma each from +0.  V: outputs a thread.
+template <int V>
+__global__ __launch_bounds__(256) void k_moe_combine(const float* __restrict__ yp,
+                                                     const int32_t* __restrict__ idx,
+                                                     const float* __restrict__ weight, int64_t T,
+                                                     int top, int E, int64_t N,
+                                                     float* __restrict__ y) {
+    const int64_t per = N / V;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < T * per;
+         i += (int64_t)gridDim.x * 256) {
+        const int64_t t = i / per, n = (i - t * per) * V;
+        float s[V];
+#pragma unroll
+        for (int v = 0; v < V; v++) s[v] = 0.0f;
+        for (int j = 0; j < top; j++) {
+            const int64_t p = t * top + j;
+            if ((unsigned)idx[p] >= (unsigned)E) continue;
+            const float w = weight[p];
+            if constexpr (V == 4) {
+                const float4 f = *reinterpret_cast<const float4*>(yp + p * N + n);
+                s[0] = fmaf(w, f.x, s[0]);
+                s[1] = fmaf(w, f.y, s[1]);
+                s[2] = fmaf(w, f.z, s[2]);
+                s[3] = fmaf(w, f.w, s[3]);
+            } else {
+                s[0] = fmaf(w, yp[p * N + n], s[0]);
+            }
+        }
+        if constexpr (V == 4)
+            *reinterpret_cast<float4*>(y + t * N + n) = make_float4(s[0], s[1], s[2], s[3]);
+        else
+            y[t * N + n] = s[0];
+    }
+}
+
+}  // namespace
+
+int launch_moe_product(const MoeArgs& m, hipStream_t s) {
+    const MoeWork L = moe_work(m.P, m.top, m.per, m.E, m.K);
+    const bool plan = m.P > MOE_SCAN;
+    RowsArgs a{};
+    a.w = m.w;
+    a.w2 = m.w2;
+    a.N = m.N;
+    a.K = m.K;
+    a.E = (int32_t)m.E;
+    a.P = (int32_t)m.P;
+    a.per = m.per;
+    a.idx = m.idx;
+    a.blocks = m.x ? m.work + L.blocks : m.xq;
+    a.items = reinterpret_cast<const int32_t*>(m.work + L.items);
+    a.order = reinterpret_cast<const int32_t*>(m.work + L.order);
+    a.count = reinterpret_cast<const int32_t*>(m.work + L.count);
+    a.y = m.y;
+    if (m.x || plan) {
+        PrepArgs p{};
+        p.x = m.x;
+        p.blocks = m.work + L.blocks;
+        p.nblocks = m.x ? m.P / m.per * (m.K / 32) : 0;
+        p.idx = m.idx;
+        p.P = a.P;
+        p.E = a.E;
+        p.R = moe_rows(m.P, m.top);
+        p.planners = plan ? a.E + 1 : 0;
+        p.items = reinterpret_cast<int32_t*>(m.work + L.items);
+        p.order = reinterpret_cast<int32_t*>(m.work + L.order);
+        p.count = reinterpret_cast<int32_t*>(m.work + L.count);
+        p.a16 = aligned16(m.x);
+        const int64_t grid = p.planners + (p.nblocks + PREP / 8 - 1) / (PREP / 8);
+        hipLaunchKernelGGL(k_moe_prep, dim3((unsigned)grid), dim3(PREP), 0, s, p);
+        const int rc = (int)hipGetLastError();
+        if (rc) return rc;
+    }
+    switch (m.type) {
+    case T_Q8_0: return launch_any<T_Q8_0>(m, a, s);
+    case T_Q4_0: return launch_any<T_Q4_0>(m, a, s);
+    case T_Q5_0: return launch_any<T_Q5_0>(m, a, s);
+    case T_Q4_1: return launch_any<T_Q4_1>(m, a, s);
+    case T_Q5_1: return launch_any<T_Q5_1>(m, a, s);
+    case T_Q8_1: return launch_any<T_Q8_1>(m, a, s);
+    case T_Q4_K: return launch_any<T_Q4_K>(m, a, s);
+    case T_Q6_K: return launch_any<T_Q6_K>(m, a, s);
+    }
+    return (int)hipErrorInvalidValue;
+}
+
+int launch_moe_combine(const float* yp, const int32_t* idx, const float* weight, int64_t T,
+                       int top, int64_t E, int64_t N, float* y, hipStream_t s) {
+    const bool four = N % 4 == 0 && aligned16(y);
+    const int64_t blocks = ((four ? T * (N / 4) : T * N) + 255) / 256;
+    const dim3 grid((unsigned)(blocks < (1 << 20) ? blocks : (1 << 20)));
+    if (four)
+        hipLaunchKernelGGL(k_moe_combine<4>, grid, dim3(256), 0, s, yp, idx, weight, T, top, (int)E,
+                           N, y);
+    else
+        hipLaunchKernelGGL(k_moe_combine<1>, grid, dim3(256), 0, s, yp, idx, weight, T, top, (int)E,
+                           N, y);
+    return (int)hipGetLastError();
+}
+
+}  // namespace qmv

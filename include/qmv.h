@@ -502,6 +502,73 @@ int qmv_kv_attention(const qmv_kv* kv, const qmv_kv_batch* seqs, const float* q,
                      int q_heads, float scale, int64_t window, float* out, void* work,
                      void* stream);
 
+/* ---- A mixture of experts in the place of a feed-forward block ----
+ * ("Architecture", "The package map": the MoE router of the forward pass.)  A
+ * token's logits name its experts (qmv_moe_route); the experts' matrices stand
+ * one after another in a tensor, expert e's N rows of K elements at e * N *
+ * the bytes of a row, each in GGUF block layout, 16-byte aligned at the first.
+ * A pair is a token and one of its `top` slots, p = token * top + slot, and
+ * idx[p] its expert; a number outside 0 .. E-1 is a slot without an expert (a
+ * token without one has none of its own: its rows of h and y are 0).  idx is
+ * read when the work runs, so a captured call follows it; whatever it holds,
+ * nothing outside the described buffers is touched.  The same expert may stand
+ * in several slots of a token.
+ * Limits: T * top <= QMV_MOE_MAX_PAIRS, E <= QMV_MOE_MAX_EXPERTS, top <=
+ * QMV_MOE_MAX_TOP, N <= 2^24, fewer than 2^33 activations. */
+#define QMV_MOE_MAX_PAIRS (1 << 20)
+#define QMV_MOE_MAX_EXPERTS 1024
+#define QMV_MOE_MAX_TOP 32
+enum qmv_moe_score { QMV_MOE_SOFTMAX = 0, QMV_MOE_SIGMOID = 1 };
+
+/* Routes T tokens: logits [T][E] f32, idx and weight [T][top].
+ *   s_e   the softmax (over all E) or the sigmoid of the logits, in f64
+ *   c_e   what experts are chosen by: fl(s_e) + bias_e in f32 (bias [E], or
+ *         NULL: fl(s_e)).  For a softmax without a bias, unless groups go by
+ *         two experts, the logit itself: the softmax keeps its order.
+ * With groups > 1 (E a multiple of it, at most 64; groups of E / groups
+ * experts side by side), only the top_groups best groups stay: by the largest
+ * c of the group (group_top 1) or the sum in f32 of its two largest (2).  The
+ * `top` experts of the largest c follow, in descending order; of equals, of
+ * groups too, the lowest number first.  weight = scale * s_e, divided by the
+ * sum of s over the chosen experts with renorm != 0 (0 where that sum is 0),
+ * in f64 and rounded once.  An expert whose logit or bias is -inf or NaN is
+ * not available (its s is left out of no sum, being 0, unless it is the bias
+ * that excludes it); where fewer than `top` are, the slots left have idx -1
+ * and weight 0.  An infinite logit is a softmax's whole weight, shared with
+ * its equals.  top <= top_groups * (E / groups); scale finite. */
+int qmv_moe_route(const float* logits, int64_t T, int64_t E, int score, const float* bias,
+                  int groups, int top_groups, int group_top, int top, int renorm, float scale,
+                  int32_t* idx, float* weight, void* stream);
+
+/* Bytes of workspace of the two products below (16-byte aligned, used by one
+ * call at a time, need not be cleared); 0 for an invalid shape. */
+size_t qmv_moe_gateup_bytes(int64_t T, int top, int64_t E, int64_t N, int64_t K);
+size_t qmv_moe_down_bytes(int64_t T, int top, int64_t E, int64_t N, int64_t K);
+
+/* Gate and up products of each pair's expert with the SwiGLU:
+ *   h[p] = silu(Wg[e] x[t]) * (Wu[e] x[t]),  e = idx[p], t = p / top
+ * w_gate, w_up: E matrices N x K of one type; h [T * top][N] f32, 4-byte
+ * aligned, overlapping nothing else.  Either x [T][K] f32 is given (4-byte
+ * aligned) and quantised into the workspace, or xq (16-byte aligned), whose
+ * first T * (K/32) * 34 bytes are the rows' Q8_0 blocks as quantize_act_q8_0
+ * or qmv_add_rmsnorm_q8_0 leave them; the other is NULL.  Each row is
+ * bit-identical to qmv_launch_gateup_swiglu on that expert's matrices with
+ * B = 1, whatever the other pairs are. */
+int qmv_moe_gateup_swiglu(int type, const void* w_gate, const void* w_up, int64_t E, int64_t N,
+                          int64_t K, const int32_t* idx, int64_t T, int top, const float* x,
+                          const void* xq, float* h, void* work, void* stream);
+
+/* Down products and the weighted sum over a token's experts:
+ *   y[t] = sum over slots j with an expert of weight[t][j] * (W[e] h[t * top + j])
+ * w: E matrices N x K; weight [T][top] f32; y [T][N] f32, 4-byte aligned.
+ * Either h [T * top][K] f32 is given and quantised to Q8_0, or hq holds the
+ * rows' Q8_0 blocks, as above.  Each product is bit-identical to qmv_launch on
+ * that expert's matrix with B = 1; the sum starts at +0 and adds the slots in
+ * ascending order, fma(weight, product, sum).  y overlaps nothing else. */
+int qmv_moe_down(int type, const void* w, int64_t E, int64_t N, int64_t K, const int32_t* idx,
+                 const float* weight, int64_t T, int top, const float* h, const void* hq, float* y,
+                 void* work, void* stream);
+
 /* Static text for a status code. */
 const char* qmv_strerror(int code);
 
