@@ -39,17 +39,14 @@ struct MoeArgs {
     float* y;               // [P][N]; a gate/up pair's rows without an expert become 0, others are left alone
 };
 
-// Workspace of a product: [0, blocks) the Q8_0 blocks of x, then the plan:
-//   items  [most items][4] int32  expert (E: rows without one), first place in `order`, rows, 0
-//   order  [P] int32              the pairs, those of one expert side by side, ascending
-//   count  int32                  items
-struct MoeWork {
-    int64_t blocks, items, order, count, total;
-};
-// Rows of an expert in one item, at most: as many as it can have when a
-// token's experts differ, up to the 16 of a matrix instruction.
-inline int moe_rows(int64_t P, int top) {
+// Rows of an expert in one item, at most, which also names the kernel: up to
+// 16 as many as an expert can have when a token's experts differ (matrix
+// products of 16 columns, qmv_moe_rows.hip), 64 or 128 a tile of the GEMM
+// (qmv_moe_gemm.hip), by the pairs an expert has on average.
+inline int moe_rows(int64_t P, int top, int64_t E) {
     const int64_t T = P / top;
+    if (P >= 96 * E) return 128;
+    if (P >= 24 * E) return 64;
     return T <= 4 ? 4 : T <= 8 ? 8 : 16;
 }
 // Items of P pairs, at most: every item but an expert's last is full.
@@ -57,16 +54,34 @@ inline int64_t moe_most_items(int64_t P, int64_t E, int rows) {
     const int64_t kinds = P < E + 1 ? P : E + 1;
     return kinds + (P - kinds) / rows;
 }
+
+// Workspace of a product: the activations, then the plan.
+//   blocks the Q8_0 blocks of x; for the GEMM instead the codes as f16 [rows][K],
+//   da     [rows][K / 32] fp16 scales, and
+//   ca     [rows][K / 32] f32 scale times the block's code sum
+//   items  [most items][4] int32  expert (E: rows without one), its first place in `order`, its
+//                                 rows, its first item
+//   order  [P] int32              the pairs, those of one expert side by side, ascending
+//   count  int32                  items
+struct MoeWork {
+    int64_t blocks, da, ca, items, order, count, total;
+};
 inline MoeWork moe_work(int64_t P, int top, int per, int64_t E, int64_t K) {
+    const int R = moe_rows(P, top, E);
+    const int64_t rows = P / per, nb = K / 32;
     MoeWork w;
     w.blocks = 0;
-    w.items = align256(P / per * (K / 32) * 34);
-    w.order = w.items + align256(moe_most_items(P, E, moe_rows(P, top)) * 16);
+    w.da = R >= 64 ? align256(rows * K * 2) : align256(rows * nb * 34);
+    w.ca = w.da + (R >= 64 ? align256(rows * nb * 2) : 0);
+    w.items = w.ca + (R >= 64 ? align256(rows * nb * 4) : 0);
+    w.order = w.items + align256(moe_most_items(P, E, R) * 16);
     w.count = w.order + align256(P * 4);
     w.total = w.count + 256;
     return w;
 }
+// The product: its preparation and the kernel that moe_rows names.
 int launch_moe_product(const MoeArgs& a, hipStream_t s);
+int launch_moe_gemm(const MoeArgs& a, hipStream_t s);
 
 // y[t][n] = sum over slots j with an expert of weight[t][j] * yp[t * top + j][n],
 // s = fma(weight, yp, s) from +0 in ascending j.

@@ -104,9 +104,13 @@ __device__ __forceinline__ float swiglu(float g, float u) {
 // ascending order to their place, and e's items: no workgroup waits for
 // another.  Its waves each take a run of the pairs, count and then write.
 struct PrepArgs {
-    const float* x;
-    uint8_t* blocks;
-    int64_t nblocks;     // Q8_0 blocks of x (0: nothing to quantise)
+    const float* x;      // or NULL: the blocks at xq
+    const uint8_t* xq;
+    uint8_t* blocks;     // Q8_0 blocks, or (gemm) f16 codes
+    uint16_t* da;        // gemm: fp16 scales
+    float* ca;           // gemm: scale times code sum
+    int64_t nblocks;     // blocks to quantise (0: none)
+    bool gemm;
     const int32_t* idx;
     int32_t P, E, R;
     int32_t planners;    // E + 1, or 0
@@ -167,40 +171,65 @@ __global__ __launch_bounds__(PREP) void k_moe_prep(PrepArgs a) {
         }
         for (int i = tid; i < items; i += PREP)
             reinterpret_cast<int4*>(a.items)[item + i] =
-                make_int4(e, start + i * a.R, min(a.R, n - i * a.R), 0);
+                make_int4(e, start, n, item);
         if (e == E && tid == 0) *a.count = item + items;
         return;
     }
     // eight lanes a block, four elements each
     const int64_t b = (int64_t)((int)blockIdx.x - a.planners) * (PREP / 8) + (tid >> 3);
     const int sub = tid & 7;
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (b < a.nblocks) {
-        const float* xb = a.x + b * 32 + 4 * sub;
-        if (a.a16) {
-            const float4 f = *reinterpret_cast<const float4*>(xb);
-            v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; i++) v[i] = xb[i];
-        }
-    }
-    float amax = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
-    const float d = amax / 127.0f;
-    const float r = 1.0f / d, id = __builtin_isinf(r) ? 0.0f : r;
+    const bool live = b < a.nblocks;
     uint32_t c = 0;
+    _Float16 d16 = 0;
+    if (a.x) {
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (live) {
+            const float* xb = a.x + b * 32 + 4 * sub;
+            if (a.a16) {
+                const float4 f = *reinterpret_cast<const float4*>(xb);
+                v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+            } else {
 #pragma unroll
-    for (int i = 0; i < 4; i++) c |= ((uint32_t)(int)roundf(v[i] * id) & 0xFFu) << (8 * i);
-    if (b >= a.nblocks) return;
+                for (int i = 0; i < 4; i++) v[i] = xb[i];
+            }
+        }
+        float amax = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
+        const float d = amax / 127.0f;
+        const float r = 1.0f / d, id = __builtin_isinf(r) ? 0.0f : r;
+#pragma unroll
+        for (int i = 0; i < 4; i++) c |= ((uint32_t)(int)roundf(v[i] * id) & 0xFFu) << (8 * i);
+        d16 = (_Float16)d;
+    } else if (live) {
+        const uint16_t* in = reinterpret_cast<const uint16_t*>(a.xq + b * 34);
+        c = (uint32_t)in[1 + 2 * sub] | ((uint32_t)in[2 + 2 * sub] << 16);
+        __builtin_memcpy(&d16, in, 2);
+    }
+    uint16_t dbits;
+    __builtin_memcpy(&dbits, &d16, 2);
+    if (a.gemm) {
+        int S = __builtin_amdgcn_sdot4((int)c, 0x01010101, 0, false);
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) S += __shfl_xor(S, o);
+        if (!live) return;
+        _Float16 h[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) h[i] = (_Float16)(float)(int8_t)(c >> (8 * i));
+        uint2 two;
+        __builtin_memcpy(&two, h, 8);
+        *reinterpret_cast<uint2*>(a.blocks + b * 64 + 8 * sub) = two;
+        if (sub == 0) {
+            a.da[b] = dbits;
+            a.ca[b] = (float)d16 * (float)S;
+        }
+        return;
+    }
+    if (!live) return;
     uint16_t* out = reinterpret_cast<uint16_t*>(a.blocks + b * 34);
     out[1 + 2 * sub] = (uint16_t)c;
     out[2 + 2 * sub] = (uint16_t)(c >> 16);
-    if (sub == 0) {
-        const _Float16 h = (_Float16)d;
-        __builtin_memcpy(out, &h, 2);
-    }
+    if (sub == 0) out[0] = dbits;
 }
 
 // --------------------------------------------------------------- product ----
@@ -375,10 +404,12 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_moe_rows(RowsArgs a) {
             left &= ~m;
         }
     } else if (a.item0 + (int)blockIdx.y < *a.count) {
-        const int4 it = reinterpret_cast<const int4*>(a.items)[a.item0 + (int)blockIdx.y];
+        const int at = a.item0 + (int)blockIdx.y;
+        const int4 it = reinterpret_cast<const int4*>(a.items)[at];
+        const int done = uniform((at - it.w) * R);    // the expert's rows in items before this one
         e = uniform(it.x);
-        rows = uniform(it.z);
-        if (tid < rows) pairs[tid] = a.order[it.y + tid];
+        rows = min(R, uniform(it.z) - done);
+        if (tid < rows) pairs[tid] = a.order[it.y + done + tid];
     }
     if (e < 0) return;
     const int64_t N = a.N, K = a.K;
@@ -651,7 +682,7 @@ int launch_rows(const MoeArgs& m, RowsArgs& a, hipStream_t s) {
 }
 
 template <int FMT, bool PAIR> int launch_fmt(const MoeArgs& m, RowsArgs& a, hipStream_t s) {
-    const int R = moe_rows(m.P, m.top);
+    const int R = moe_rows(m.P, m.top, m.E);
     if (m.P <= MOE_SCAN)
         return R == 4 ? launch_rows<FMT, PAIR, 1, true>(m, a, s)
              : R == 8 ? launch_rows<FMT, PAIR, 2, true>(m, a, s)
@@ -706,7 +737,6 @@ __global__ __launch_bounds__(256) void k_moe_combine(const float* __restrict__ y
 
 int launch_moe_product(const MoeArgs& m, hipStream_t s) {
     const MoeWork L = moe_work(m.P, m.top, m.per, m.E, m.K);
-    const bool plan = m.P > MOE_SCAN;
     RowsArgs a{};
     a.w = m.w;
     a.w2 = m.w2;
@@ -721,15 +751,21 @@ int launch_moe_product(const MoeArgs& m, hipStream_t s) {
     a.order = reinterpret_cast<const int32_t*>(m.work + L.order);
     a.count = reinterpret_cast<const int32_t*>(m.work + L.count);
     a.y = m.y;
+    const int R = moe_rows(m.P, m.top, m.E);
+    const bool gemm = R >= 64, plan = gemm || m.P > MOE_SCAN;
     if (m.x || plan) {
         PrepArgs p{};
         p.x = m.x;
+        p.xq = m.xq;
         p.blocks = m.work + L.blocks;
-        p.nblocks = m.x ? m.P / m.per * (m.K / 32) : 0;
+        p.da = reinterpret_cast<uint16_t*>(m.work + L.da);
+        p.ca = reinterpret_cast<float*>(m.work + L.ca);
+        p.nblocks = m.x || gemm ? m.P / m.per * (m.K / 32) : 0;
+        p.gemm = gemm;
         p.idx = m.idx;
         p.P = a.P;
         p.E = a.E;
-        p.R = moe_rows(m.P, m.top);
+        p.R = R;
         p.planners = plan ? a.E + 1 : 0;
         p.items = reinterpret_cast<int32_t*>(m.work + L.items);
         p.order = reinterpret_cast<int32_t*>(m.work + L.order);
@@ -740,6 +776,7 @@ int launch_moe_product(const MoeArgs& m, hipStream_t s) {
         const int rc = (int)hipGetLastError();
         if (rc) return rc;
     }
+    if (gemm) return launch_moe_gemm(m, s);
     switch (m.type) {
     case T_Q8_0: return launch_any<T_Q8_0>(m, a, s);
     case T_Q4_0: return launch_any<T_Q4_0>(m, a, s);

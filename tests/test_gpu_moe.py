@@ -109,8 +109,8 @@ def test_route_values_that_are_not_finite(g, sigmoid, renorm, groups, biased):
 
 # ----------------------------------------------------------------- products --
 
-def expert_blobs(fmt, E, N, K, seed):
-    return [synth.weights(fmt, N, K, seed + e)[0] for e in range(E)]
+def expert_blobs(fmt, E, N, K, seed, **k):
+    return [synth.weights(fmt, N, K, seed + e, **k)[0] for e in range(E)]
 
 
 def pick(rng, T, top, E, kind):
@@ -138,9 +138,9 @@ def guards_hold(whole, n, fill=0xA5):
     return (raw[:256] == fill).all() and (raw[256 + n:] == fill).all()
 
 
-def check_gateup(g, fmt, T, top, E, N, K, kind, seed=0, staged=False):
+def check_gateup(g, fmt, T, top, E, N, K, kind, seed=0, staged=False, **k):
     rng = np.random.default_rng(seed + T * 7 + N)
-    gates, ups = expert_blobs(fmt, E, N, K, seed + 10), expert_blobs(fmt, E, N, K, seed + 500)
+    gates, ups = expert_blobs(fmt, E, N, K, seed + 10, **k), expert_blobs(fmt, E, N, K, seed + 500, **k)
     x, idx = synth.activations(T, K, seed + 3), pick(rng, T, top, E, kind)
     h, whole = guarded((T, top, N))
     n = g.qmv_moe_gateup_bytes(T, top, E, N, K)
@@ -152,9 +152,9 @@ def check_gateup(g, fmt, T, top, E, N, K, kind, seed=0, staged=False):
     assert guards_hold(whole, h.numel() * 4) and guards_hold(wwhole, n)
 
 
-def check_down(g, fmt, T, top, E, N, K, kind, seed=0, staged=False):
+def check_down(g, fmt, T, top, E, N, K, kind, seed=0, staged=False, **k):
     rng = np.random.default_rng(seed + T * 7 + N)
-    blobs = expert_blobs(fmt, E, N, K, seed + 10)
+    blobs = expert_blobs(fmt, E, N, K, seed + 10, **k)
     h = synth.activations(T * top, K, seed + 3).reshape(T, top, K)
     idx = pick(rng, T, top, E, kind)
     weight = rng.random((T, top)).astype(np.float32)
@@ -218,3 +218,32 @@ def test_no_pair_has_an_expert(g):
         assert not h.cpu().numpy().view(np.uint32).any()
         y = g.moe_down(g.Q8_0, w, 20, 64, idx, torch.full((T, top), float("nan"), device="cuda"), h=torch.randn(T, top, 64, device="cuda"))
         assert not y.cpu().numpy().view(np.uint32).any()
+
+
+# Tiles of 64 and 128 rows of an expert, full and part full; a last tile of a few weight rows; short last chunks, an odd
+# number of blocks
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T,top,E,N,K", [
+    (48, 1, 2, 33, 32), (30, 2, 2, 130, 288), (100, 2, 3, 70, 512), (97, 1, 1, 17, 96), (150, 2, 3, 129, 512 + 64),
+    (260, 1, 2, 68, 896)])
+@pytest.mark.parametrize("kind", ["any", "none"])
+def test_many_rows(g, fmt, T, top, E, N, K, kind):
+    K = K if fits(fmt, K) else -(-K // 256) * 256
+    check_gateup(g, fmt, T, top, E, N, K, kind, staged=kind == "any")
+    check_down(g, fmt, T, top, E, N, K, kind, staged=kind == "any")
+    check_down(g, fmt, T * top, 1, E, N, K, kind)
+
+
+@pytest.mark.parametrize("kind", ["one", "different"])
+@pytest.mark.parametrize("T,top,E", [(70, 2, 3), (300, 2, 4)])
+def test_many_rows_unevenly(g, kind, T, top, E):
+    check_gateup(g, synth.Q4_K, T, top, E, 100, 512, kind)
+    check_down(g, synth.Q8_0, T, top, E, 100, 512, kind)
+
+
+# Q6_K's int8 sub-scales over their whole range (odd ones beyond 64 do not fold into f16), and a few rows of them
+@pytest.mark.parametrize("T,top,E", [(3, 2, 3), (40, 2, 3), (70, 1, 2), (200, 2, 2)])
+@pytest.mark.parametrize("s_range", [(-128, 127), (-66, 66), (127, 127), (-128, -128)])
+def test_q6_k_scales(g, T, top, E, s_range):
+    check_gateup(g, synth.Q6_K, T, top, E, 80, 768, "any", s_range=s_range)
+    check_down(g, synth.Q6_K, T * top, 1, E, 80, 768, "any", s_range=s_range)
