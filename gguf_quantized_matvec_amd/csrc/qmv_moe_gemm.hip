@@ -186,21 +186,26 @@ __device__ __forceinline__ void decode(const Raw<FMT>& r, int b, uint32_t (&o)[1
             const uint32_t c = ((r.ql[i] >> (4 * (kk >> 1))) & 0x0F0F0F0Fu) |
                                (((r.qh[i] >> (2 * kk)) & 0x03030303u) << 4);
             codes4(c, 32.0f, o + 2 * i);
-            // the codes' lowest bits, should they be needed
-            s.x |= ((c & 1u) | ((c >> 7) & 2u) | ((c >> 14) & 4u) | ((c >> 21) & 8u)) << (4 * i);
         }
         if (unfit(r)) {
-            s.x &= ((s0 & 1) ? 0xFFFFu : 0u) | ((s1 & 1) ? 0xFFFF0000u : 0u);
-        } else {
-            s.x = 0;
-        }
+            // the codes' lowest bits where the sub-scale is odd
 #pragma unroll
-        for (int i = 0; i < 16; i++) {
-            const _Float16 f = i < 8 ? f0 : f1;
-            if (s.x)
+            for (int i = 0; i < 8; i++) {
+                const uint32_t c = r.ql[i] >> (4 * (kk >> 1));
+                if ((i < 4 ? s0 : s1) & 1)
+                    s.x |= ((c & 1u) | ((c >> 7) & 2u) | ((c >> 14) & 4u) | ((c >> 21) & 8u)) << (4 * i);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+                const _Float16 f = i < 8 ? f0 : f1;
                 o[i] = as_u32(__builtin_elementwise_fma(as_h2(o[i]), h2{f, f}, -as_h2(two_bits(s.x, 2 * i))));
-            else
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+                const _Float16 f = i < 8 ? f0 : f1;
                 o[i] = as_u32(as_h2(o[i]) * h2{f, f});
+            }
         }
     } else {
         // 16 bytes of nibbles: the low ones are elements 0..15, the high ones 16..31
@@ -231,10 +236,7 @@ __device__ __forceinline__ void decode(const Raw<FMT>& r, int b, uint32_t (&o)[1
 }
 
 // ------------------------------------------------------------------- GEMM ----
-constexpr int SB = 2;             // blocks a step
-constexpr int PR = 4 * SB;        // 16-byte pieces of a tile row in a step
 constexpr int TN = 128;           // weight rows of a workgroup
-constexpr int THREADS = 256;
 
 struct GemmArgs {
     const uint8_t *w, *w2;
@@ -248,13 +250,19 @@ struct GemmArgs {
     bool vec;                      // rows of y begin 16-byte aligned
 };
 
-// Piece q of tile row r: rows of 128 bytes, pieces exchanged so that 16
-// consecutive rows' same piece (one pass of a 16-byte read) meets all banks.
-__device__ __forceinline__ int slot(int r, int q) { return r * PR + (q ^ ((r >> 1) & 7)); }
+// Where piece q of tile row r stands, rows of PR 16-byte pieces: pieces change
+// places so that 16 consecutive rows' same piece (one pass of a 16-byte read)
+// meets all banks.
+template <int PR> __device__ __forceinline__ int slot(int r, int q) {
+    return r * PR + (q ^ (PR == 16 ? r & 15 : (r >> 1) & 7));
+}
 
-template <int FMT, bool PAIR, int AT>
-__global__ __launch_bounds__(THREADS, 2) void k_moe_gemm(GemmArgs a) {
-    constexpr int TM = 64 * AT;                       // rows of the expert in a tile
+template <int FMT, bool PAIR, int WA>
+__global__ __launch_bounds__(128 * WA, 2) void k_moe_gemm(GemmArgs a) {
+    constexpr int THREADS = 128 * WA;                 // 2 x WA waves
+    constexpr int SB = WA;                            // blocks a step: a weight block a thread
+    constexpr int PR = 4 * SB;                        // 16-byte pieces of a tile row in a step
+    constexpr int TM = 32 * WA;                       // rows of the expert in a tile
     constexpr int COLS = PAIR ? TN / 2 : TN;          // outputs of a row
     constexpr bool MIN = has_min<FMT>();
     // two objects a kind, not one of two halves: the compiler sees that reads
@@ -299,7 +307,7 @@ __global__ __launch_bounds__(THREADS, 2) void k_moe_gemm(GemmArgs a) {
     const int H = (nb + SB - 1) / SB;                 // steps
 
     // this thread's weight row and block of each step, and activation row for the scales
-    const int sr = tid >> 1, sk = tid & 1;
+    const int sr = tid / SB, sk = tid % SB;
     const uint8_t* wrow;
     {
         int64_t n = n0 + (PAIR ? 32 * (sr >> 6) + (sr & 31) : sr);
@@ -309,23 +317,27 @@ __global__ __launch_bounds__(THREADS, 2) void k_moe_gemm(GemmArgs a) {
     }
     const bool scales = sr < TM;
     const int64_t srow = (int64_t)(pairs[scales ? sr : 0] / a.per) * nb;
-    // activation pieces: an instruction fills 64 slots, 8 tile rows; lane l the
-    // slot l % 8 of row l / 8
-    const uint8_t* asrc[2 * AT];
-    int apiece[2 * AT];
+    // activation pieces: an instruction fills 64 slots, 64 / PR tile rows; lane
+    // l the slot l % PR of row l / PR
+    constexpr int NA = TM * PR / THREADS, AR = 64 / PR;
+    const uint8_t* asrc[NA];
 #pragma unroll
-    for (int i = 0; i < 2 * AT; i++) {
-        const int r = 16 * AT * wv + 8 * i + (lane >> 3);
-        apiece[i] = (lane & 7) ^ ((r >> 1) & 7);
-        asrc[i] = a.codes + ((int64_t)(pairs[r] / a.per) * K + 8 * apiece[i]) * 2;
+    for (int i = 0; i < NA; i++) {
+        const int r = AR * (NA * wv + i) + lane / PR;
+        const int piece = slot<PR>(r, lane % PR) - r * PR;    // the exchange is its own inverse
+        asrc[i] = a.codes + ((int64_t)(pairs[r] / a.per) * K + 8 * piece) * 2;
     }
     auto issue_a = [&](int h, uint4* la) {
 #pragma unroll
-        for (int i = 0; i < 2 * AT; i++) {
+        for (int i = 0; i < NA; i++) {
             const uint8_t* src = asrc[i] + (int64_t)h * (SB * 64);
-            // a block past the row's end (an odd number of blocks): any bytes of the row, times a scale of 0
-            if (SB * h + (apiece[i] >> 2) >= nb) src -= 64;
-            __builtin_amdgcn_global_load_lds(src, (lds_void*)(la + (16 * AT * wv + 8 * i) * PR), 16, 0, 0);
+            if (SB * h + SB > nb) {
+                // blocks past the row's end: its last one again, times a weight
+                // scale of 0 (of the i-th piece, block (lane % PR / 4) ^ i)
+                const int past = SB * h + (((lane % PR) >> 2) ^ i) - (nb - 1);
+                src -= past > 0 ? 64 * past : 0;
+            }
+            __builtin_amdgcn_global_load_lds(src, (lds_void*)(la + AR * (NA * wv + i) * PR), 16, 0, 0);
         }
     };
     struct {
@@ -350,7 +362,7 @@ __global__ __launch_bounds__(THREADS, 2) void k_moe_gemm(GemmArgs a) {
         const bool have = b < nb;
 #pragma unroll
         for (int q = 0; q < 4; q++)
-            lw[slot(sr, 4 * sk + q)] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            lw[slot<PR>(sr, 4 * sk + q)] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
         ws[PB][sk][sr] = have ? s.d : 0u;
         if constexpr (MIN || FMT == T_Q6_K) wx[PB][sk][sr] = have ? s.x : 0u;
         if constexpr (FMT == T_Q6_K) {
@@ -362,59 +374,46 @@ __global__ __launch_bounds__(THREADS, 2) void k_moe_gemm(GemmArgs a) {
         }
     };
 
-    float p[2 * AT][16], y[2 * AT][16];     // tile (i, j): weight rows 32 i, activation rows 32 j
-    each<2 * AT>([&](auto t) {
+    float p[2][16], y[2][16];      // of weight rows 0 .. 31 and 32 .. 63 of the wave's
+    each<2>([&](auto i) {
 #pragma unroll
-        for (int c = 0; c < 16; c++) p[t][c] = y[t][c] = 0.0f;
+        for (int c = 0; c < 16; c++) p[i][c] = y[i][c] = 0.0f;
     });
     const v16f zero16 = {};
     const uint32_t first_k = kq ? 0u : ~0u;   // of the rank-1 product only k = 0 counts
-    const int wrow0 = 64 * wn + lr, arow0 = 32 * AT * wa + lr;
+    const int wrow0 = 64 * wn + lr, arow = 32 * wa + lr;
 
-    // the product of the buffers of parity P, a tile at a time: the scheduler
-    // is kept from running ahead with products (and registers) of later tiles;
-    // the other wave of the SIMD fills the gaps
-    auto multiply = [&](auto par, bool odd) {
+    // the product of the buffers of parity P; ODD: a Q6_K step with values that left out a bit
+    auto multiply = [&](auto par, auto odd) {
         constexpr int PB = decltype(par)::value;
         const uint4* lw = PB ? lw1 : lw0;
         const uint4* la = PB ? la1 : la0;
         each<SB>([&](auto bk) {
-            v8h Wf[2][2], Af[AT][2];
+            v8h Af[2];
+            each<2>([&](auto hh) { Af[hh] = __builtin_bit_cast(v8h, la[slot<PR>(arow, 4 * bk + 2 * hh + kq)]); });
+            const v4h As = __builtin_bit_cast(v4h, make_uint2(as[PB][bk][arow], 0u));
+            const float ca = MIN ? ac[PB][bk][MIN ? arow : 0] : 0.0f;
             each<2>([&](auto i) {
+                v8h Wf[2];
                 each<2>([&](auto hh) {
-                    Wf[i][hh] = __builtin_bit_cast(v8h, lw[slot(wrow0 + 32 * i, 4 * bk + 2 * hh + kq)]);
+                    Wf[hh] = __builtin_bit_cast(v8h, lw[slot<PR>(wrow0 + 32 * i, 4 * bk + 2 * hh + kq)]);
                 });
-            });
-            each<AT>([&](auto j) {
-                each<2>([&](auto hh) {
-                    Af[j][hh] = __builtin_bit_cast(v8h, la[slot(arow0 + 32 * j, 4 * bk + 2 * hh + kq)]);
-                });
-            });
-            each<2 * AT>([&](auto t) {
-                constexpr int i = t / AT, j = t % AT;
-                const uint32_t d = ws[PB][bk][wrow0 + 32 * i] & first_k;
-                const v4h Ws = __builtin_bit_cast(v4h, make_uint2(d, 0u));
-                const v4h As = __builtin_bit_cast(v4h, make_uint2(as[PB][bk][arow0 + 32 * j], 0u));
-                if constexpr (AT == 2) {
-                    asm volatile("" : "+v"(Af[j][0]), "+v"(Af[j][1]));
-                }
-                v16f I = __builtin_amdgcn_mfma_f32_32x32x16_f16(Wf[i][0], Af[j][0], zero16, 0, 0, 0);
-                I = __builtin_amdgcn_mfma_f32_32x32x16_f16(Wf[i][1], Af[j][1], I, 0, 0, 0);
-                if constexpr (FMT == T_Q6_K) {
-                    if (odd) {   // what the weights' values left out
-                        const uint32_t w = wx[PB][bk][wrow0 + 32 * i] >> (8 * kq);
-                        each<2>([&](auto hh) {
-                            uint4 o;
-                            o.x = two_bits(w, 16 * hh);
-                            o.y = two_bits(w, 16 * hh + 2);
-                            o.z = two_bits(w, 16 * hh + 4);
-                            o.w = two_bits(w, 16 * hh + 6);
-                            I = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, o), Af[j][hh], I, 0, 0, 0);
-                        });
-                    }
+                const v4h Ws = __builtin_bit_cast(v4h, make_uint2(ws[PB][bk][wrow0 + 32 * i] & first_k, 0u));
+                v16f I = __builtin_amdgcn_mfma_f32_32x32x16_f16(Wf[0], Af[0], zero16, 0, 0, 0);
+                I = __builtin_amdgcn_mfma_f32_32x32x16_f16(Wf[1], Af[1], I, 0, 0, 0);
+                if constexpr (decltype(odd)::value) {   // what the weights' values left out
+                    const uint32_t w = wx[PB][bk][wrow0 + 32 * i] >> (8 * kq);
+                    each<2>([&](auto hh) {
+                        uint4 o;
+                        o.x = two_bits(w, 16 * hh);
+                        o.y = two_bits(w, 16 * hh + 2);
+                        o.z = two_bits(w, 16 * hh + 4);
+                        o.w = two_bits(w, 16 * hh + 6);
+                        I = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, o), Af[hh], I, 0, 0, 0);
+                    });
+                    asm volatile("" : "+v"(I));   // rare: one tile at a time, for the registers
                 }
                 const v16f S = __builtin_amdgcn_mfma_f32_32x32x8f16(Ws, As, zero16, 0, 0, 0);
-                const float ca = MIN ? ac[PB][bk][MIN ? arow0 + 32 * j : 0] : 0.0f;
 #pragma unroll
                 for (int g = 0; g < 4; g++) {
                     float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -423,20 +422,16 @@ __global__ __launch_bounds__(THREADS, 2) void k_moe_gemm(GemmArgs a) {
                     const float fs[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
                     for (int c = 0; c < 4; c++) {
-                        float& o = p[t][4 * g + c];
+                        float& o = p[i][4 * g + c];
                         o = fmaf(I[4 * g + c], S[4 * g + c], o);
                         if constexpr (MIN) o = fmaf(fs[c], ca, o);
                     }
                 }
-                // A tile of the large variant ends before the next one's products
-                // begin: two tiles' results at once do not fit the registers.
-                if constexpr (AT == 2) {
-                    asm volatile("" : "+v"(p[t][0]), "+v"(p[t][1]), "+v"(p[t][2]), "+v"(p[t][3]), "+v"(p[t][4]),
-                                 "+v"(p[t][5]), "+v"(p[t][6]), "+v"(p[t][7]), "+v"(p[t][8]), "+v"(p[t][9]),
-                                 "+v"(p[t][10]), "+v"(p[t][11]), "+v"(p[t][12]), "+v"(p[t][13]), "+v"(p[t][14]),
-                                 "+v"(p[t][15]));
-                }
             });
+            // Q6_K's fetched bytes leave no registers for a third tile in flight; a
+            // spill would wait for the fetches, which count as memory loads too
+            if constexpr (FMT == T_Q6_K) __builtin_amdgcn_sched_barrier(0);
+            if constexpr (FMT == T_Q6_K) asm volatile("" : "+v"(p[0][15]), "+v"(p[1][15]) : : "memory");
         });
     };
     auto step = [&](int h, auto par) {
@@ -455,13 +450,17 @@ __global__ __launch_bounds__(THREADS, 2) void k_moe_gemm(GemmArgs a) {
             issue_a(h + 1, Next::value ? la1 : la0);
             if (h + 2 < H) fetch_step(h + 2);
         }
-        multiply(par, odd);
-        if ((h & 3) == 3 || h + 1 == H) {   // the end of a chunk of 8 blocks
-            each<2 * AT>([&](auto t) {
+        if (FMT == T_Q6_K && odd)
+            multiply(par, std::integral_constant<bool, FMT == T_Q6_K>{});
+        else
+            multiply(par, std::false_type{});
+        // the end of a chunk of 8 blocks (of SB = 4 every other step: par says which)
+        if ((SB == 4 ? Par::value == 1 : (h & 3) == 3) || h + 1 == H) {
+            each<2>([&](auto i) {
 #pragma unroll
                 for (int c = 0; c < 16; c++) {
-                    y[t][c] = y[t][c] + p[t][c];
-                    p[t][c] = 0.0f;
+                    y[i][c] = y[i][c] + p[i][c];
+                    p[i][c] = 0.0f;
                 }
             });
         }
@@ -476,43 +475,41 @@ __global__ __launch_bounds__(THREADS, 2) void k_moe_gemm(GemmArgs a) {
         if (h + 1 < H) step(h + 1, std::integral_constant<int, 1>{});
     }
 
-    // lane: row arow0 + 32 j; element c of tile i: weight row 8 (c / 4) + 4 kq + c % 4
-    each<AT>([&](auto j) {
-        if (arow0 + 32 * j >= rows) return;
-        float* out = a.y + pairs[arow0 + 32 * j] * N;
-        each<PAIR ? 1 : 2>([&](auto i) {
+    // lane: row arow; element c of tile i: weight row 8 (c / 4) + 4 kq + c % 4
+    if (arow >= rows) return;
+    float* out = a.y + pairs[arow] * N;
+    each<PAIR ? 1 : 2>([&](auto i) {
 #pragma unroll
-            for (int g = 0; g < 4; g++) {
-                const int64_t n = n0 + (PAIR ? 32 * wn : 64 * wn + 32 * i) + 8 * g + 4 * kq;
-                float v[4];
+        for (int g = 0; g < 4; g++) {
+            const int64_t n = n0 + (PAIR ? 32 * wn : 64 * wn + 32 * i) + 8 * g + 4 * kq;
+            float v[4];
+#pragma unroll
+            for (int c = 0; c < 4; c++)
+                v[c] = PAIR ? swiglu(y[0][4 * g + c], y[1][4 * g + c]) : y[i][4 * g + c];
+            if (a.vec && n + 4 <= N) {
+                *reinterpret_cast<float4*>(out + n) = make_float4(v[0], v[1], v[2], v[3]);
+            } else {
 #pragma unroll
                 for (int c = 0; c < 4; c++)
-                    v[c] = PAIR ? swiglu(y[j][4 * g + c], y[AT + j][4 * g + c]) : y[i * AT + j][4 * g + c];
-                if (a.vec && n + 4 <= N) {
-                    *reinterpret_cast<float4*>(out + n) = make_float4(v[0], v[1], v[2], v[3]);
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 4; c++)
-                        if (n + c < N) out[n + c] = v[c];
-                }
+                    if (n + c < N) out[n + c] = v[c];
             }
-        });
+        }
     });
 }
 
-template <int FMT, bool PAIR, int AT>
+template <int FMT, bool PAIR, int WA>
 int launch_at(const MoeArgs& m, GemmArgs& a, hipStream_t s) {
     constexpr int COLS = PAIR ? TN / 2 : TN;
-    const int64_t tiles = moe_most_items(m.P, m.E, 64 * AT) * ((m.N + COLS - 1) / COLS);
-    hipLaunchKernelGGL((k_moe_gemm<FMT, PAIR, AT>), dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(THREADS),
-                       0, s, a);
+    const int64_t tiles = moe_most_items(m.P, m.E, 32 * WA) * ((m.N + COLS - 1) / COLS);
+    hipLaunchKernelGGL((k_moe_gemm<FMT, PAIR, WA>), dim3((unsigned)((tiles + 7) / 8 * 8)),
+                       dim3(128 * WA), 0, s, a);
     return (int)hipGetLastError();
 }
 
 template <int FMT> int launch_fmt(const MoeArgs& m, GemmArgs& a, hipStream_t s) {
     const bool big = moe_rows(m.P, m.top, m.E) == 128;
-    if (m.w2) return big ? launch_at<FMT, true, 2>(m, a, s) : launch_at<FMT, true, 1>(m, a, s);
-    return big ? launch_at<FMT, false, 2>(m, a, s) : launch_at<FMT, false, 1>(m, a, s);
+    if (m.w2) return big ? launch_at<FMT, true, 4>(m, a, s) : launch_at<FMT, true, 2>(m, a, s);
+    return big ? launch_at<FMT, false, 4>(m, a, s) : launch_at<FMT, false, 2>(m, a, s);
 }
 
 }  // namespace
