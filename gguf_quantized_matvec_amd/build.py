@@ -26,6 +26,7 @@ SOURCES = [(os.path.join(CSRC, "qmv_kernels.hip"), ["-mllvm", "-amdgpu-mfma-vgpr
            (os.path.join(CSRC, "qmv_step_api.cpp"), []),
            (os.path.join(CSRC, "qmv_moe_route.hip"), []),
            (os.path.join(CSRC, "qmv_moe_rows.hip"), ["-mllvm", "-amdgpu-mfma-vgpr-form"]),
+           (os.path.join(CSRC, "qmv_moe_gemv.hip"), []),
            (os.path.join(CSRC, "qmv_moe_gemm.hip"), ["-mllvm", "-amdgpu-mfma-vgpr-form"]),
            (os.path.join(CSRC, "qmv_moe_api.cpp"), []),
            (os.path.join(CSRC, "qmv_api.cpp"), [])]

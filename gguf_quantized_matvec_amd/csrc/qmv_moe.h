@@ -55,8 +55,18 @@ inline int64_t moe_most_items(int64_t P, int64_t E, int rows) {
     return kinds + (P - kinds) / rows;
 }
 
+// A row of activations as k_moe_gemv reads it: C = ceil(K / 256) chunks of 272
+// bytes (256 codes and 16 bytes, so that lanes on different chunks differ in
+// their banks), 8 C scales and, for formats with a minimum, 8 C scales times
+// code sums.
+inline __host__ __device__ int moe_gemv_row(int64_t K, bool min) {
+    const int C = (int)((K / 32 + 7) / 8);
+    return (C * 272 + 8 * C * 4 * (min ? 2 : 1) + 15) & ~15;
+}
+
 // Workspace of a product: the activations, then the plan.
-//   blocks the Q8_0 blocks of x; for the GEMM instead the codes as f16 [rows][K],
+//   blocks the Q8_0 blocks of x; for a single token its rows as above; for the
+//          GEMM the codes as f16 [rows][K],
 //   da     [rows][K / 32] fp16 scales, and
 //   ca     [rows][K / 32] f32 scale times the block's code sum
 //   items  [most items][4] int32  expert (E: rows without one), its first place in `order`, its
@@ -71,7 +81,7 @@ inline MoeWork moe_work(int64_t P, int top, int per, int64_t E, int64_t K) {
     const int64_t rows = P / per, nb = K / 32;
     MoeWork w;
     w.blocks = 0;
-    w.da = R >= 64 ? align256(rows * K * 2) : align256(rows * nb * 34);
+    w.da = R >= 64 ? align256(rows * K * 2) : align256(rows * (nb * 34 + 512) + 2 * rows * nb * 4);
     w.ca = w.da + (R >= 64 ? align256(rows * nb * 2) : 0);
     w.items = w.ca + (R >= 64 ? align256(rows * nb * 4) : 0);
     w.order = w.items + align256(moe_most_items(P, E, R) * 16);
@@ -79,13 +89,21 @@ inline MoeWork moe_work(int64_t P, int top, int per, int64_t E, int64_t K) {
     w.total = w.count + 256;
     return w;
 }
-// The product: its preparation and the kernel that moe_rows names.
+// The products into a.y, by the kernel that fits.
 int launch_moe_product(const MoeArgs& a, hipStream_t s);
+// y[t][n] = sum over slots j with an expert of weight[t][j] * product[t * top + j][n],
+// s = fma(weight, product, s) from +0 in ascending j; a.y: room for the products.
+int launch_moe_down(const MoeArgs& a, const float* weight, float* y, hipStream_t s);
+
+// Many rows of an expert, after the preparation (qmv_moe_gemm.hip).
 int launch_moe_gemm(const MoeArgs& a, hipStream_t s);
 
-// y[t][n] = sum over slots j with an expert of weight[t][j] * yp[t * top + j][n],
-// s = fma(weight, yp, s) from +0 in ascending j.
-int launch_moe_combine(const float* yp, const int32_t* idx, const float* weight, int64_t T,
-                       int top, int64_t E, int64_t N, float* y, hipStream_t s);
+// A single token (qmv_moe_gemv.hip): whether the kernel takes the call, whether
+// it quantises x itself, and the product (a gate/up pair) or the weighted sum
+// into y.  rows: the activations quantised (moe_gemv_row), or NULL: a.x or a.xq.
+bool moe_gemv_fits(const MoeArgs& a);
+bool moe_gemv_quantises(const MoeArgs& a);
+int launch_moe_gemv(const MoeArgs& a, const uint8_t* rows, const float* weight, float* y,
+                    hipStream_t s);
 
 }  // namespace qmv

@@ -109,8 +109,7 @@ int qmv_moe_down(int type, const void* w, int64_t E, int64_t N, int64_t K, const
     float* yp = reinterpret_cast<float*>(wk + qmv::moe_work(T * top, top, 1, E, K).total);
     const qmv::MoeArgs a{type, static_cast<const uint8_t*>(w), nullptr, E, N, K, idx, T * top, top,
                          1, h, static_cast<const uint8_t*>(hq), wk, yp};
-    if ((rc = launched(qmv::launch_moe_product(a, s)))) return rc;
-    return launched(qmv::launch_moe_combine(yp, idx, weight, T, top, E, N, y, s));
+    return launched(qmv::launch_moe_down(a, weight, y, s));
 }
 
 }  // extern "C"

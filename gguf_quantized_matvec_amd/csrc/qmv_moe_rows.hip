@@ -111,6 +111,10 @@ struct PrepArgs {
     float* ca;           // gemm: scale times code sum
     int64_t nblocks;     // blocks to quantise (0: none)
     bool gemm;
+    int32_t row;         // not 0: rows of `row` bytes as k_moe_gemv reads them, of
+    int32_t nb;          // nb blocks, their scales times
+    float back;          // this
+    bool min;            // and scales times code sums
     const int32_t* idx;
     int32_t P, E, R;
     int32_t planners;    // E + 1, or 0
@@ -208,11 +212,23 @@ __global__ __launch_bounds__(PREP) void k_moe_prep(PrepArgs a) {
     }
     uint16_t dbits;
     __builtin_memcpy(&dbits, &d16, 2);
-    if (a.gemm) {
+    if (a.gemm || a.row) {
         int S = __builtin_amdgcn_sdot4((int)c, 0x01010101, 0, false);
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) S += __shfl_xor(S, o);
         if (!live) return;
+        if (a.row) {
+            const int64_t r = b / a.nb;
+            const int k = (int)(b - r * a.nb), C = (a.nb + 7) >> 3;
+            uint8_t* to = a.blocks + r * a.row;
+            *reinterpret_cast<uint32_t*>(to + (k >> 3) * 272 + (k & 7) * 32 + 4 * sub) = c;
+            if (sub == 0) {
+                float* da = reinterpret_cast<float*>(to + C * 272);
+                da[k] = (float)d16 * a.back;
+                if (a.min) da[8 * C + k] = (float)d16 * (float)S;
+            }
+            return;
+        }
         _Float16 h[4];
 #pragma unroll
         for (int i = 0; i < 4; i++) h[i] = (_Float16)(float)(int8_t)(c >> (8 * i));
@@ -735,8 +751,61 @@ __global__ __launch_bounds__(256) void k_moe_combine(const float* __restrict__ y
 
 }  // namespace
 
-int launch_moe_product(const MoeArgs& m, hipStream_t s) {
+static int launch_moe_combine(const float* yp, const int32_t* idx, const float* weight, int64_t T,
+                       int top, int64_t E, int64_t N, float* y, hipStream_t s) {
+    const bool four = N % 4 == 0 && aligned16(y);
+    const int64_t blocks = ((four ? T * (N / 4) : T * N) + 255) / 256;
+    const dim3 grid((unsigned)(blocks < (1 << 20) ? blocks : (1 << 20)));
+    if (four)
+        hipLaunchKernelGGL(k_moe_combine<4>, grid, dim3(256), 0, s, yp, idx, weight, T, top, (int)E,
+                           N, y);
+    else
+        hipLaunchKernelGGL(k_moe_combine<1>, grid, dim3(256), 0, s, yp, idx, weight, T, top, (int)E,
+                           N, y);
+    return (int)hipGetLastError();
+}
+
+// The launch before a product: the sorted pairs (plan) and the activations as
+// the kernel takes them (f16 for the GEMM, rows for the GEMV, else Q8_0 blocks
+// of x).
+static int prepare(const MoeArgs& m, bool plan, bool gemm, bool gemv, hipStream_t s) {
     const MoeWork L = moe_work(m.P, m.top, m.per, m.E, m.K);
+    PrepArgs p{};
+    p.x = m.x;
+    p.xq = m.xq;
+    p.blocks = m.work + L.blocks;
+    p.da = reinterpret_cast<uint16_t*>(m.work + L.da);
+    p.ca = reinterpret_cast<float*>(m.work + L.ca);
+    p.nblocks = m.x || gemm ? m.P / m.per * (m.K / 32) : 0;
+    p.gemm = gemm;
+    if (gemv) {
+        p.min = m.type == T_Q4_K || m.type == T_Q4_1 || m.type == T_Q5_1;
+        p.row = moe_gemv_row(m.K, p.min);
+        p.nb = (int32_t)(m.K / 32);
+        p.back = m.type == T_Q4_0 ? 1.0f / 16 : m.type == T_Q5_0 ? 1.0f / 8 : m.type == T_Q6_K ? 1.0f / 4 : 1.0f;
+    }
+    p.idx = m.idx;
+    p.P = (int32_t)m.P;
+    p.E = (int32_t)m.E;
+    p.R = moe_rows(m.P, m.top, m.E);
+    p.planners = plan ? p.E + 1 : 0;
+    p.items = reinterpret_cast<int32_t*>(m.work + L.items);
+    p.order = reinterpret_cast<int32_t*>(m.work + L.order);
+    p.count = reinterpret_cast<int32_t*>(m.work + L.count);
+    p.a16 = aligned16(m.x);
+    const int64_t grid = p.planners + (p.nblocks + PREP / 8 - 1) / (PREP / 8);
+    if (grid == 0) return 0;
+    hipLaunchKernelGGL(k_moe_prep, dim3((unsigned)grid), dim3(PREP), 0, s, p);
+    return (int)hipGetLastError();
+}
+
+int launch_moe_product(const MoeArgs& m, hipStream_t s) {
+    if (m.w2 && moe_gemv_fits(m)) return launch_moe_gemv(m, nullptr, nullptr, m.y, s);
+    const MoeWork L = moe_work(m.P, m.top, m.per, m.E, m.K);
+    const bool gemm = moe_rows(m.P, m.top, m.E) >= 64;
+    const int rc = prepare(m, gemm || m.P > MOE_SCAN, gemm, false, s);
+    if (rc) return rc;
+    if (gemm) return launch_moe_gemm(m, s);
     RowsArgs a{};
     a.w = m.w;
     a.w2 = m.w2;
@@ -751,32 +820,6 @@ int launch_moe_product(const MoeArgs& m, hipStream_t s) {
     a.order = reinterpret_cast<const int32_t*>(m.work + L.order);
     a.count = reinterpret_cast<const int32_t*>(m.work + L.count);
     a.y = m.y;
-    const int R = moe_rows(m.P, m.top, m.E);
-    const bool gemm = R >= 64, plan = gemm || m.P > MOE_SCAN;
-    if (m.x || plan) {
-        PrepArgs p{};
-        p.x = m.x;
-        p.xq = m.xq;
-        p.blocks = m.work + L.blocks;
-        p.da = reinterpret_cast<uint16_t*>(m.work + L.da);
-        p.ca = reinterpret_cast<float*>(m.work + L.ca);
-        p.nblocks = m.x || gemm ? m.P / m.per * (m.K / 32) : 0;
-        p.gemm = gemm;
-        p.idx = m.idx;
-        p.P = a.P;
-        p.E = a.E;
-        p.R = R;
-        p.planners = plan ? a.E + 1 : 0;
-        p.items = reinterpret_cast<int32_t*>(m.work + L.items);
-        p.order = reinterpret_cast<int32_t*>(m.work + L.order);
-        p.count = reinterpret_cast<int32_t*>(m.work + L.count);
-        p.a16 = aligned16(m.x);
-        const int64_t grid = p.planners + (p.nblocks + PREP / 8 - 1) / (PREP / 8);
-        hipLaunchKernelGGL(k_moe_prep, dim3((unsigned)grid), dim3(PREP), 0, s, p);
-        const int rc = (int)hipGetLastError();
-        if (rc) return rc;
-    }
-    if (gemm) return launch_moe_gemm(m, s);
     switch (m.type) {
     case T_Q8_0: return launch_any<T_Q8_0>(m, a, s);
     case T_Q4_0: return launch_any<T_Q4_0>(m, a, s);
@@ -790,18 +833,18 @@ int launch_moe_product(const MoeArgs& m, hipStream_t s) {
     return (int)hipErrorInvalidValue;
 }
 
-int launch_moe_combine(const float* yp, const int32_t* idx, const float* weight, int64_t T,
-                       int top, int64_t E, int64_t N, float* y, hipStream_t s) {
-    const bool four = N % 4 == 0 && aligned16(y);
-    const int64_t blocks = ((four ? T * (N / 4) : T * N) + 255) / 256;
-    const dim3 grid((unsigned)(blocks < (1 << 20) ? blocks : (1 << 20)));
-    if (four)
-        hipLaunchKernelGGL(k_moe_combine<4>, grid, dim3(256), 0, s, yp, idx, weight, T, top, (int)E,
-                           N, y);
-    else
-        hipLaunchKernelGGL(k_moe_combine<1>, grid, dim3(256), 0, s, yp, idx, weight, T, top, (int)E,
-                           N, y);
-    return (int)hipGetLastError();
+int launch_moe_down(const MoeArgs& m, const float* weight, float* y, hipStream_t s) {
+    if (moe_gemv_fits(m)) {
+        const uint8_t* rows = nullptr;
+        if (m.x && !moe_gemv_quantises(m)) {
+            const int rc = prepare(m, false, false, true, s);
+            if (rc) return rc;
+            rows = m.work + moe_work(m.P, m.top, m.per, m.E, m.K).blocks;
+        }
+        return launch_moe_gemv(m, rows, weight, y, s);
+    }
+    const int rc = launch_moe_product(m, s);
+    return rc ? rc : launch_moe_combine(m.y, m.idx, weight, m.P / m.top, m.top, m.E, m.N, y, s);
 }
 
 }  // namespace qmv

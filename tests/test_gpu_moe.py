@@ -122,7 +122,8 @@ def pick(rng, T, top, E, kind):
     idx = rng.integers(0, E, (T, top)).astype(np.int32)
     if kind == "none":
         idx[rng.random((T, top)) < 0.4] = rng.choice([-1, E, 1 << 30, -(1 << 31)])
-        idx[0] = -1
+        if T > 1:
+            idx[0] = -1
     return idx
 
 
@@ -247,3 +248,15 @@ def test_many_rows_unevenly(g, kind, T, top, E):
 def test_q6_k_scales(g, T, top, E, s_range):
     check_gateup(g, synth.Q6_K, T, top, E, 80, 768, "any", s_range=s_range)
     check_down(g, synth.Q6_K, T * top, 1, E, 80, 768, "any", s_range=s_range)
+
+
+# One token: a row of 1 to 64 chunks, short last ones, several rows a wave and one; 1 to 16 slots, and more
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("top,E,N,K", [(1, 2, 33, 32), (2, 4, 70, 256), (3, 5, 37, 96), (8, 9, 21, 896), (16, 16, 9, 512),
+                                       (20, 24, 9, 256), (2, 3, 19, 4864), (2, 3, 10, 8192), (2, 2, 7, 14336)])
+@pytest.mark.parametrize("kind", ["none", "any"])
+def test_one_token(g, fmt, top, E, N, K, kind):
+    K = K if fits(fmt, K) else -(-K // 256) * 256
+    for seed in (0, 7):
+        check_gateup(g, fmt, 1, top, E, N, K, kind, seed=seed, staged=seed == 7)
+        check_down(g, fmt, 1, top, E, N, K, kind, seed=seed, staged=seed == 7)
