@@ -39,15 +39,15 @@ struct MoeArgs {
     float* y;               // [P][N]; a gate/up pair's rows without an expert become 0, others are left alone
 };
 
-// Rows of an expert in one item, at most, which also names the kernel: up to
-// 16 as many as an expert can have when a token's experts differ (matrix
-// products of 16 columns, qmv_moe_rows.hip), 64 or 128 a tile of the GEMM
+// Rows of an expert in one item, at most, which also names the kernel: 4 where
+// no expert has more when a token's experts differ, else 16 (matrix products of
+// 16 columns, qmv_moe_rows.hip), 64 or 128 a tile of the GEMM
 // (qmv_moe_gemm.hip), by the pairs an expert has on average.
 inline int moe_rows(int64_t P, int top, int64_t E) {
     const int64_t T = P / top;
     if (P >= 96 * E) return 128;
     if (P >= 24 * E) return 64;
-    return T <= 4 ? 4 : T <= 8 ? 8 : 16;
+    return T <= 4 ? 4 : 16;
 }
 // Items of P pairs, at most: every item but an expert's last is full.
 inline int64_t moe_most_items(int64_t P, int64_t E, int rows) {

@@ -4,16 +4,16 @@
 // order; include/qmv.h), with the weights of the expert that each pair names.
 // Every pair's result is bit-identical to qmv_launch on that expert's matrix.
 //
-// An item is up to R = 4 NI pairs of one expert.  A workgroup of 8 waves takes
-// an item and 8 / KS tiles of 16 weight rows; KS waves share a tile and take
-// its 256-element chunks in turn.  A wave fetches the 16 rows' bytes of a
+// An item is up to R (4 or 16) pairs of one expert.  A workgroup of 8 waves
+// takes an item and 8 / KS tiles of 16 weight rows; KS waves share a tile and
+// take its 256-element chunks in turn.  A wave fetches the 16 rows' bytes of a
 // chunk as 16-byte pieces into registers, two chunks ahead (the gate's and the
 // up's of a pair), lays them into its slice of LDS, and lane (nn = l % 16,
 // kg = l / 16) decodes its quarter of each of weight row nn's blocks into an
 // operand of v_mfma_i32_16x16x32_i8.  Result element i of the lane is
 // activation row 4 kg + i of the instruction; the item's row j stands at
-// 4 (j % 4) + j / 4, so with NI rows a lane only the elements i < NI are
-// scaled: few rows cost few f32 terms.  The item's activations lie in LDS, a
+// 4 (j % 4) + j / 4, so that up to 4 NI rows need the elements i < NI only (NI
+// = 1, 2, 4, by the item's rows): few rows cost few f32 terms.  The item's activations lie in LDS, a
 // segment of chunks at a time, shared by the 8 waves.
 //
 // Order inside a block does not matter (the integers are exact), so lane kg
@@ -26,6 +26,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "qmv_moe.h"
 
@@ -36,6 +37,7 @@ constexpr int T_Q4_0 = 2, T_Q4_1 = 3, T_Q5_0 = 6, T_Q5_1 = 7, T_Q8_0 = 8, T_Q8_1
               T_Q4_K = 12, T_Q6_K = 14;
 
 typedef int v4i __attribute__((ext_vector_type(4)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
 // QK, BB: elements and bytes of a block; CB: bytes of a chunk of 256 elements;
 // PPS: 16-byte pieces that cover a chunk at the worst alignment of its start.
@@ -63,9 +65,13 @@ template <int FMT> constexpr bool nibble_block() {
 template <int FMT> constexpr float scale_back() {
     return FMT == T_Q4_0 ? 1.0f / 16 : FMT == T_Q5_0 ? 1.0f / 8 : 1.0f;
 }
-template <int FMT> constexpr int pieces() { return (16 * Fmt<FMT>::PPS + 63) / 64; }
-template <int FMT> constexpr int row_stride() { return 16 * Fmt<FMT>::PPS + 16; }
-template <int FMT> constexpr int slice() { return 16 * row_stride<FMT>(); }
+// AL: every chunk starts 16-byte aligned and is whole (K a multiple of 256 and
+// the chunk a multiple of 16 bytes).  LDS rows are an odd number of pieces
+// long, so that 16 rows' same piece meets all banks.
+template <int FMT> constexpr bool can_align() { return Fmt<FMT>::CB % 16 == 0; }
+template <int FMT, bool AL> constexpr int row_pieces() { return AL ? Fmt<FMT>::CB / 16 : Fmt<FMT>::PPS; }
+template <int FMT, bool AL> constexpr int row_stride() { return 16 * (row_pieces<FMT, AL>() | 1); }
+template <int FMT, bool AL> constexpr int slice() { return 16 * row_stride<FMT, AL>(); }
 
 constexpr int WAVES = 8;
 constexpr int SEG = 16;
@@ -260,42 +266,35 @@ struct RowsArgs {
     int32_t ks;              // waves that share a tile: 1, 2, 4, 8
     int32_t seg;             // chunks of activations in LDS at a time: SEG, or all if they are fewer
     int32_t item0;           // the launch's first item
+    bool scan;               // the workgroups find their items among idx; else items, order, count
 };
 
 // One chunk of the 16 weight rows at rb (this lane's row) against the item's
 // rows: p[i] = the chunk's sum of row kg + 4 i, in the documented order.
 // ac: this lane's row of the activation codes (of the matrix operand); da, ca:
-// scales (times scale_back) and scale * code sum of row kg, 32 floats from one
-// row i to the next.  nbc: blocks of the chunk.
-template <int FMT, int NI>
+// scales (times scale_back) and scale * code sum of block b's rows kg + 4 i at
+// [b * R + i].  nbc: blocks of the chunk.
+template <int FMT, int NI, int R>
 __device__ __forceinline__ void chunk_rows(const uint8_t* rb, const uint8_t* ac, const float* da,
                                            const float* ca, int nbc, int kg, float (&p)[NI]) {
     using F = Fmt<FMT>;
     const v4i zero = {0, 0, 0, 0};
-    float dv[NI][8], cv[has_min<FMT>() ? NI : 1][8];
 #pragma unroll
-    for (int i = 0; i < NI; i++) {
-        const float4 a = *reinterpret_cast<const float4*>(da + 32 * i);
-        const float4 b = *reinterpret_cast<const float4*>(da + 32 * i + 4);
-        dv[i][0] = a.x; dv[i][1] = a.y; dv[i][2] = a.z; dv[i][3] = a.w;
-        dv[i][4] = b.x; dv[i][5] = b.y; dv[i][6] = b.z; dv[i][7] = b.w;
-        if constexpr (has_min<FMT>()) {
-            const float4 c = *reinterpret_cast<const float4*>(ca + 32 * i);
-            const float4 d = *reinterpret_cast<const float4*>(ca + 32 * i + 4);
-            cv[i][0] = c.x; cv[i][1] = c.y; cv[i][2] = c.z; cv[i][3] = c.w;
-            cv[i][4] = d.x; cv[i][5] = d.y; cv[i][6] = d.z; cv[i][7] = d.w;
-        }
-        p[i] = 0.0f;
-    }
+    for (int i = 0; i < NI; i++) p[i] = 0.0f;
     // the superblock's fields
     uint64_t q[4];
     uint64_t qh[2];
-    uint4 hdr = make_uint4(0, 0, 0, 0);
+    uint32_t sc[4] = {0, 0, 0, 0}, mn[2] = {0, 0};
     float dw = 0.0f, dmin = 0.0f;
     if constexpr (FMT == T_Q4_K) {
-        hdr = ld<uint4>(rb);
+        const uint4 hdr = ld<uint4>(rb);
         dw = half_bits(hdr.x & 0xFFFFu);
         dmin = half_bits(hdr.x >> 16);
+        // 6-bit scales and minimums of sub-blocks 0..3, 4..7, one a byte
+        sc[0] = hdr.y & 0x3F3F3F3Fu;
+        mn[0] = hdr.z & 0x3F3F3F3Fu;
+        sc[1] = (hdr.w & 0x0F0F0F0Fu) | ((hdr.y >> 2) & 0x30303030u);
+        mn[1] = ((hdr.w >> 4) & 0x0F0F0F0Fu) | ((hdr.z >> 2) & 0x30303030u);
 #pragma unroll
         for (int j = 0; j < 4; j++) q[j] = ld<uint64_t>(rb + 16 + 32 * j + 8 * kg);
     } else if constexpr (FMT == T_Q6_K) {
@@ -303,18 +302,22 @@ __device__ __forceinline__ void chunk_rows(const uint8_t* rb, const uint8_t* ac,
         for (int j = 0; j < 4; j++) q[j] = ld<uint64_t>(rb + 32 * j + 8 * kg);
         qh[0] = ld<uint64_t>(rb + 128 + 8 * kg);
         qh[1] = ld<uint64_t>(rb + 160 + 8 * kg);
-        hdr = ld<uint4>(rb + 192);
+        const uint4 v = ld<uint4>(rb + 192);
+        sc[0] = v.x; sc[1] = v.y; sc[2] = v.z; sc[3] = v.w;
         dw = half_bits(ld<uint16_t>(rb + 208));
     }
 #pragma unroll
     for (int b = 0; b < 8; b++) {
-        if (F::QK == 32 && b >= nbc) break;
+        // a short chunk's missing blocks get scales of 0 (their activation
+        // scales are staged as 0): no branch between the blocks, whose reads
+        // and products overlap
         const long a = *reinterpret_cast<const long*>(ac + 32 * b);
         v4i I;
         float mw = 0.0f;   // the minimum's factor: p += mw * ca
         if constexpr (F::QK == 32) {
             const uint8_t* blk = rb + F::BB * b;
-            dw = half_bits(ld<uint16_t>(blk));
+            const uint32_t dbits = ld<uint16_t>(blk);
+            dw = half_bits(b < nbc ? dbits : 0u);
             uint64_t w;
             if constexpr (FMT == T_Q8_0 || FMT == T_Q8_1) {
                 w = ld<uint64_t>(blk + (FMT == T_Q8_0 ? 2 : 4) + 8 * kg);
@@ -344,25 +347,18 @@ __device__ __forceinline__ void chunk_rows(const uint8_t* rb, const uint8_t* ac,
                 }
                 w = ((uint64_t)hi << 32) | lo;
             }
-            if constexpr (has_min<FMT>()) mw = half_bits(ld<uint16_t>(blk + 2));
+            if constexpr (has_min<FMT>()) {
+                const uint32_t mbits = ld<uint16_t>(blk + 2);
+                mw = half_bits(b < nbc ? mbits : 0u);
+            }
             I = __builtin_amdgcn_mfma_i32_16x16x32_i8(a, (long)w, zero, 0, 0, 0);
         } else if constexpr (FMT == T_Q4_K) {
-            const uint32_t s12[3] = {hdr.y, hdr.z, hdr.w};
-            auto byte = [&](int i) -> int { return (int)((s12[i >> 2] >> (8 * (i & 3))) & 0xFFu); };
-            int sc, mn;
-            if (b < 4) {
-                sc = byte(b) & 63;
-                mn = byte(b + 4) & 63;
-            } else {
-                sc = (byte(b + 4) & 15) | ((byte(b - 4) >> 6) << 4);
-                mn = (byte(b + 4) >> 4) | ((byte(b) >> 6) << 4);
-            }
-            mw = -(dmin * (float)mn);
+            mw = -(dmin * (float)((mn[b >> 2] >> (8 * (b & 3))) & 0xFFu));
             const uint64_t raw = (b & 1) ? q[b >> 1] >> 4 : q[b >> 1];
             I = __builtin_amdgcn_mfma_i32_16x16x32_i8(a, (long)(raw & 0x0F0F0F0F0F0F0F0Full), zero,
                                                      0, 0, 0);
 #pragma unroll
-            for (int i = 0; i < NI; i++) I[i] = __mul24(sc, I[i]);
+            for (int i = 0; i < NI; i++) I[i] = __mul24((int)((sc[b >> 2] >> (8 * (b & 3))) & 0xFFu), I[i]);
         } else {
             const int h = b >> 2, kq = b & 3;
             uint64_t ql = q[2 * h + (kq & 1)];
@@ -372,8 +368,7 @@ __device__ __forceinline__ void chunk_rows(const uint8_t* rb, const uint8_t* ac,
             // q6 - 32 bytewise: no borrow leaves a byte whose top bit is set before
             const uint64_t top = 0x8080808080808080ull;
             const uint64_t w = ((q6 | top) - 0x2020202020202020ull) ^ top;
-            const uint32_t sc6[4] = {hdr.x, hdr.y, hdr.z, hdr.w};
-            const uint32_t sw = sc6[b >> 1] >> (16 * (b & 1));
+            const uint32_t sw = sc[b >> 1] >> (16 * (b & 1));
             const int s0 = (int8_t)(sw & 0xFF), s1 = (int8_t)((sw >> 8) & 0xFF);
             // each half of the block has a scale of its own: two products, the other half's codes zero
             const long lo = kg < 2 ? (long)w : 0, hi = kg < 2 ? 0 : (long)w;
@@ -382,18 +377,31 @@ __device__ __forceinline__ void chunk_rows(const uint8_t* rb, const uint8_t* ac,
 #pragma unroll
             for (int i = 0; i < NI; i++) I[i] = __mul24(s0, I0[i]) + __mul24(s1, I1[i]);
         }
+        typedef float vec __attribute__((ext_vector_type(NI)));
+        const vec dv = *reinterpret_cast<const vec*>(da + b * R);
+        vec cv = dv;
+        if constexpr (has_min<FMT>()) cv = *reinterpret_cast<const vec*>(ca + b * R);
 #pragma unroll
         for (int i = 0; i < NI; i++) {
-            p[i] = fmaf((float)I[i], dw * dv[i][b], p[i]);
-            if constexpr (has_min<FMT>()) p[i] = fmaf(mw, cv[i][b], p[i]);
+            p[i] = fmaf((float)I[i], dw * dv[i], p[i]);
+            if constexpr (has_min<FMT>()) p[i] = fmaf(mw, cv[i], p[i]);
+        }
+        // a few blocks at a time: the reads and products of more would run ahead
+        // and not fit the registers
+        if ((b + 1) % (NI == 4 ? 2 : 4) == 0) {
+            if constexpr (NI == 1) asm volatile("" : "+v"(p[0]) : : "memory");
+            if constexpr (NI == 2) asm volatile("" : "+v"(p[0]), "+v"(p[1]) : : "memory");
+            if constexpr (NI == 4) asm volatile("" : "+v"(p[0]), "+v"(p[1]), "+v"(p[2]), "+v"(p[3]) : : "memory");
         }
     }
 }
 
-template <int FMT, bool PAIR, int NI, bool SCAN>
+template <int FMT, bool PAIR, int R, bool AL>
 __global__ __launch_bounds__(64 * WAVES, 4) void k_moe_rows(RowsArgs a) {
     using F = Fmt<FMT>;
-    constexpr int R = 4 * NI, NP = pieces<FMT>(), MATS = PAIR ? 2 : 1;
+    constexpr int MATS = PAIR ? 2 : 1, NIM = R / 4;
+    constexpr int PPS = row_pieces<FMT, AL>(), NP = (16 * PPS + 63) / 64;
+    constexpr int STRIDE = row_stride<FMT, AL>(), SLICE = slice<FMT, AL>();
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     int* pairs = reinterpret_cast<int*>(smem);    // [16] the item's pairs
     const int tid = threadIdx.x, lane = tid & 63, wv = uniform(tid >> 6);
@@ -401,7 +409,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_moe_rows(RowsArgs a) {
 
     // the item: its expert and rows
     int e = -1, rows = 0;
-    if constexpr (SCAN) {
+    if (a.scan) {
         const int key = lane < a.P ? key_of(a.idx[lane], a.E) : -1;
         uint64_t left = __builtin_amdgcn_ballot_w64(lane < a.P);
         int item = a.item0 + (int)blockIdx.y;
@@ -458,52 +466,58 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_moe_rows(RowsArgs a) {
     const uint32_t lim = (uint32_t)(room < 0x7fffffff ? room : 0x7fffffff);
     const bool tail = room < 16 * Rb + 16;          // pieces may reach past the last expert's end
     const int last_row = (int)(N - 1 - n0 < 15 ? N - 1 - n0 : 15);
-    uint8_t* wl = smem + 64 + wv * slice<FMT>();
-    uint8_t* acts = smem + 64 + WAVES * slice<FMT>();
+    uint8_t* wl = smem + 64 + wv * SLICE;
+    uint8_t* acts = smem + 64 + WAVES * SLICE;
     const int seg = a.seg;
-    float* dbuf = reinterpret_cast<float*>(acts + seg * R * ACT_STRIDE);    // [seg][R][8]
+    float* dbuf = reinterpret_cast<float*>(acts + seg * R * ACT_STRIDE);    // [seg][8][4][R / 4]: row kg + 4 i at [kg][i]
     float* cbuf = dbuf + seg * R * 8;                                       // the same, with a minimum
     float* pbuf = cbuf + (has_min<FMT>() ? seg * R * 8 : 0);                // [seg][TW][MATS][R][16], KS > 1
 
     // 16-byte pieces: lane l's k-th is piece 64 k + l of the tile's rows
     uint32_t rowoff[NP];
-    int pn[NP], pj[NP];
+    uint32_t where[NP];    // its place in the slice | its number in the row << 16
 #pragma unroll
     for (int k = 0; k < NP; k++) {
-        const int p = min(64 * k + lane, 16 * F::PPS - 1);
-        pn[k] = p / F::PPS;
-        pj[k] = p - pn[k] * F::PPS;
-        rowoff[k] = a0 + (uint32_t)min(pn[k], last_row) * (uint32_t)Rb;
+        const int p = min(64 * k + lane, 16 * PPS - 1);
+        const int n = p / PPS;
+        const int j = p - n * PPS;
+        where[k] = (uint32_t)(n * STRIDE + 16 * j) | (uint32_t)j << 16;
+        rowoff[k] = a0 + (uint32_t)min(n, last_row) * (uint32_t)Rb + (AL ? 16 * j : 0);
     }
-    // a piece past the chunk's end is its last one again, one past the blob's
-    // end is moved back (staged bytewise)
+    // not AL: a piece past the chunk's end is its last one again, one past the
+    // blob's end is moved back (and staged bytewise)
     auto piece = [&](int k, int c) -> uint32_t {
         const uint32_t len = F::QK == 32 ? min(8, nb - 8 * c) * F::BB : F::CB;
         const uint32_t s = rowoff[k] + (uint32_t)c * F::CB;
-        return min((s & ~15u) + 16 * pj[k], (s + len - 1) & ~15u);
+        return min((s & ~15u) + 16 * (where[k] >> 16), (s + len - 1) & ~15u);
     };
-    auto fetch = [&](const uint8_t* base, int c, uint4 (&r)[NP]) {
+    auto fetch = [&](const uint8_t* base, int c, v4u (&r)[NP]) {
+        if constexpr (AL) {
+            const uint8_t* at = base + (int64_t)c * F::CB;
+#pragma unroll
+            for (int k = 0; k < NP; k++) r[k] = *reinterpret_cast<const v4u*>(at + rowoff[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < NP; k++) __builtin_memcpy(&r[k], base + min(piece(k, c), lim), 16);
+        }
+    };
+    auto stage = [&](int c, const v4u (&r)[NP]) {
 #pragma unroll
         for (int k = 0; k < NP; k++)
-            __builtin_memcpy(&r[k], base + min(piece(k, c), lim), 16);
-    };
-    auto stage = [&](int c, const uint4 (&r)[NP]) {
-#pragma unroll
-        for (int k = 0; k < NP; k++)
-            if (64 * k + lane < 16 * F::PPS)
-                *reinterpret_cast<uint4*>(wl + pn[k] * row_stride<FMT>() + 16 * pj[k]) = r[k];
-        if (tail) {
+            if (64 * k + lane < 16 * PPS)
+                *reinterpret_cast<v4u*>(wl + (where[k] & 0xFFFFu)) = r[k];
+        if (!AL && tail) {
             // pieces that were moved back: their bytes to where they belong
 #pragma unroll
             for (int k = 0; k < NP; k++) {
                 const uint32_t off = piece(k, c);
                 const uint32_t s = rowoff[k] + (uint32_t)c * F::CB;
                 if (off > lim) {
-                    uint8_t* to = wl + pn[k] * row_stride<FMT>() + (lim - (s & ~15u));
+                    uint8_t* at = wl + (where[k] & 0xFFFFu) - 16 * (where[k] >> 16) + (lim - (s & ~15u));
                     uint16_t h[8];
                     __builtin_memcpy(h, &r[k], 16);
 #pragma unroll
-                    for (int i = 0; i < 8; i++) __builtin_memcpy(to + 2 * i, &h[i], 2);
+                    for (int i = 0; i < 8; i++) __builtin_memcpy(at + 2 * i, &h[i], 2);
                 }
             }
         }
@@ -511,41 +525,59 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_moe_rows(RowsArgs a) {
     };
 
     // the wave's steps: its chunks ks, ks + KS, ...; of a pair first the gate's, then the up's
-    const int mychunks = (C - ks + KS - 1) / KS;   // may be 0
-    uint4 r0[NP], r1[NP];
-    if (mychunks > 0) fetch(wt, ks, r0);
-    if (PAIR ? mychunks > 0 : mychunks > 1) fetch(wt2, PAIR ? ks : ks + KS, r1);
+    // and of a single matrix two of them by turns.  Every fetch is made, beyond
+    // the end the last chunk's again: a fetch behind a branch would make each
+    // wait for one set of registers wait for the other's too
+    auto valid = [&](int c) { return min(c, C - 1); };
+    constexpr int TURN = PAIR ? 1 : 2;
+    v4u r0[NP], r1[NP];
+    fetch(wt, ks, r0);
+    fetch(wt2, PAIR ? ks : valid(ks + KS), r1);
 
-    float acc[MATS][NI];
+    float acc[MATS][NIM];
 #pragma unroll
     for (int m = 0; m < MATS; m++)
 #pragma unroll
-        for (int i = 0; i < NI; i++) acc[m][i] = 0.0f;
+        for (int i = 0; i < NIM; i++) acc[m][i] = 0.0f;
     float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // KS > 1: this thread's outputs tid + 512 q
     const int outs = TW * MATS * R * 16;
 
     // this lane's activation row of the matrix operand, and where its scales begin
-    const int arow = (nn >> 2) + ((nn & 3) < NI ? 4 * (nn & 3) : 0);
+    const int arow = (nn >> 2) + ((nn & 3) < NIM ? 4 * (nn & 3) : 0);
 
-    auto work = [&](int m, int c, int c0, const uint4 (&r)[NP]) {
-        stage(c, r);
+    // the staged chunk c against the item's rows
+    auto multiply = [&](int m, int c, int c0) {
         const int cs = c - c0;
         const uint32_t s = a0 + (uint32_t)min(nn, last_row) * (uint32_t)Rb + (uint32_t)c * F::CB;
-        const uint8_t* rb = wl + nn * row_stride<FMT>() + (s & 15);
+        const uint8_t* rb = wl + nn * STRIDE + (AL ? 0 : s & 15);
         const uint8_t* ac = acts + (cs * R + arow) * ACT_STRIDE + 8 * kg;
-        const float* da = dbuf + (cs * R + kg) * 8;
-        const float* ca = cbuf + (cs * R + kg) * 8;
-        float p[NI];
-        chunk_rows<FMT, NI>(rb, ac, da, ca, F::QK == 32 ? min(8, nb - 8 * c) : 8, kg, p);
-        wave_sync();
-        if (KS == 1) {
+        const float* da = dbuf + cs * R * 8 + kg * NIM;
+        const float* ca = cbuf + cs * R * 8 + kg * NIM;
+        float* o = pbuf + cs * outs + ((tw * MATS + m) * R + kg) * 16 + nn;
+        const int nbc = F::QK == 32 && !AL ? min(8, nb - 8 * c) : 8;
+        auto run = [&](auto ni) {
+            constexpr int NI = decltype(ni)::value;
+            float p[NI];
+            chunk_rows<FMT, NI, R>(rb, ac, da, ca, nbc, kg, p);
 #pragma unroll
-            for (int i = 0; i < NI; i++) acc[m][i] = acc[m][i] + p[i];
+            for (int i = 0; i < NI; i++) {
+                if (KS == 1)
+                    acc[m][i] = acc[m][i] + p[i];
+                else
+                    o[64 * i] = p[i];
+            }
+        };
+        if constexpr (NIM == 4) {
+            if (rows > 8)
+                run(std::integral_constant<int, 4>{});
+            else if (rows > 4)
+                run(std::integral_constant<int, 2>{});
+            else
+                run(std::integral_constant<int, 1>{});
         } else {
-            float* o = pbuf + cs * outs + ((tw * MATS + m) * R + kg) * 16 + nn;
-#pragma unroll
-            for (int i = 0; i < NI; i++) o[64 * i] = p[i];
+            run(std::integral_constant<int, 1>{});
         }
+        wave_sync();
     };
 
     int c = ks;
@@ -554,9 +586,15 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_moe_rows(RowsArgs a) {
         __syncthreads();
         // the segment's activations: a thread a block
         {
-            const int nbs = min(nb, 8 * c1) - 8 * c0;
-            for (int i = tid; i < rows * nbs; i += 64 * WAVES) {
-                const int j = i / nbs, b = i - j * nbs;
+            const int nbs = min(nb, 8 * c1) - 8 * c0, all = 8 * (c1 - c0);
+            for (int i = tid; i < rows * all; i += 64 * WAVES) {
+                const int j = i / all, b = i - j * all;
+                const int at = b * R + (j & 3) * NIM + (j >> 2);
+                if (b >= nbs) {   // the missing blocks of a short chunk
+                    dbuf[at] = 0.0f;
+                    if constexpr (has_min<FMT>()) cbuf[at] = 0.0f;
+                    continue;
+                }
                 const int64_t row = pairs[j] / a.per;
                 uint32_t v[9];
                 __builtin_memcpy(v, a.blocks + (row * nb + 8 * c0 + b) * 34, 34);
@@ -572,7 +610,6 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_moe_rows(RowsArgs a) {
                     to[0] = make_uint4(q[0], q[1], q[2], q[3]);
                     to[1] = make_uint4(q[4], q[5], q[6], q[7]);
                 }
-                const int at = ((b >> 3) * R + j) * 8 + (b & 7);
                 dbuf[at] = d * scale_back<FMT>();
                 if constexpr (has_min<FMT>()) {
                     int S = 0;
@@ -583,30 +620,21 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_moe_rows(RowsArgs a) {
             }
         }
         __syncthreads();
-        if constexpr (PAIR) {
-            for (; c < c1; c += KS) {
-                work(0, c, c0, r0);
-                if (c + KS < C) fetch(wt, c + KS, r0);
-                work(1, c, c0, r1);
-                if (c + KS < C) fetch(wt2, c + KS, r1);
-            }
-        } else {
-            while (c < c1) {
-                work(0, c, c0, r0);
-                if (c + 2 * KS < C) fetch(wt, c + 2 * KS, r0);
-                c += KS;
-                if (c >= c1) break;   // only in the last segment: the others hold an even number of the wave's chunks
-                work(0, c, c0, r1);
-                if (c + 2 * KS < C) fetch(wt, c + 2 * KS, r1);
-                c += KS;
-            }
+        for (; c < c1; c += TURN * KS) {
+            stage(c, r0);
+            fetch(wt, valid(c + TURN * KS), r0);
+            multiply(0, c, c0);
+            const int d = PAIR ? c : c + KS;
+            stage(valid(d), r1);
+            fetch(wt2, valid(d + TURN * KS), r1);
+            if (PAIR || d < c1) multiply(MATS - 1, d, c0);   // the last segment may end between the two
         }
         if (KS > 1) {
             __syncthreads();
 #pragma unroll
             for (int q = 0; q < 4; q++) {
                 const int o = tid + 64 * WAVES * q;
-                if (o < outs)
+                if (o < outs && (o >> 4) % R < rows)
                     for (int cs = 0; cs < c1 - c0; cs++) sum[q] = sum[q] + pbuf[cs * outs + o];
             }
         }
@@ -615,7 +643,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_moe_rows(RowsArgs a) {
     if (KS == 1) {
         if (!mine) return;
 #pragma unroll
-        for (int i = 0; i < NI; i++) {
+        for (int i = 0; i < NIM; i++) {
             const int j = kg + 4 * i;
             if (j < rows && nn <= last_row)
                 a.y[pairs[j] * N + n0 + nn] = PAIR ? swiglu(acc[0][i], acc[MATS - 1][i]) : acc[0][i];
@@ -658,23 +686,23 @@ int raise_lds_limit(const void* kernel, std::atomic<int> (&state)[64]) {
     return 0;
 }
 
-template <int FMT, bool PAIR, int NI, bool SCAN>
+template <int FMT, bool PAIR, int R, bool AL>
 int launch_rows(const MoeArgs& m, RowsArgs& a, hipStream_t s) {
     using F = Fmt<FMT>;
-    constexpr int R = 4 * NI, MATS = PAIR ? 2 : 1;
+    constexpr int MATS = PAIR ? 2 : 1;
     const int64_t tiles = (a.N + 15) / 16, C = ((a.K >> 5) + 7) / 8;
     a.wbytes = m.E * a.N * (a.K / F::QK) * F::BB;
     const int64_t items = moe_most_items(m.P, m.E, R);
     // waves that share a tile: enough waves to fill the chip
     int ks = 1;
-    while (ks < 8 && 2 * ks <= C && tiles * items * ks * 2 <= 4096) ks *= 2;
+    while (ks < 8 && 2 * ks <= C && tiles * items * ks < 4096) ks *= 2;
     a.ks = ks;
     const int TW = WAVES / ks;
     // a segment: as many chunks as leave a compute unit two workgroups, at
     // least two a wave (the fetches run two ahead); 16 of them take at most
     // 148 KB in any variant
     auto lds_of = [&](int seg) {
-        return 64 + (size_t)WAVES * slice<FMT>() +
+        return 64 + (size_t)WAVES * slice<FMT, AL>() +
                (size_t)seg * R * (ACT_STRIDE + 32 * (has_min<FMT>() ? 2 : 1)) +
                (ks > 1 ? (size_t)seg * TW * MATS * R * 64 : 0);
     };
@@ -683,11 +711,11 @@ int launch_rows(const MoeArgs& m, RowsArgs& a, hipStream_t s) {
     a.seg = (int32_t)(C < seg ? C : seg);
     const size_t lds = lds_of(a.seg);
     static std::atomic<int> state[64];
-    const int rc = raise_lds_limit(reinterpret_cast<const void*>(&k_moe_rows<FMT, PAIR, NI, SCAN>), state);
+    const int rc = raise_lds_limit(reinterpret_cast<const void*>(&k_moe_rows<FMT, PAIR, R, AL>), state);
     if (rc) return rc;
     for (int64_t at = 0; at < items; at += MOST_Y) {   // a grid's second dimension ends at 65535
         a.item0 = (int32_t)at;
-        hipLaunchKernelGGL((k_moe_rows<FMT, PAIR, NI, SCAN>),
+        hipLaunchKernelGGL((k_moe_rows<FMT, PAIR, R, AL>),
                            dim3((unsigned)((tiles + TW - 1) / TW),
                                 (unsigned)(items - at < MOST_Y ? items - at : MOST_Y)),
                            dim3(64 * WAVES), lds, s, a);
@@ -698,14 +726,14 @@ int launch_rows(const MoeArgs& m, RowsArgs& a, hipStream_t s) {
 }
 
 template <int FMT, bool PAIR> int launch_fmt(const MoeArgs& m, RowsArgs& a, hipStream_t s) {
-    const int R = moe_rows(m.P, m.top, m.E);
-    if (m.P <= MOE_SCAN)
-        return R == 4 ? launch_rows<FMT, PAIR, 1, true>(m, a, s)
-             : R == 8 ? launch_rows<FMT, PAIR, 2, true>(m, a, s)
-                      : launch_rows<FMT, PAIR, 4, true>(m, a, s);
-    return R == 4 ? launch_rows<FMT, PAIR, 1, false>(m, a, s)
-         : R == 8 ? launch_rows<FMT, PAIR, 2, false>(m, a, s)
-                  : launch_rows<FMT, PAIR, 4, false>(m, a, s);
+    const bool four = moe_rows(m.P, m.top, m.E) == 4;
+    if constexpr (can_align<FMT>()) {
+        if (m.K % 256 == 0)
+            return four ? launch_rows<FMT, PAIR, 4, true>(m, a, s) : launch_rows<FMT, PAIR, 16, true>(m, a, s);
+    }
+    if constexpr (FMT != T_Q4_K)   // whose rows are always whole chunks
+        return four ? launch_rows<FMT, PAIR, 4, false>(m, a, s) : launch_rows<FMT, PAIR, 16, false>(m, a, s);
+    return (int)hipErrorInvalidValue;
 }
 
 template <int FMT> int launch_any(const MoeArgs& m, RowsArgs& a, hipStream_t s) {
@@ -820,6 +848,7 @@ int launch_moe_product(const MoeArgs& m, hipStream_t s) {
     a.order = reinterpret_cast<const int32_t*>(m.work + L.order);
     a.count = reinterpret_cast<const int32_t*>(m.work + L.count);
     a.y = m.y;
+    a.scan = m.P <= MOE_SCAN;
     switch (m.type) {
     case T_Q8_0: return launch_any<T_Q8_0>(m, a, s);
     case T_Q4_0: return launch_any<T_Q4_0>(m, a, s);
