@@ -27,6 +27,7 @@
 
 #include <atomic>
 #include <type_traits>
+#include <utility>
 
 #include "qmv_moe.h"
 
@@ -87,6 +88,14 @@ template <typename T> __device__ __forceinline__ T ld(const uint8_t* p) {
     T v;
     __builtin_memcpy(&v, p, sizeof(T));
     return v;
+}
+template <class Fn, int... Is>
+__device__ __forceinline__ void each_of(Fn&& f, std::integer_sequence<int, Is...>) {
+    (f(std::integral_constant<int, Is>{}), ...);
+}
+// f(0), f(1), ... f(N - 1) with constants
+template <int N, class Fn> __device__ __forceinline__ void each(Fn&& f) {
+    each_of(f, std::make_integer_sequence<int, N>{});
 }
 __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -269,45 +278,82 @@ struct RowsArgs {
     bool scan;               // the workgroups find their items among idx; else items, order, count
 };
 
+// A chunk's fields in LDS as aligned dwords: reads that do not lie on their own
+// size's border take twice the time there.  Blocks of 18, 22, 34 and 210 bytes
+// leave fields, and without AL the chunk itself, on any even byte: a field at
+// byte O is read from the dwords around it and shifted down.
+template <bool AL> struct Fields {
+    const uint32_t *even, *odd;   // the dwords that hold bytes 0 and 2
+    uint32_t se, so;              // where in them: 0 or 2
+    const uint8_t* at;            // byte 0
+    __device__ __forceinline__ explicit Fields(const uint8_t* rb) : at(rb) {
+        if constexpr (AL) {
+            even = odd = reinterpret_cast<const uint32_t*>(rb);
+            se = 0;
+            so = 2;
+        } else {
+            const uint32_t low = (uint32_t)reinterpret_cast<uintptr_t>(rb) & 2u;
+            even = reinterpret_cast<const uint32_t*>(rb - low);
+            odd = reinterpret_cast<const uint32_t*>(rb + low);
+            se = low;
+            so = 2 - low;
+        }
+    }
+    // N dwords at byte O + 4 l
+    template <int O, int N> __device__ __forceinline__ void get(int l, uint32_t (&o)[N]) const {
+        const uint32_t* p = (O % 4 ? odd + (O - 2) / 4 : even + O / 4) + l;
+        if constexpr (AL && O % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < N; i++) o[i] = p[i];
+        } else {
+            uint32_t v[N + 1];
+#pragma unroll
+            for (int i = 0; i <= N; i++) v[i] = p[i];
+#pragma unroll
+            for (int i = 0; i < N; i++) o[i] = __builtin_amdgcn_alignbyte(v[i + 1], v[i], O % 4 ? so : se);
+        }
+    }
+    template <int O> __device__ __forceinline__ uint32_t half() const {
+        return *reinterpret_cast<const uint16_t*>(at + O);
+    }
+};
+
 // One chunk of the 16 weight rows at rb (this lane's row) against the item's
 // rows: p[i] = the chunk's sum of row kg + 4 i, in the documented order.
 // ac: this lane's row of the activation codes (of the matrix operand); da, ca:
 // scales (times scale_back) and scale * code sum of block b's rows kg + 4 i at
 // [b * R + i].  nbc: blocks of the chunk.
-template <int FMT, int NI, int R>
-__device__ __forceinline__ void chunk_rows(const uint8_t* rb, const uint8_t* ac, const float* da,
+template <int FMT, int NI, int R, bool AL>
+__device__ __forceinline__ void chunk_rows(const Fields<AL>& rb, const uint8_t* ac, const float* da,
                                            const float* ca, int nbc, int kg, float (&p)[NI]) {
     using F = Fmt<FMT>;
     const v4i zero = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < NI; i++) p[i] = 0.0f;
     // the superblock's fields
-    uint64_t q[4];
-    uint64_t qh[2];
+    uint32_t q[4][2], qh[2][2];
     uint32_t sc[4] = {0, 0, 0, 0}, mn[2] = {0, 0};
     float dw = 0.0f, dmin = 0.0f;
     if constexpr (FMT == T_Q4_K) {
-        const uint4 hdr = ld<uint4>(rb);
-        dw = half_bits(hdr.x & 0xFFFFu);
-        dmin = half_bits(hdr.x >> 16);
+        uint32_t hdr[4];
+        rb.template get<0, 4>(0, hdr);
+        dw = half_bits(hdr[0] & 0xFFFFu);
+        dmin = half_bits(hdr[0] >> 16);
         // 6-bit scales and minimums of sub-blocks 0..3, 4..7, one a byte
-        sc[0] = hdr.y & 0x3F3F3F3Fu;
-        mn[0] = hdr.z & 0x3F3F3F3Fu;
-        sc[1] = (hdr.w & 0x0F0F0F0Fu) | ((hdr.y >> 2) & 0x30303030u);
-        mn[1] = ((hdr.w >> 4) & 0x0F0F0F0Fu) | ((hdr.z >> 2) & 0x30303030u);
-#pragma unroll
-        for (int j = 0; j < 4; j++) q[j] = ld<uint64_t>(rb + 16 + 32 * j + 8 * kg);
+        sc[0] = hdr[1] & 0x3F3F3F3Fu;
+        mn[0] = hdr[2] & 0x3F3F3F3Fu;
+        sc[1] = (hdr[3] & 0x0F0F0F0Fu) | ((hdr[1] >> 2) & 0x30303030u);
+        mn[1] = ((hdr[3] >> 4) & 0x0F0F0F0Fu) | ((hdr[2] >> 2) & 0x30303030u);
+        each<4>([&](auto j) { rb.template get<16 + 32 * j, 2>(2 * kg, q[j]); });
     } else if constexpr (FMT == T_Q6_K) {
-#pragma unroll
-        for (int j = 0; j < 4; j++) q[j] = ld<uint64_t>(rb + 32 * j + 8 * kg);
-        qh[0] = ld<uint64_t>(rb + 128 + 8 * kg);
-        qh[1] = ld<uint64_t>(rb + 160 + 8 * kg);
-        const uint4 v = ld<uint4>(rb + 192);
-        sc[0] = v.x; sc[1] = v.y; sc[2] = v.z; sc[3] = v.w;
-        dw = half_bits(ld<uint16_t>(rb + 208));
+        each<4>([&](auto j) { rb.template get<32 * j, 2>(2 * kg, q[j]); });
+        each<2>([&](auto j) { rb.template get<128 + 32 * j, 2>(2 * kg, qh[j]); });
+        rb.template get<192, 4>(0, sc);
+        dw = half_bits(rb.template half<208>());
     }
-#pragma unroll
-    for (int b = 0; b < 8; b++) {
+    auto wide = [](const uint32_t (&v)[2]) { return ((uint64_t)v[1] << 32) | v[0]; };
+    each<8>([&](auto bc) {
+        constexpr int b = bc;
         // a short chunk's missing blocks get scales of 0 (their activation
         // scales are staged as 0): no branch between the blocks, whose reads
         // and products overlap
@@ -315,56 +361,56 @@ __device__ __forceinline__ void chunk_rows(const uint8_t* rb, const uint8_t* ac,
         v4i I;
         float mw = 0.0f;   // the minimum's factor: p += mw * ca
         if constexpr (F::QK == 32) {
-            const uint8_t* blk = rb + F::BB * b;
-            const uint32_t dbits = ld<uint16_t>(blk);
+            constexpr int O = F::BB * b;
+            const uint32_t dbits = rb.template half<O>();
             dw = half_bits(b < nbc ? dbits : 0u);
-            uint64_t w;
+            uint32_t w[2];
             if constexpr (FMT == T_Q8_0 || FMT == T_Q8_1) {
-                w = ld<uint64_t>(blk + (FMT == T_Q8_0 ? 2 : 4) + 8 * kg);
+                rb.template get<O + (FMT == T_Q8_0 ? 2 : 4), 2>(2 * kg, w);
             } else {
                 constexpr int QS = FMT == T_Q4_0 ? 2 : FMT == T_Q4_1 ? 4 : FMT == T_Q5_0 ? 6 : 8;
-                const uint32_t v = ld<uint32_t>(blk + QS + 4 * kg);
-                uint32_t lo, hi;
+                uint32_t one[1];
+                rb.template get<O + QS, 1>(kg, one);
+                const uint32_t v = one[0];
                 if constexpr (FMT == T_Q4_0) {
-                    lo = ((v << 4) & 0xF0F0F0F0u) ^ 0x80808080u;
-                    hi = (v & 0xF0F0F0F0u) ^ 0x80808080u;
+                    w[0] = ((v << 4) & 0xF0F0F0F0u) ^ 0x80808080u;
+                    w[1] = (v & 0xF0F0F0F0u) ^ 0x80808080u;
                 } else if constexpr (FMT == T_Q4_1) {
-                    lo = v & 0x0F0F0F0Fu;
-                    hi = (v >> 4) & 0x0F0F0F0Fu;
+                    w[0] = v & 0x0F0F0F0Fu;
+                    w[1] = (v >> 4) & 0x0F0F0F0Fu;
                 } else {
                     // fifth bits of elements 4kg .. 4kg+3 and 16 + 4kg ..: h * 0x204081 puts
                     // bit j of a nibble h at bit 8 j (plus others, masked off), without carries
-                    const uint32_t h = ld<uint32_t>(blk + (FMT == T_Q5_0 ? 2 : 4)) >> (4 * kg);
+                    rb.template get<O + (FMT == T_Q5_0 ? 2 : 4), 1>(0, one);
+                    const uint32_t h = one[0] >> (4 * kg);
                     const uint32_t l5 = __umul24(h & 15u, 0x204081u) & 0x01010101u;
                     const uint32_t h5 = __umul24((h >> 16) & 15u, 0x204081u) & 0x01010101u;
                     if constexpr (FMT == T_Q5_0) {
-                        lo = (((v << 3) & 0x78787878u) | (l5 << 7)) ^ 0x80808080u;
-                        hi = (((v >> 1) & 0x78787878u) | (h5 << 7)) ^ 0x80808080u;
+                        w[0] = (((v << 3) & 0x78787878u) | (l5 << 7)) ^ 0x80808080u;
+                        w[1] = (((v >> 1) & 0x78787878u) | (h5 << 7)) ^ 0x80808080u;
                     } else {
-                        lo = (v & 0x0F0F0F0Fu) | (l5 << 4);
-                        hi = ((v >> 4) & 0x0F0F0F0Fu) | (h5 << 4);
+                        w[0] = (v & 0x0F0F0F0Fu) | (l5 << 4);
+                        w[1] = ((v >> 4) & 0x0F0F0F0Fu) | (h5 << 4);
                     }
                 }
-                w = ((uint64_t)hi << 32) | lo;
             }
             if constexpr (has_min<FMT>()) {
-                const uint32_t mbits = ld<uint16_t>(blk + 2);
+                const uint32_t mbits = rb.template half<O + 2>();
                 mw = half_bits(b < nbc ? mbits : 0u);
             }
-            I = __builtin_amdgcn_mfma_i32_16x16x32_i8(a, (long)w, zero, 0, 0, 0);
+            I = __builtin_amdgcn_mfma_i32_16x16x32_i8(a, (long)wide(w), zero, 0, 0, 0);
         } else if constexpr (FMT == T_Q4_K) {
             mw = -(dmin * (float)((mn[b >> 2] >> (8 * (b & 3))) & 0xFFu));
-            const uint64_t raw = (b & 1) ? q[b >> 1] >> 4 : q[b >> 1];
+            const uint64_t raw = wide(q[b >> 1]) >> (4 * (b & 1));
             I = __builtin_amdgcn_mfma_i32_16x16x32_i8(a, (long)(raw & 0x0F0F0F0F0F0F0F0Full), zero,
                                                      0, 0, 0);
 #pragma unroll
             for (int i = 0; i < NI; i++) I[i] = __mul24((int)((sc[b >> 2] >> (8 * (b & 3))) & 0xFFu), I[i]);
         } else {
-            const int h = b >> 2, kq = b & 3;
-            uint64_t ql = q[2 * h + (kq & 1)];
-            if (kq & 2) ql >>= 4;
+            constexpr int h = b >> 2, kq = b & 3;
+            const uint64_t ql = wide(q[2 * h + (kq & 1)]) >> (kq & 2 ? 4 : 0);
             const uint64_t q6 = (ql & 0x0F0F0F0F0F0F0F0Full) |
-                                (((qh[h] >> (2 * kq)) & 0x0303030303030303ull) << 4);
+                                (((wide(qh[h]) >> (2 * kq)) & 0x0303030303030303ull) << 4);
             // q6 - 32 bytewise: no borrow leaves a byte whose top bit is set before
             const uint64_t top = 0x8080808080808080ull;
             const uint64_t w = ((q6 | top) - 0x2020202020202020ull) ^ top;
@@ -388,12 +434,12 @@ __device__ __forceinline__ void chunk_rows(const uint8_t* rb, const uint8_t* ac,
         }
         // a few blocks at a time: the reads and products of more would run ahead
         // and not fit the registers
-        if ((b + 1) % (NI == 4 ? 2 : 4) == 0) {
+        if constexpr ((b + 1) % (NI == 4 ? 2 : 4) == 0) {
             if constexpr (NI == 1) asm volatile("" : "+v"(p[0]) : : "memory");
             if constexpr (NI == 2) asm volatile("" : "+v"(p[0]), "+v"(p[1]) : : "memory");
             if constexpr (NI == 4) asm volatile("" : "+v"(p[0]), "+v"(p[1]), "+v"(p[2]), "+v"(p[3]) : : "memory");
         }
-    }
+    });
 }
 
 template <int FMT, bool PAIR, int R, bool AL>
@@ -427,9 +473,10 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_moe_rows(RowsArgs a) {
             item -= items;
             left &= ~m;
         }
-    } else if (a.item0 + (int)blockIdx.y < *a.count) {
+    } else {
         const int at = a.item0 + (int)blockIdx.y;
-        const int4 it = reinterpret_cast<const int4*>(a.items)[at];
+        const int4 it = reinterpret_cast<const int4*>(a.items)[at];   // read along with the count
+        if (at >= *a.count) return;
         const int done = uniform((at - it.w) * R);    // the expert's rows in items before this one
         e = uniform(it.x);
         rows = min(R, uniform(it.z) - done);
@@ -558,7 +605,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_moe_rows(RowsArgs a) {
         auto run = [&](auto ni) {
             constexpr int NI = decltype(ni)::value;
             float p[NI];
-            chunk_rows<FMT, NI, R>(rb, ac, da, ca, nbc, kg, p);
+            chunk_rows<FMT, NI, R, AL>(Fields<AL>(rb), ac, da, ca, nbc, kg, p);
 #pragma unroll
             for (int i = 0; i < NI; i++) {
                 if (KS == 1)
