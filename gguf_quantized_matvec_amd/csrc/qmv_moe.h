@@ -98,7 +98,7 @@ int launch_moe_down(const MoeArgs& a, const float* weight, float* y, hipStream_t
 // Many rows of an expert, after the preparation (qmv_moe_gemm.hip).
 int launch_moe_gemm(const MoeArgs& a, hipStream_t s);
 
-// A single token (qmv_moe_gemv.hip): whether the kernel takes the call, whether
+// Single tokens (qmv_moe_gemv.hip): whether the kernel takes the call, whether
 // it quantises x itself, and the product (a gate/up pair) or the weighted sum
 // into y.  rows: the activations quantised (moe_gemv_row), or NULL: a.x or a.xq.
 bool moe_gemv_fits(const MoeArgs& a);

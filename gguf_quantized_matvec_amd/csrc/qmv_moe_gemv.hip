@@ -1,6 +1,6 @@
-// Experts' products for single tokens, for gfx950: a pair's weights are read by
-// no other pair, so the multiply is a matrix-vector product bound by the bytes
-// of the experts' weights.  Order and rounding are qmv_launch's (include/qmv.h);
+// Experts' products for single tokens and few of them, for gfx950: hardly any
+// two pairs share an expert, so the multiply is a matrix-vector product a pair,
+// bound by the bytes of the experts' weights.  Order and rounding are qmv_launch's (include/qmv.h);
 // every pair's result is bit-identical to it.
 //
 // Every lane owns one 256-element chunk of one weight row: it streams the
@@ -19,6 +19,7 @@
 //
 // Built with -ffp-contract=off: every float operation is the one written.
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include <type_traits>
@@ -411,7 +412,21 @@ template <int FMT> int launch_fmt(const MoeArgs& m, GemvArgs& a, hipStream_t s) 
 
 bool moe_gemv_fits(const MoeArgs& m) {
     const bool min = m.type == T_Q4_K || m.type == T_Q4_1 || m.type == T_Q5_1;
-    if (m.P / m.top != 1) return false;
+    // Every pair reads its expert's weights here, once a pair; there once an
+    // expert, behind a second launch.  So by the bytes that repeated experts
+    // would read again, as far as the experts of different tokens are
+    // independent (E (1 - (1 - top / E)^T) of them).  Measured, here / there in
+    // us, at repeated MB: 64 experts of 2 x 1024 x 2048 in Q4_0, 8 a token: 8
+    // tokens (52 MB) 23.9 / 29.9, 12 (106 MB) 32.3 / 33.7, 16 41.2 / 33.9; 16 of
+    // 4096 x 4096 in Q6_K, 2 a token: 4 tokens (20 MB) 25.8 / 27.7, 8 (76 MB)
+    // 46.9 / 48.3, 12 67.0 / 53.1.  Matrices beyond 16 MB do not stay in the
+    // caches between two readers: 8 of 2 x 14336 x 4096 in Q4_K, 2 a token: 1
+    // token 28.9 / 31.9, 2 (33 MB) 56.2 / 54.4, 4 98.9 / 86.4.
+    if (m.P > 128) return false;
+    const double T = (double)(m.P / m.top), E = (double)m.E;
+    const double experts = m.top < E ? E * (1.0 - pow(1.0 - m.top / E, T)) : E;
+    const double matrix = (double)(m.w2 ? 2 : 1) * m.N * row_bytes(m.type, m.K);
+    if (T > 1.0 && (matrix > 16e6 || (m.P - experts) * matrix > 60e6)) return false;
     if (m.w2) return m.K <= 8192;                       // two rows a wave at least
     return m.K <= 16384 && m.top <= MOST_SLOTS &&
            m.top * (moe_gemv_row(m.K, min) + 256) + 8 * 256 <= 64 * 1024;

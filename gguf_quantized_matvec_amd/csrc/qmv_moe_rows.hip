@@ -434,7 +434,7 @@ __device__ __forceinline__ void chunk_rows(const Fields<AL>& rb, const uint8_t* 
         }
         // a few blocks at a time: the reads and products of more would run ahead
         // and not fit the registers
-        if constexpr ((b + 1) % (NI == 4 ? 2 : 4) == 0) {
+        if constexpr ((b + 1) % ((NI == 4 ? 2 : 4) / (AL ? 1 : 2)) == 0) {
             if constexpr (NI == 1) asm volatile("" : "+v"(p[0]) : : "memory");
             if constexpr (NI == 2) asm volatile("" : "+v"(p[0]), "+v"(p[1]) : : "memory");
             if constexpr (NI == 4) asm volatile("" : "+v"(p[0]), "+v"(p[1]), "+v"(p[2]), "+v"(p[3]) : : "memory");
@@ -576,10 +576,12 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_moe_rows(RowsArgs a) {
     // the end the last chunk's again: a fetch behind a branch would make each
     // wait for one set of registers wait for the other's too
     auto valid = [&](int c) { return min(c, C - 1); };
+    // Long chunks that need address arithmetic leave registers for one set only.
     constexpr int TURN = PAIR ? 1 : 2;
+    constexpr bool ONE = !AL && R == 16 && NP >= 4;
     v4u r0[NP], r1[NP];
     fetch(wt, ks, r0);
-    fetch(wt2, PAIR ? ks : valid(ks + KS), r1);
+    if constexpr (!ONE) fetch(wt2, PAIR ? ks : valid(ks + KS), r1);
 
     float acc[MATS][NIM];
 #pragma unroll
@@ -668,12 +670,20 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_moe_rows(RowsArgs a) {
         }
         __syncthreads();
         for (; c < c1; c += TURN * KS) {
-            stage(c, r0);
-            fetch(wt, valid(c + TURN * KS), r0);
-            multiply(0, c, c0);
             const int d = PAIR ? c : c + KS;
-            stage(valid(d), r1);
-            fetch(wt2, valid(d + TURN * KS), r1);
+            stage(c, r0);
+            if constexpr (ONE)
+                fetch(wt2, valid(d), r0);
+            else
+                fetch(wt, valid(c + TURN * KS), r0);
+            multiply(0, c, c0);
+            if constexpr (ONE) {
+                stage(valid(d), r0);
+                fetch(wt, valid(c + TURN * KS), r0);
+            } else {
+                stage(valid(d), r1);
+                fetch(wt2, valid(d + TURN * KS), r1);
+            }
             if (PAIR || d < c1) multiply(MATS - 1, d, c0);   // the last segment may end between the two
         }
         if (KS > 1) {
