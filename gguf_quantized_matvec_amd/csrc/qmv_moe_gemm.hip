@@ -48,6 +48,7 @@ template <int FMT> constexpr int block_bytes() {
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 v4h __attribute__((ext_vector_type(4)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) void lds_void;
 
@@ -78,7 +79,7 @@ __device__ __forceinline__ float swiglu(float g, float u) {
 // The bytes that decode one 32-element block of a row.
 template <int FMT> struct Raw { uint32_t v[(block_bytes<FMT>() + 3) / 4]; };
 template <> struct Raw<T_Q4_K> { uint32_t hdr[4], q[8]; };           // d, dmin, scales; the block's 32 nibble bytes
-template <> struct Raw<T_Q6_K> { uint32_t ql[8], qh[8], sd; };       // two sub-scales | d << 16
+template <> struct Raw<T_Q6_K> { uint32_t ql[8], qh[8], sub, d; };   // sub: the block's two sub-scales
 
 // Block b of the row at `row`.
 template <int FMT>
@@ -90,12 +91,10 @@ __device__ __forceinline__ void fetch(const uint8_t* row, int b, Raw<FMT>& r) {
     } else if constexpr (FMT == T_Q6_K) {
         const uint8_t* s = row + (int64_t)210 * (b >> 3);
         const int j = b & 7, h = j >> 2;
-        uint16_t sub, d;
         __builtin_memcpy(r.ql, s + 64 * h + 32 * (j & 1), 32);
         __builtin_memcpy(r.qh, s + 128 + 32 * h, 32);
-        __builtin_memcpy(&sub, s + 192 + 2 * j, 2);
-        __builtin_memcpy(&d, s + 208, 2);
-        r.sd = (uint32_t)sub | ((uint32_t)d << 16);
+        r.sub = *reinterpret_cast<const uint16_t*>(s + 192 + 2 * j);   // not combined here: that would wait for them
+        r.d = *reinterpret_cast<const uint16_t*>(s + 208);
     } else {
         __builtin_memcpy(r.v, row + (int64_t)b * block_bytes<FMT>(), block_bytes<FMT>());
     }
@@ -132,7 +131,7 @@ struct Scale {
 // e of Scale::x holds it for element e; the multiply adds those ones in
 // products of their own, in steps that have any.
 __device__ __forceinline__ bool unfit(const Raw<T_Q6_K>& r) {
-    const int s0 = (int8_t)(r.sd & 0xFF), s1 = (int8_t)((r.sd >> 8) & 0xFF);
+    const int s0 = (int8_t)(r.sub & 0xFF), s1 = (int8_t)((r.sub >> 8) & 0xFF);
     return ((s0 & 1) && (s0 > 64 || s0 < -64)) || ((s1 & 1) && (s1 > 64 || s1 < -64));
 }
 // Bits i and i + 1 of w as the f16 pair of 0 or 1.
@@ -178,8 +177,8 @@ __device__ __forceinline__ void decode(const Raw<FMT>& r, int b, uint32_t (&o)[1
         }
     } else if constexpr (FMT == T_Q6_K) {
         const int kk = b & 3;
-        const int s0 = (int8_t)(r.sd & 0xFF), s1 = (int8_t)((r.sd >> 8) & 0xFF);
-        s.d = r.sd >> 16;
+        const int s0 = (int8_t)(r.sub & 0xFF), s1 = (int8_t)((r.sub >> 8) & 0xFF);
+        s.d = r.d;
         const _Float16 f0 = (_Float16)(float)s0, f1 = (_Float16)(float)s1;
 #pragma unroll
         for (int i = 0; i < 8; i++) {
@@ -269,7 +268,8 @@ __global__ __launch_bounds__(128 * WA, 2) void k_moe_gemm(GemmArgs a) {
     // of one do not wait for the copy into the other
     __shared__ uint4 lw0[TN * PR], lw1[TN * PR], la0[TM * PR], la1[TM * PR];
     __shared__ uint32_t ws[2][SB][TN], as[2][SB][TM];
-    __shared__ uint32_t wx[2][SB][MIN || FMT == T_Q6_K ? TN : 4];
+    __shared__ uint32_t wodd[2][SB][FMT == T_Q6_K ? TN : 4];
+    __shared__ v4f wmin[2][SB][MIN ? TN / 4 : 1];
     __shared__ float ac[2][SB][MIN ? TM : 4];
     __shared__ int pairs[TM], flag[4];
     const int tid = threadIdx.x, lane = tid & 63, wv = uniform(tid >> 6);
@@ -325,18 +325,15 @@ __global__ __launch_bounds__(128 * WA, 2) void k_moe_gemm(GemmArgs a) {
     for (int i = 0; i < NA; i++) {
         const int r = AR * (NA * wv + i) + lane / PR;
         const int piece = slot<PR>(r, lane % PR) - r * PR;    // the exchange is its own inverse
-        asrc[i] = a.codes + ((int64_t)(pairs[r] / a.per) * K + 8 * piece) * 2;
+        asrc[i] = a.codes + ((int64_t)(pairs[r] / a.per) * K + 8 * (piece & 3)) * 2;   // of block 0
     }
     auto issue_a = [&](int h, uint4* la) {
 #pragma unroll
         for (int i = 0; i < NA; i++) {
-            const uint8_t* src = asrc[i] + (int64_t)h * (SB * 64);
-            if (SB * h + SB > nb) {
-                // blocks past the row's end: its last one again, times a weight
-                // scale of 0 (of the i-th piece, block (lane % PR / 4) ^ i)
-                const int past = SB * h + (((lane % PR) >> 2) ^ i) - (nb - 1);
-                src -= past > 0 ? 64 * past : 0;
-            }
+            // block past the row's end: its last one again, times a weight scale
+            // of 0 (the i-th piece is of block (lane % PR / 4) ^ i)
+            const int b = min(SB * h + (((lane % PR) >> 2) ^ i), nb - 1);
+            const uint8_t* src = asrc[i] + (uint32_t)b * 64u;
             __builtin_amdgcn_global_load_lds(src, (lds_void*)(la + AR * (NA * wv + i) * PR), 16, 0, 0);
         }
     };
@@ -364,8 +361,9 @@ __global__ __launch_bounds__(128 * WA, 2) void k_moe_gemm(GemmArgs a) {
         for (int q = 0; q < 4; q++)
             lw[slot<PR>(sr, 4 * sk + q)] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
         ws[PB][sk][sr] = have ? s.d : 0u;
-        if constexpr (MIN || FMT == T_Q6_K) wx[PB][sk][sr] = have ? s.x : 0u;
+        if constexpr (MIN) reinterpret_cast<float*>(wmin[PB][sk])[sr] = have ? __uint_as_float(s.x) : 0.0f;
         if constexpr (FMT == T_Q6_K) {
+            wodd[PB][sk][sr] = have ? s.x : 0u;
             if (have && s.x) flag[h & 3] = 1;
         }
         if (scales) {
@@ -402,7 +400,7 @@ __global__ __launch_bounds__(128 * WA, 2) void k_moe_gemm(GemmArgs a) {
                 v16f I = __builtin_amdgcn_mfma_f32_32x32x16_f16(Wf[0], Af[0], zero16, 0, 0, 0);
                 I = __builtin_amdgcn_mfma_f32_32x32x16_f16(Wf[1], Af[1], I, 0, 0, 0);
                 if constexpr (decltype(odd)::value) {   // what the weights' values left out
-                    const uint32_t w = wx[PB][bk][wrow0 + 32 * i] >> (8 * kq);
+                    const uint32_t w = wodd[PB][bk][wrow0 + 32 * i] >> (8 * kq);
                     each<2>([&](auto hh) {
                         uint4 o;
                         o.x = two_bits(w, 16 * hh);
@@ -416,10 +414,9 @@ __global__ __launch_bounds__(128 * WA, 2) void k_moe_gemm(GemmArgs a) {
                 const v16f S = __builtin_amdgcn_mfma_f32_32x32x8f16(Ws, As, zero16, 0, 0, 0);
 #pragma unroll
                 for (int g = 0; g < 4; g++) {
-                    float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    v4f fs = {};
                     // the minimums of the lane's g-th run of four weight rows
-                    if constexpr (MIN) f = *reinterpret_cast<const float4*>(&wx[PB][bk][64 * wn + 32 * i + 8 * g + 4 * kq]);
-                    const float fs[4] = {f.x, f.y, f.z, f.w};
+                    if constexpr (MIN) fs = wmin[PB][bk][MIN ? 16 * wn + 8 * i + 2 * g + kq : 0];
 #pragma unroll
                     for (int c = 0; c < 4; c++) {
                         float& o = p[i][4 * g + c];
