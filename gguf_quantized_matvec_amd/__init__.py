@@ -25,7 +25,8 @@ EXPORTS = ("qmv_act_bytes", "quantize_act_q8_0", "qmv_launch", "qmv_launch_group
            "qmv_launch_gateup_swiglu_q8k", "qmv_launch_group_q8k", "qmm_launch_q8k", "qmv_partials_q8k_launch", "qmv_prepared_bytes", "qmv_prepare",
            "qmm_launch_q8k_prepared", "qmm_partials_q8k_prepared_launch", "qmv_add_rmsnorm_q8_0", "qmv_add_rmsnorm_q8_k",
            "qmv_kv_bytes", "qmv_kv_append", "qmv_kv_read", "qmv_kv_attention_bytes", "qmv_kv_attention_rows", "qmv_kv_attention",
-           "qmv_moe_route", "qmv_moe_gateup_bytes", "qmv_moe_gateup_swiglu", "qmv_moe_down_bytes", "qmv_moe_down", "qmv_strerror")
+           "qmv_moe_route", "qmv_moe_gateup_bytes", "qmv_moe_gateup_swiglu", "qmv_moe_down_bytes", "qmv_moe_down",
+           "qmv_moe_rows", "qmv_strerror")
 MAX_BATCH = 16
 MAX_GROUP = 8
 MOE_SCORES = {"softmax": 0, "sigmoid": 1}
@@ -111,13 +112,15 @@ def lib() -> ctypes.CDLL:
             getattr(L, f).restype = ctypes.c_size_t
         L.qmv_moe_gateup_swiglu.argtypes = [I, P, P, I64, I64, I64, P, I64, I, P, P, P, P, P]
         L.qmv_moe_down.argtypes = [I, P, I64, I64, I64, P, P, I64, I, P, P, P, P, P]
+        L.qmv_moe_rows.argtypes = [I, I, I64, I, I64, I64, I64]
         for f in ("quantize_act_q8_0", "qmv_launch", "qmv_launch_group", "qmm_launch",
                   "qmv_partials_launch", "qmm_partials_launch", "qmv_launch_noalloc",
                   "qmv_launch_gateup_swiglu", "qmv_launch_gateup_swiglu_q8", "quantize_act_q8_k", "qmv_launch_q8k",
                   "qmv_launch_gateup_swiglu_q8k", "qmv_launch_group_q8k", "qmm_launch_q8k", "qmv_partials_q8k_launch", "qmv_prepare",
                   "qmm_launch_q8k_prepared", "qmm_partials_q8k_prepared_launch", "qmv_add_rmsnorm_q8_0",
                   "qmv_add_rmsnorm_q8_k", "qmv_kv_append", "qmv_kv_read", "qmv_kv_attention_rows",
-                  "qmv_kv_attention", "qmv_moe_route", "qmv_moe_gateup_swiglu", "qmv_moe_down"):
+                  "qmv_kv_attention", "qmv_moe_route", "qmv_moe_gateup_swiglu", "qmv_moe_down",
+                  "qmv_moe_rows"):
             getattr(L, f).restype = I
         L.qmv_strerror.argtypes = [I]
         L.qmv_strerror.restype = ctypes.c_char_p
@@ -315,6 +318,10 @@ def qmv_moe_down(type: int, w: int, E: int, N: int, K: int, idx: int, weight: in
                  h, hq, y: int, work: int, stream: int = 0) -> None:
     _check(lib().qmv_moe_down(type, w, E, N, K, idx, weight, T, top, h, hq, y, work, stream),
            "qmv_moe_down")
+
+
+def qmv_moe_rows(type: int, down: bool, T: int, top: int, E: int, N: int, K: int) -> int:
+    return int(lib().qmv_moe_rows(type, int(down), T, top, E, N, K))
 
 
 def qmv_strerror(code: int) -> str:

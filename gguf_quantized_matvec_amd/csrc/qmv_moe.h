@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "../../include/qmv.h"
 #include "qmv_internal.h"
 
 namespace qmv {
@@ -41,13 +42,24 @@ struct MoeArgs {
 
 // Rows of an expert in one item, at most, which also names the kernel: 4 where
 // no expert has more when a token's experts differ, else 16 (matrix products of
-// 16 columns, qmv_moe_rows.hip), 64 or 128 a tile of the GEMM
-// (qmv_moe_gemm.hip), by the pairs an expert has on average.
-inline int moe_rows(int64_t P, int top, int64_t E) {
-    const int64_t T = P / top;
-    if (P >= 96 * E) return 128;
-    if (P >= 24 * E) return 64;
-    return T <= 4 ? 4 : 16;
+// 16 columns, qmv_moe_rows.hip), or 64 or 128 a tile of the GEMM
+// (qmv_moe_gemm.hip), by the pairs an expert has on average.  Measured with 16,
+// 64 and 128, in us:
+//   pairs an expert                          48            96           192           384
+//   gate/up Q4_K, 8 of 14336 x 4096      399 430 597   705 707 730  1335 1170 1233  2644 2189 2076
+//   gate/up Q4_0, 64 of 1024 x 2048      107 120 161   187 174 222   348  286  333
+//   down Q5_0, 16 of 896 x 4864           65  89  88    86  94  93   145  121  106   264  182  204
+//   down Q6_K, 8 of 4096 x 14336         321 500 305   534 630 597   979  913  760  1873 1588 1228
+// (Q6_K fetches more registers than the smaller tile has, and costs the matrix
+// products of 16 columns two dots a block.)
+inline int moe_rows(int type, int64_t P, int top, int64_t E) {
+    if (type == QMV_Q6_K) {
+        if (P >= 48 * E) return 128;
+    } else {
+        if (P >= 256 * E) return 128;
+        if (P >= 96 * E) return 64;
+    }
+    return P / top <= 4 ? 4 : 16;
 }
 // Items of P pairs, at most: every item but an expert's last is full.
 inline int64_t moe_most_items(int64_t P, int64_t E, int rows) {
@@ -76,8 +88,8 @@ inline __host__ __device__ int moe_gemv_row(int64_t K, bool min) {
 struct MoeWork {
     int64_t blocks, da, ca, items, order, count, total;
 };
-inline MoeWork moe_work(int64_t P, int top, int per, int64_t E, int64_t K) {
-    const int R = moe_rows(P, top, E);
+inline MoeWork moe_work(int type, int64_t P, int top, int per, int64_t E, int64_t K) {
+    const int R = moe_rows(type, P, top, E);
     const int64_t rows = P / per, nb = K / 32;
     MoeWork w;
     w.blocks = 0;
@@ -89,6 +101,15 @@ inline MoeWork moe_work(int64_t P, int top, int per, int64_t E, int64_t K) {
     w.total = w.count + 256;
     return w;
 }
+inline MoeWork moe_work(const MoeArgs& a) { return moe_work(a.type, a.P, a.top, a.per, a.E, a.K); }
+inline int moe_rows(const MoeArgs& a) { return moe_rows(a.type, a.P, a.top, a.E); }
+// Bytes that are enough for every type (Q6_K alone has its own items).
+inline int64_t moe_work_bytes(int64_t P, int top, int per, int64_t E, int64_t K) {
+    const int64_t six = moe_work(QMV_Q6_K, P, top, per, E, K).total;
+    const int64_t others = moe_work(QMV_Q4_0, P, top, per, E, K).total;
+    return six > others ? six : others;
+}
+
 // The products into a.y, by the kernel that fits.
 int launch_moe_product(const MoeArgs& a, hipStream_t s);
 // y[t][n] = sum over slots j with an expert of weight[t][j] * product[t * top + j][n],

@@ -65,7 +65,7 @@ int qmv_moe_route(const float* logits, int64_t T, int64_t E, int score, const fl
 
 size_t qmv_moe_gateup_bytes(int64_t T, int top, int64_t E, int64_t N, int64_t K) {
     if (!pairs_ok(T, E, top) || !shape_ok(N, K, T)) return 0;
-    return (size_t)qmv::moe_work(T * top, top, top, E, K).total;
+    return (size_t)qmv::moe_work_bytes(T * top, top, top, E, K);
 }
 
 int qmv_moe_gateup_swiglu(int type, const void* w_gate, const void* w_up, int64_t E, int64_t N,
@@ -88,7 +88,7 @@ int qmv_moe_gateup_swiglu(int type, const void* w_gate, const void* w_up, int64_
 
 size_t qmv_moe_down_bytes(int64_t T, int top, int64_t E, int64_t N, int64_t K) {
     if (!pairs_ok(T, E, top) || !shape_ok(N, K, T * top)) return 0;
-    return (size_t)(qmv::moe_work(T * top, top, 1, E, K).total + qmv::align256(T * top * N * 4));
+    return (size_t)(qmv::moe_work_bytes(T * top, top, 1, E, K) + qmv::align256(T * top * N * 4));
 }
 
 int qmv_moe_down(int type, const void* w, int64_t E, int64_t N, int64_t K, const int32_t* idx,
@@ -106,10 +106,26 @@ int qmv_moe_down(int type, const void* w, int64_t E, int64_t N, int64_t K, const
     if ((rc = check_device())) return rc;
     hipStream_t s = static_cast<hipStream_t>(stream);
     uint8_t* wk = static_cast<uint8_t*>(work);
-    float* yp = reinterpret_cast<float*>(wk + qmv::moe_work(T * top, top, 1, E, K).total);
+    float* yp = reinterpret_cast<float*>(wk + qmv::moe_work_bytes(T * top, top, 1, E, K));
     const qmv::MoeArgs a{type, static_cast<const uint8_t*>(w), nullptr, E, N, K, idx, T * top, top,
                          1, h, static_cast<const uint8_t*>(hq), wk, yp};
     return launched(qmv::launch_moe_down(a, weight, y, s));
+}
+
+int qmv_moe_rows(int type, int down, int64_t T, int top, int64_t E, int64_t N, int64_t K) {
+    if (check_type(type, K) || !pairs_ok(T, E, top) || !shape_ok(N, K, down ? T * top : T)) return 0;
+    qmv::MoeArgs a{};
+    static const uint8_t some = 0;
+    a.type = type;
+    a.w = &some;
+    a.w2 = down ? nullptr : &some;
+    a.E = E;
+    a.N = N;
+    a.K = K;
+    a.P = T * top;
+    a.top = top;
+    a.per = down ? 1 : top;
+    return qmv::moe_gemv_fits(a) ? 1 : qmv::moe_rows(a);
 }
 
 }  // extern "C"

@@ -13,15 +13,25 @@
 // leave four adjacent floats at a time, a gate's and an up's element meet in
 // one lane, and a block's minimum term takes one activation scalar a lane.
 //
-// A workgroup of 4 waves owns 128 weight rows (of a gate/up pair 64 of each,
-// in runs of 32) x 64 AT rows of an expert; a wave owns 64 x 32 AT.  K is
-// walked two blocks a step: the activations' f16 codes go from memory to LDS
-// directly, a thread decodes one weight block into LDS, both into the buffers
-// of the next step, while the current ones are multiplied; one barrier a step.
-// 64 x 64 a wave, because the matrix operands come from LDS: per block 8 KB
-// for four tiles (64 of its cycles) against 4 x 96 of the matrix cores; 64 x
-// 32 a wave would take 48 for 2 x 96.  73 KB and 256 registers leave two
-// workgroups a compute unit, whose barriers do not meet.
+// A workgroup of 8 (4) waves owns 128 weight rows (of a gate/up pair 64 of
+// each, in runs of 32) x 128 (64) rows of an expert; a wave owns 64 x 32: its
+// sums, the chunk's and the row's, and two tiles' products take 128 of 256
+// registers, and 64 x 64 would spill them.  K is walked four (two) blocks a
+// step: the activations' f16 codes go from memory to LDS directly, a thread
+// decodes one weight block into LDS, both into the buffers of the next step,
+// while the current ones are multiplied; one barrier a step.  144 (73) KB leave
+// one workgroup a compute unit (two), two waves a SIMD.
+//
+// What bounds it is the vector unit, not the matrix cores: of a 32 x 32 tile's
+// block 96 cycles of MFMA, but 16 fma with their 4 cycles each (32 with a
+// minimum) and about 20 more operations of the decoding, which 128 rows share.
+// Counted at 2048 tokens, 2 of 8 experts of 2 x 14336 x 4096 in Q4_K: vector
+// units 55-60 % busy, matrix cores 24 %, a third of the waves' time waiting at
+// the barrier or for LDS.  Measured there 2748 us (350 TFLOP/s), and 1541 us
+// (312) for 4096 x 14336 in Q6_K; the multiply alone, without decoding and
+// fetching, took 1594 and 730.  Half the waves decoding after they multiply
+// instead of before gave 2628 and 1594; with operands read a block ahead as
+// well 2803 (Q6_K spills).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -247,6 +257,7 @@ struct GemmArgs {
     const int32_t *items, *order, *count;
     float* y;
     bool vec;                      // rows of y begin 16-byte aligned
+    int64_t from;                  // the launch's first workgroup, a multiple of 8
 };
 
 // Where piece q of tile row r stands, rows of PR 16-byte pieces: pieces change
@@ -280,7 +291,7 @@ __global__ __launch_bounds__(128 * WA, 2) void k_moe_gemm(GemmArgs a) {
     // them, in which an expert's rows advance fastest
     const int NT = (int)((a.N + COLS - 1) / COLS);
     const int64_t total = (int64_t)*a.count * NT;
-    const int64_t x = blockIdx.x & 7, k = blockIdx.x >> 3, share = total >> 3, rest = total & 7;
+    const int64_t x = blockIdx.x & 7, k = (a.from + blockIdx.x) >> 3, share = total >> 3, rest = total & 7;
     if (k >= share + (x < rest)) return;
     const int64_t L = x * share + (x < rest ? x : rest) + k;
     const int4 it = reinterpret_cast<const int4*>(a.items)[L / NT];
@@ -498,21 +509,28 @@ template <int FMT, bool PAIR, int WA>
 int launch_at(const MoeArgs& m, GemmArgs& a, hipStream_t s) {
     constexpr int COLS = PAIR ? TN / 2 : TN;
     const int64_t tiles = moe_most_items(m.P, m.E, 32 * WA) * ((m.N + COLS - 1) / COLS);
-    hipLaunchKernelGGL((k_moe_gemm<FMT, PAIR, WA>), dim3((unsigned)((tiles + 7) / 8 * 8)),
-                       dim3(128 * WA), 0, s, a);
-    return (int)hipGetLastError();
+    // a grid's dimension ends below 2^32 threads
+    constexpr int64_t MOST = ((int64_t)1 << 31) / (128 * WA);
+    for (a.from = 0; a.from < tiles; a.from += MOST) {
+        const int64_t n = tiles - a.from < MOST ? tiles - a.from : MOST;
+        hipLaunchKernelGGL((k_moe_gemm<FMT, PAIR, WA>), dim3((unsigned)((n + 7) / 8 * 8)),
+                           dim3(128 * WA), 0, s, a);
+        const int rc = (int)hipGetLastError();
+        if (rc) return rc;
+    }
+    return 0;
 }
 
 template <int FMT> int launch_fmt(const MoeArgs& m, GemmArgs& a, hipStream_t s) {
-    const bool big = moe_rows(m.P, m.top, m.E) == 128;
-    if (m.w2) return big ? launch_at<FMT, true, 4>(m, a, s) : launch_at<FMT, true, 2>(m, a, s);
-    return big ? launch_at<FMT, false, 4>(m, a, s) : launch_at<FMT, false, 2>(m, a, s);
+    if constexpr (FMT != T_Q6_K)
+        if (moe_rows(m) == 64) return m.w2 ? launch_at<FMT, true, 2>(m, a, s) : launch_at<FMT, false, 2>(m, a, s);
+    return m.w2 ? launch_at<FMT, true, 4>(m, a, s) : launch_at<FMT, false, 4>(m, a, s);
 }
 
 }  // namespace
 
 int launch_moe_gemm(const MoeArgs& m, hipStream_t s) {
-    const MoeWork L = moe_work(m.P, m.top, m.per, m.E, m.K);
+    const MoeWork L = moe_work(m);
     GemmArgs a{};
     a.w = m.w;
     a.w2 = m.w2;

@@ -13,8 +13,8 @@
 // operand of v_mfma_i32_16x16x32_i8.  Result element i of the lane is
 // activation row 4 kg + i of the instruction; the item's row j stands at
 // 4 (j % 4) + j / 4, so that up to 4 NI rows need the elements i < NI only (NI
-// = 1, 2, 4, by the item's rows): few rows cost few f32 terms.  The item's activations lie in LDS, a
-// segment of chunks at a time, shared by the 8 waves.
+// = 1, 2, 4, by the item's rows): few rows cost few f32 terms.  The item's
+// activations lie in LDS, a segment of chunks at a time, shared by the 8 waves.
 //
 // Order inside a block does not matter (the integers are exact), so lane kg
 // takes bytes 4kg .. 4kg+3 of a 16-byte nibble block, low and high nibbles,
@@ -783,7 +783,7 @@ int launch_rows(const MoeArgs& m, RowsArgs& a, hipStream_t s) {
 }
 
 template <int FMT, bool PAIR> int launch_fmt(const MoeArgs& m, RowsArgs& a, hipStream_t s) {
-    const bool four = moe_rows(m.P, m.top, m.E) == 4;
+    const bool four = moe_rows(m) == 4;
     if constexpr (can_align<FMT>()) {
         if (m.K % 256 == 0)
             return four ? launch_rows<FMT, PAIR, 4, true>(m, a, s) : launch_rows<FMT, PAIR, 16, true>(m, a, s);
@@ -854,7 +854,7 @@ static int launch_moe_combine(const float* yp, const int32_t* idx, const float* 
 // the kernel takes them (f16 for the GEMM, rows for the GEMV, else Q8_0 blocks
 // of x).
 static int prepare(const MoeArgs& m, bool plan, bool gemm, bool gemv, hipStream_t s) {
-    const MoeWork L = moe_work(m.P, m.top, m.per, m.E, m.K);
+    const MoeWork L = moe_work(m);
     PrepArgs p{};
     p.x = m.x;
     p.xq = m.xq;
@@ -872,7 +872,7 @@ static int prepare(const MoeArgs& m, bool plan, bool gemm, bool gemv, hipStream_
     p.idx = m.idx;
     p.P = (int32_t)m.P;
     p.E = (int32_t)m.E;
-    p.R = moe_rows(m.P, m.top, m.E);
+    p.R = moe_rows(m);
     p.planners = plan ? p.E + 1 : 0;
     p.items = reinterpret_cast<int32_t*>(m.work + L.items);
     p.order = reinterpret_cast<int32_t*>(m.work + L.order);
@@ -886,8 +886,8 @@ static int prepare(const MoeArgs& m, bool plan, bool gemm, bool gemv, hipStream_
 
 int launch_moe_product(const MoeArgs& m, hipStream_t s) {
     if (m.w2 && moe_gemv_fits(m)) return launch_moe_gemv(m, nullptr, nullptr, m.y, s);
-    const MoeWork L = moe_work(m.P, m.top, m.per, m.E, m.K);
-    const bool gemm = moe_rows(m.P, m.top, m.E) >= 64;
+    const MoeWork L = moe_work(m);
+    const bool gemm = moe_rows(m) >= 64;
     const int rc = prepare(m, gemm || m.P > MOE_SCAN, gemm, false, s);
     if (rc) return rc;
     if (gemm) return launch_moe_gemm(m, s);
@@ -925,7 +925,7 @@ int launch_moe_down(const MoeArgs& m, const float* weight, float* y, hipStream_t
         if (m.x && !moe_gemv_quantises(m)) {
             const int rc = prepare(m, false, false, true, s);
             if (rc) return rc;
-            rows = m.work + moe_work(m.P, m.top, m.per, m.E, m.K).blocks;
+            rows = m.work + moe_work(m).blocks;
         }
         return launch_moe_gemv(m, rows, weight, y, s);
     }

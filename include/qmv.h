@@ -532,9 +532,9 @@ enum qmv_moe_score { QMV_MOE_SOFTMAX = 0, QMV_MOE_SIGMOID = 1 };
  * groups too, the lowest number first.  weight = scale * s_e, divided by the
  * sum of s over the chosen experts with renorm != 0 (0 where that sum is 0),
  * in f64 and rounded once.  An expert whose logit or bias is -inf or NaN is
- * not available (its s is left out of no sum, being 0, unless it is the bias
- * that excludes it); where fewer than `top` are, the slots left have idx -1
- * and weight 0.  An infinite logit is a softmax's whole weight, shared with
+ * not available: a logit of these has s = 0, a bias of these leaves s in the
+ * softmax's sum.  Where fewer than `top` are, the slots left have idx -1 and
+ * weight 0.  An infinite logit is a softmax's whole weight, shared with
  * its equals.  top <= top_groups * (E / groups); scale finite. */
 int qmv_moe_route(const float* logits, int64_t T, int64_t E, int score, const float* bias,
                   int groups, int top_groups, int group_top, int top, int renorm, float scale,
@@ -568,6 +568,11 @@ int qmv_moe_gateup_swiglu(int type, const void* w_gate, const void* w_up, int64_
 int qmv_moe_down(int type, const void* w, int64_t E, int64_t N, int64_t K, const int32_t* idx,
                  const float* weight, int64_t T, int top, const float* h, const void* hq, float* y,
                  void* work, void* stream);
+
+/* The rows of an expert that a workgroup of such a call (down 0: the gate/up
+ * pair) takes, which names its kernel: 1, 4, 16, 64 or 128; 0 for invalid
+ * arguments.  For tests that mean a kernel; nothing is enqueued. */
+int qmv_moe_rows(int type, int down, int64_t T, int top, int64_t E, int64_t N, int64_t K);
 
 /* Static text for a status code. */
 const char* qmv_strerror(int code);

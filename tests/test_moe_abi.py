@@ -74,6 +74,17 @@ def test_workspaces():
         assert g.qmv_moe_down_bytes(*bad) == 0
 
 
+def test_the_kernel_of_a_call():
+    # type, down, T, top, E, N, K
+    assert g.qmv_moe_rows(g.Q4_0, 0, 1, 2, 8, 48, 64) == g.qmv_moe_rows(g.Q4_0, 1, 1, 2, 8, 48, 64) == 1
+    assert [g.qmv_moe_rows(g.Q4_0, 0, T, 2, 2, 48, 16384) for T in (4, 5, 95, 96, 255, 256)] == [4, 16, 16, 64, 64, 128]
+    assert [g.qmv_moe_rows(g.Q6_K, 1, T, 2, 2, 48, 16384 + 256) for T in (4, 5, 47, 48)] == [4, 16, 16, 128]
+    for bad in [(99, 0, 4, 2, 8, 48, 64), (g.Q4_0, 0, 0, 2, 8, 48, 64), (g.Q4_0, 0, 4, 33, 64, 48, 64),
+                (g.Q4_0, 1, 4, 2, 0, 48, 64), (g.Q4_0, 1, 4, 2, 8, 0, 64), (g.Q4_0, 1, 4, 2, 8, 48, 48),
+                (g.Q4_K, 1, 4, 2, 8, 48, 288), (g.Q4_0, 1, 1 << 18, 1, 8, 48, 1 << 15)]:
+        assert g.qmv_moe_rows(*bad) == 0
+
+
 def test_python_refusals():
     torch = pytest.importorskip("torch")
     t = torch.zeros(4, 16)
