@@ -45,13 +45,13 @@ struct MoeArgs {
 // 16 columns, qmv_moe_rows.hip), or 64 or 128 a tile of the GEMM
 // (qmv_moe_gemm.hip), by the pairs an expert has on average.  Measured with 16,
 // 64 and 128, in us:
-//   pairs an expert                          48            96           192           384
-//   gate/up Q4_K, 8 of 14336 x 4096      399 430 597   705 707 730  1335 1170 1233  2644 2189 2076
-//   gate/up Q4_0, 64 of 1024 x 2048      107 120 161   187 174 222   348  286  333
-//   down Q5_0, 16 of 896 x 4864           65  89  88    86  94  93   145  121  106   264  182  204
-//   down Q6_K, 8 of 4096 x 14336         321 500 305   534 630 597   979  913  760  1873 1588 1228
-// (Q6_K fetches more registers than the smaller tile has, and costs the matrix
-// products of 16 columns two dots a block.)
+//   pairs an expert                          48            96           192             384
+//   gate/up Q4_K, 8 of 14336 x 4096      403 443 569   704 731 686  1338 1210 1162  2631 2259 1963
+//   gate/up Q4_0, 64 of 1024 x 2048      106 114 152   187 178 198   350  295  299
+//   down Q5_0, 16 of 896 x 4864           65  92 123    86  96 127   145  129  139   264  188  196
+//   down Q6_K, 8 of 4096 x 14336         321  -  305   534  -  597   979   -   760  1873   -  1228
+// (Q6_K has no tile of 64, whose decoding it would not share enough, and costs
+// the matrix products of 16 columns two dots a block.)
 inline int moe_rows(int type, int64_t P, int top, int64_t E) {
     if (type == QMV_Q6_K) {
         if (P >= 48 * E) return 128;

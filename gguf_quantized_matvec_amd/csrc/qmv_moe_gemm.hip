@@ -13,25 +13,28 @@
 // leave four adjacent floats at a time, a gate's and an up's element meet in
 // one lane, and a block's minimum term takes one activation scalar a lane.
 //
-// A workgroup of 8 (4) waves owns 128 weight rows (of a gate/up pair 64 of
-// each, in runs of 32) x 128 (64) rows of an expert; a wave owns 64 x 32: its
-// sums, the chunk's and the row's, and two tiles' products take 128 of 256
-// registers, and 64 x 64 would spill them.  K is walked four (two) blocks a
-// step: the activations' f16 codes go from memory to LDS directly, a thread
-// decodes one weight block into LDS, both into the buffers of the next step,
-// while the current ones are multiplied; one barrier a step.  144 (73) KB leave
-// one workgroup a compute unit (two), two waves a SIMD.
+// A workgroup of 4 waves owns 128 weight rows (of a gate/up pair 64 of each, in
+// runs of 32) x 128 or 64 rows of an expert, a wave 64 x 64 or 64 x 32 of them;
+// Q6_K, whose fetched bytes leave no registers for 64 x 64, has 8 waves of 64 x
+// 32.  K is walked two blocks (8 waves: four) a step: the activations' f16
+// codes go from memory to LDS directly, a thread decodes one weight block into
+// LDS, both into the buffers of the next step, while the current ones are
+// multiplied; one barrier a step.  74 KB (8 waves: 145) and 256 registers leave
+// two waves a SIMD, of two workgroups, whose barriers do not meet.
 //
-// What bounds it is the vector unit, not the matrix cores: of a 32 x 32 tile's
-// block 96 cycles of MFMA, but 16 fma with their 4 cycles each (32 with a
-// minimum) and about 20 more operations of the decoding, which 128 rows share.
-// Counted at 2048 tokens, 2 of 8 experts of 2 x 14336 x 4096 in Q4_K: vector
-// units 55-60 % busy, matrix cores 24 %, a third of the waves' time waiting at
-// the barrier or for LDS.  Measured there 2748 us (350 TFLOP/s), and 1541 us
-// (312) for 4096 x 14336 in Q6_K; the multiply alone, without decoding and
-// fetching, took 1594 and 730.  Half the waves decoding after they multiply
-// instead of before gave 2628 and 1594; with operands read a block ahead as
-// well 2803 (Q6_K spills).
+// 64 x 64 a wave, because the operands come from LDS: 2 KB a tile of 32 x 32
+// and block, 16 of the unit's cycles against 24 of its four matrix cores; 64 x
+// 32 takes 24, 32 x 32 (16 waves) 32.  Measured at 2048 tokens, 2 of 8 experts
+// of 2 x 14336 x 4096 (4096 x 14336): Q4_0 1823 (1091) us, with 64 x 32 2047
+// (1159), with 32 x 32 2369; Q4_K 2488 (1499), 2649 (1499), 2687; Q8_0 2030,
+// 2241, 2212; Q6_K down 1528 with 64 x 32, 1561 with 64 x 64, 2319 with 32 x 32.
+// That is 315 to 530 TFLOP/s.  Matrix cores 24 to 35 % busy, vector units 45 to
+// 60 %: of a tile's block 96 cycles of MFMA, but 16 fma of 4 cycles (32 with a
+// minimum) and 15 to 20 operations of the decoding, which the tile's rows
+// share.  Without the decoding 16 waves took 1550 instead of 2369 us.  Half of
+// 8 waves decoding after they multiply instead of before gave 4 % for Q4_K and
+// lost 4 % for Q6_K; operands read a block ahead lost 6 %; a raised priority
+// while multiplying changed nothing.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -77,6 +80,13 @@ template <int N, class Fn> __device__ __forceinline__ void each(Fn&& f) {
     each_of(f, std::make_integer_sequence<int, N>{});
 }
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// The 16 values are computed here, not later where they are used.
+__device__ __forceinline__ void pin16(float (&v)[16]) {
+    asm volatile("" : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3]), "+v"(v[4]), "+v"(v[5]), "+v"(v[6]), "+v"(v[7]),
+                      "+v"(v[8]), "+v"(v[9]), "+v"(v[10]), "+v"(v[11]), "+v"(v[12]), "+v"(v[13]), "+v"(v[14]),
+                      "+v"(v[15]) : : "memory");
+}
 
 // silu(g) u in f64 as t = exp(-g), s = g / (1 + t), s u, rounded once.
 __device__ __forceinline__ float swiglu(float g, float u) {
@@ -267,17 +277,20 @@ template <int PR> __device__ __forceinline__ int slot(int r, int q) {
     return r * PR + (q ^ (PR == 16 ? r & 15 : (r >> 1) & 7));
 }
 
-template <int FMT, bool PAIR, int WA>
-__global__ __launch_bounds__(128 * WA, 2) void k_moe_gemm(GemmArgs a) {
-    constexpr int THREADS = 128 * WA;                 // 2 x WA waves
-    constexpr int SB = WA;                            // blocks a step: a weight block a thread
+template <int FMT, bool PAIR, int AT, int WM>
+__global__ __launch_bounds__(128 * WM, 2) void k_moe_gemm(GemmArgs a) {
+    constexpr int THREADS = 128 * WM;                 // 2 x WM waves
+    constexpr int SB = WM;                            // blocks a step: a weight block a thread
     constexpr int PR = 4 * SB;                        // 16-byte pieces of a tile row in a step
-    constexpr int TM = 32 * WA;                       // rows of the expert in a tile
+    constexpr int TM = 32 * AT * WM;                  // rows of the expert in a tile
     constexpr int COLS = PAIR ? TN / 2 : TN;          // outputs of a row
+    // the weights: piece q of row r at q WP + r, so that the pieces' places differ by
+    // constants, and SB blocks of 16 / SB rows (one pass of a 16-byte write) meet all banks
+    constexpr int WP = TN + 4 / SB;
     constexpr bool MIN = has_min<FMT>();
     // two objects a kind, not one of two halves: the compiler sees that reads
     // of one do not wait for the copy into the other
-    __shared__ uint4 lw0[TN * PR], lw1[TN * PR], la0[TM * PR], la1[TM * PR];
+    __shared__ uint4 lw0[WP * PR], lw1[WP * PR], la0[TM * PR], la1[TM * PR];
     __shared__ uint32_t ws[2][SB][TN], as[2][SB][TM];
     __shared__ uint32_t wodd[2][SB][FMT == T_Q6_K ? TN : 4];
     __shared__ v4f wmin[2][SB][MIN ? TN / 4 : 1];
@@ -342,8 +355,9 @@ __global__ __launch_bounds__(128 * WA, 2) void k_moe_gemm(GemmArgs a) {
 #pragma unroll
         for (int i = 0; i < NA; i++) {
             // block past the row's end: its last one again, times a weight scale
-            // of 0 (the i-th piece is of block (lane % PR / 4) ^ i)
-            const int b = min(SB * h + (((lane % PR) >> 2) ^ i), nb - 1);
+            // of 0 (the exchange of pieces takes two bits, of SB = 2 one, of a tile row's
+            // number to the block's; of the i-th row they are i's lowest)
+            const int b = min(SB * h + (((lane % PR) >> 2) ^ (i & (SB - 1))), nb - 1);
             const uint8_t* src = asrc[i] + (uint32_t)b * 64u;
             __builtin_amdgcn_global_load_lds(src, (lds_void*)(la + AR * (NA * wv + i) * PR), 16, 0, 0);
         }
@@ -370,7 +384,7 @@ __global__ __launch_bounds__(128 * WA, 2) void k_moe_gemm(GemmArgs a) {
         const bool have = b < nb;
 #pragma unroll
         for (int q = 0; q < 4; q++)
-            lw[slot<PR>(sr, 4 * sk + q)] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            lw[(4 * sk + q) * WP + sr] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
         ws[PB][sk][sr] = have ? s.d : 0u;
         if constexpr (MIN) reinterpret_cast<float*>(wmin[PB][sk])[sr] = have ? __uint_as_float(s.x) : 0.0f;
         if constexpr (FMT == T_Q6_K) {
@@ -383,63 +397,74 @@ __global__ __launch_bounds__(128 * WA, 2) void k_moe_gemm(GemmArgs a) {
         }
     };
 
-    float p[2][16], y[2][16];      // of weight rows 0 .. 31 and 32 .. 63 of the wave's
+    // tile (i, j): weight rows 32 i and activation rows 32 j onward of the wave's
+    float p[2][AT][16], y[2][AT][16];
     each<2>([&](auto i) {
+        each<AT>([&](auto j) {
 #pragma unroll
-        for (int c = 0; c < 16; c++) p[i][c] = y[i][c] = 0.0f;
+            for (int c = 0; c < 16; c++) p[i][j][c] = y[i][j][c] = 0.0f;
+        });
     });
     const v16f zero16 = {};
     const uint32_t first_k = kq ? 0u : ~0u;   // of the rank-1 product only k = 0 counts
-    const int wrow0 = 64 * wn + lr, arow = 32 * wa + lr;
+    const int wrow0 = 64 * wn + lr, arow = 32 * AT * wa + lr;
 
-    // the product of the buffers of parity P; ODD: a Q6_K step with values that left out a bit
-    auto multiply = [&](auto par, auto odd) {
+    uint32_t apiece = 16 * slot<PR>(arow, kq);        // where the lane's first piece stands
+
+    // the product of the buffers of parity P; odd: a Q6_K step with values that left out a bit
+    auto multiply = [&](auto par, bool odd) {
         constexpr int PB = decltype(par)::value;
         const uint4* lw = PB ? lw1 : lw0;
         const uint4* la = PB ? la1 : la0;
+        asm volatile("" : "+v"(apiece));              // the pieces' places are computed here, not kept
         each<SB>([&](auto bk) {
-            v8h Af[2];
-            each<2>([&](auto hh) { Af[hh] = __builtin_bit_cast(v8h, la[slot<PR>(arow, 4 * bk + 2 * hh + kq)]); });
-            const v4h As = __builtin_bit_cast(v4h, make_uint2(as[PB][bk][arow], 0u));
-            const float ca = MIN ? ac[PB][bk][MIN ? arow : 0] : 0.0f;
-            each<2>([&](auto i) {
-                v8h Wf[2];
+            v8h Af[AT][2], Wf[2][2];
+            each<AT>([&](auto j) {
                 each<2>([&](auto hh) {
-                    Wf[hh] = __builtin_bit_cast(v8h, lw[slot<PR>(wrow0 + 32 * i, 4 * bk + 2 * hh + kq)]);
+                    Af[j][hh] = __builtin_bit_cast(v8h, *(const uint4*)((const char*)la + (apiece ^ (16 * (4 * bk + 2 * hh))) +
+                                                                        512 * PR * j));
                 });
-                const v4h Ws = __builtin_bit_cast(v4h, make_uint2(ws[PB][bk][wrow0 + 32 * i] & first_k, 0u));
-                v16f I = __builtin_amdgcn_mfma_f32_32x32x16_f16(Wf[0], Af[0], zero16, 0, 0, 0);
-                I = __builtin_amdgcn_mfma_f32_32x32x16_f16(Wf[1], Af[1], I, 0, 0, 0);
-                if constexpr (decltype(odd)::value) {   // what the weights' values left out
-                    const uint32_t w = wodd[PB][bk][wrow0 + 32 * i] >> (8 * kq);
-                    each<2>([&](auto hh) {
-                        uint4 o;
-                        o.x = two_bits(w, 16 * hh);
-                        o.y = two_bits(w, 16 * hh + 2);
-                        o.z = two_bits(w, 16 * hh + 4);
-                        o.w = two_bits(w, 16 * hh + 6);
-                        I = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, o), Af[hh], I, 0, 0, 0);
-                    });
-                    asm volatile("" : "+v"(I));   // rare: one tile at a time, for the registers
-                }
-                const v16f S = __builtin_amdgcn_mfma_f32_32x32x8f16(Ws, As, zero16, 0, 0, 0);
-#pragma unroll
-                for (int g = 0; g < 4; g++) {
-                    v4f fs = {};
-                    // the minimums of the lane's g-th run of four weight rows
-                    if constexpr (MIN) fs = wmin[PB][bk][MIN ? 16 * wn + 8 * i + 2 * g + kq : 0];
-#pragma unroll
-                    for (int c = 0; c < 4; c++) {
-                        float& o = p[i][4 * g + c];
-                        o = fmaf(I[4 * g + c], S[4 * g + c], o);
-                        if constexpr (MIN) o = fmaf(fs[c], ca, o);
-                    }
-                }
             });
-            // Q6_K's fetched bytes leave no registers for a third tile in flight; a
-            // spill would wait for the fetches, which count as memory loads too
-            if constexpr (FMT == T_Q6_K) __builtin_amdgcn_sched_barrier(0);
-            if constexpr (FMT == T_Q6_K) asm volatile("" : "+v"(p[0][15]), "+v"(p[1][15]) : : "memory");
+            each<2>([&](auto i) {
+                each<2>([&](auto hh) { Wf[i][hh] = __builtin_bit_cast(v8h, lw[(4 * bk + 2 * hh + kq) * WP + wrow0 + 32 * i]); });
+            });
+            each<2>([&](auto i) {
+                const v4h Ws = __builtin_bit_cast(v4h, make_uint2(ws[PB][bk][wrow0 + 32 * i] & first_k, 0u));
+                each<AT>([&](auto j) {
+                    const v4h As = __builtin_bit_cast(v4h, make_uint2(as[PB][bk][arow + 32 * j], 0u));
+                    const float ca = MIN ? ac[PB][bk][MIN ? arow + 32 * j : 0] : 0.0f;
+                    v16f I = __builtin_amdgcn_mfma_f32_32x32x16_f16(Wf[i][0], Af[j][0], zero16, 0, 0, 0);
+                    const v16f S = __builtin_amdgcn_mfma_f32_32x32x8f16(Ws, As, zero16, 0, 0, 0);
+                    I = __builtin_amdgcn_mfma_f32_32x32x16_f16(Wf[i][1], Af[j][1], I, 0, 0, 0);
+                    if (FMT == T_Q6_K && odd) {   // what the weights' values left out
+                        const uint32_t w = wodd[PB][bk][wrow0 + 32 * i] >> (8 * kq);
+                        each<2>([&](auto hh) {
+                            uint4 o;
+                            o.x = two_bits(w, 16 * hh);
+                            o.y = two_bits(w, 16 * hh + 2);
+                            o.z = two_bits(w, 16 * hh + 4);
+                            o.w = two_bits(w, 16 * hh + 6);
+                            I = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, o), Af[j][hh], I, 0, 0, 0);
+                        });
+                    }
+#pragma unroll
+                    for (int g = 0; g < 4; g++) {
+                        v4f fs = {};
+                        // the minimums of the lane's g-th run of four weight rows
+                        if constexpr (MIN) fs = wmin[PB][bk][MIN ? 16 * wn + 8 * i + 2 * g + kq : 0];
+#pragma unroll
+                        for (int c = 0; c < 4; c++) {
+                            float& o = p[i][j][4 * g + c];
+                            o = fmaf(I[4 * g + c], S[4 * g + c], o);
+                            if constexpr (MIN) o = fmaf(fs[c], ca, o);
+                        }
+                    }
+                    pin16(p[i][j]);
+                    // one tile after another where registers are short (2048 tokens, down of
+                    // 4096 x 14336: Q4_K 1574 -> 1523 us; Q4_0 1098 -> 1127)
+                    if constexpr (FMT == T_Q4_K || FMT == T_Q6_K) __builtin_amdgcn_sched_barrier(0);
+                });
+            });
         });
     };
     auto step = [&](int h, auto par) {
@@ -454,22 +479,23 @@ __global__ __launch_bounds__(128 * WA, 2) void k_moe_gemm(GemmArgs a) {
             if (tid == 0) flag[(h + 3) & 3] = 0;      // read a step ago, set again in two steps
         }
         if (h + 1 < H) {
+            // the longest decoding starts after the copies (Q6_K 1606 -> 1561 us; others lose 1 %)
+            if constexpr (FMT == T_Q6_K) issue_a(h + 1, Next::value ? la1 : la0);
             stage(h + 1, Next{});
-            issue_a(h + 1, Next::value ? la1 : la0);
+            if constexpr (FMT != T_Q6_K) issue_a(h + 1, Next::value ? la1 : la0);
             if (h + 2 < H) fetch_step(h + 2);
         }
-        if (FMT == T_Q6_K && odd)
-            multiply(par, std::integral_constant<bool, FMT == T_Q6_K>{});
-        else
-            multiply(par, std::false_type{});
+        multiply(par, odd);
         // the end of a chunk of 8 blocks (of SB = 4 every other step: par says which)
         if ((SB == 4 ? Par::value == 1 : (h & 3) == 3) || h + 1 == H) {
             each<2>([&](auto i) {
+                each<AT>([&](auto j) {
 #pragma unroll
-                for (int c = 0; c < 16; c++) {
-                    y[i][c] = y[i][c] + p[i][c];
-                    p[i][c] = 0.0f;
-                }
+                    for (int c = 0; c < 16; c++) {
+                        y[i][j][c] = y[i][j][c] + p[i][j][c];
+                        p[i][j][c] = 0.0f;
+                    }
+                });
             });
         }
     };
@@ -483,38 +509,40 @@ __global__ __launch_bounds__(128 * WA, 2) void k_moe_gemm(GemmArgs a) {
         if (h + 1 < H) step(h + 1, std::integral_constant<int, 1>{});
     }
 
-    // lane: row arow; element c of tile i: weight row 8 (c / 4) + 4 kq + c % 4
-    if (arow >= rows) return;
-    float* out = a.y + pairs[arow] * N;
-    each<PAIR ? 1 : 2>([&](auto i) {
+    // lane: row arow + 32 j; element c of tile i: weight row 8 (c / 4) + 4 kq + c % 4
+    each<AT>([&](auto j) {
+        if (arow + 32 * j >= rows) return;
+        float* out = a.y + pairs[arow + 32 * j] * N;
+        each<PAIR ? 1 : 2>([&](auto i) {
 #pragma unroll
-        for (int g = 0; g < 4; g++) {
-            const int64_t n = n0 + (PAIR ? 32 * wn : 64 * wn + 32 * i) + 8 * g + 4 * kq;
-            float v[4];
-#pragma unroll
-            for (int c = 0; c < 4; c++)
-                v[c] = PAIR ? swiglu(y[0][4 * g + c], y[1][4 * g + c]) : y[i][4 * g + c];
-            if (a.vec && n + 4 <= N) {
-                *reinterpret_cast<float4*>(out + n) = make_float4(v[0], v[1], v[2], v[3]);
-            } else {
+            for (int g = 0; g < 4; g++) {
+                const int64_t n = n0 + (PAIR ? 32 * wn : 64 * wn + 32 * i) + 8 * g + 4 * kq;
+                float v[4];
 #pragma unroll
                 for (int c = 0; c < 4; c++)
-                    if (n + c < N) out[n + c] = v[c];
+                    v[c] = PAIR ? swiglu(y[0][j][4 * g + c], y[1][j][4 * g + c]) : y[i][j][4 * g + c];
+                if (a.vec && n + 4 <= N) {
+                    *reinterpret_cast<float4*>(out + n) = make_float4(v[0], v[1], v[2], v[3]);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; c++)
+                        if (n + c < N) out[n + c] = v[c];
+                }
             }
-        }
+        });
     });
 }
 
-template <int FMT, bool PAIR, int WA>
+template <int FMT, bool PAIR, int AT, int WM>
 int launch_at(const MoeArgs& m, GemmArgs& a, hipStream_t s) {
     constexpr int COLS = PAIR ? TN / 2 : TN;
-    const int64_t tiles = moe_most_items(m.P, m.E, 32 * WA) * ((m.N + COLS - 1) / COLS);
+    const int64_t tiles = moe_most_items(m.P, m.E, 32 * AT * WM) * ((m.N + COLS - 1) / COLS);
     // a grid's dimension ends below 2^32 threads
-    constexpr int64_t MOST = ((int64_t)1 << 31) / (128 * WA);
+    constexpr int64_t MOST = ((int64_t)1 << 31) / (128 * WM);
     for (a.from = 0; a.from < tiles; a.from += MOST) {
         const int64_t n = tiles - a.from < MOST ? tiles - a.from : MOST;
-        hipLaunchKernelGGL((k_moe_gemm<FMT, PAIR, WA>), dim3((unsigned)((n + 7) / 8 * 8)),
-                           dim3(128 * WA), 0, s, a);
+        hipLaunchKernelGGL((k_moe_gemm<FMT, PAIR, AT, WM>), dim3((unsigned)((n + 7) / 8 * 8)),
+                           dim3(128 * WM), 0, s, a);
         const int rc = (int)hipGetLastError();
         if (rc) return rc;
     }
@@ -522,9 +550,13 @@ int launch_at(const MoeArgs& m, GemmArgs& a, hipStream_t s) {
 }
 
 template <int FMT> int launch_fmt(const MoeArgs& m, GemmArgs& a, hipStream_t s) {
-    if constexpr (FMT != T_Q6_K)
-        if (moe_rows(m) == 64) return m.w2 ? launch_at<FMT, true, 2>(m, a, s) : launch_at<FMT, false, 2>(m, a, s);
-    return m.w2 ? launch_at<FMT, true, 4>(m, a, s) : launch_at<FMT, false, 4>(m, a, s);
+    if constexpr (FMT == T_Q6_K) {
+        return m.w2 ? launch_at<FMT, true, 1, 4>(m, a, s) : launch_at<FMT, false, 1, 4>(m, a, s);
+    } else {
+        if (moe_rows(m) == 64)
+            return m.w2 ? launch_at<FMT, true, 1, 2>(m, a, s) : launch_at<FMT, false, 1, 2>(m, a, s);
+        return m.w2 ? launch_at<FMT, true, 2, 2>(m, a, s) : launch_at<FMT, false, 2, 2>(m, a, s);
+    }
 }
 
 }  // namespace
