@@ -392,8 +392,9 @@ __global__ __launch_bounds__(128 * WM, 2) void k_moe_gemm(GemmArgs a) {
             if (have && s.x) flag[h & 3] = 1;
         }
         if (scales) {
-            as[PB][sk][sr] = raw.da;
-            if constexpr (MIN) ac[PB][sk][sr] = raw.ca;
+            // 0 past the row's end here too: the block read in its place may have no finite scale
+            as[PB][sk][sr] = have ? raw.da : 0u;
+            if constexpr (MIN) ac[PB][sk][sr] = have ? raw.ca : 0.0f;
         }
     };
 
@@ -406,7 +407,7 @@ __global__ __launch_bounds__(128 * WM, 2) void k_moe_gemm(GemmArgs a) {
         });
     });
     const v16f zero16 = {};
-    const uint32_t first_k = kq ? 0u : ~0u;   // of the rank-1 product only k = 0 counts
+    const uint32_t first_k = kq ? 0u : ~0u;   // of the rank-1 product only k = 0 counts (in both operands: 0 inf is not 0)
     const int wrow0 = 64 * wn + lr, arow = 32 * AT * wa + lr;
 
     uint32_t apiece = 16 * slot<PR>(arow, kq);        // where the lane's first piece stands
@@ -431,7 +432,7 @@ __global__ __launch_bounds__(128 * WM, 2) void k_moe_gemm(GemmArgs a) {
             each<2>([&](auto i) {
                 const v4h Ws = __builtin_bit_cast(v4h, make_uint2(ws[PB][bk][wrow0 + 32 * i] & first_k, 0u));
                 each<AT>([&](auto j) {
-                    const v4h As = __builtin_bit_cast(v4h, make_uint2(as[PB][bk][arow + 32 * j], 0u));
+                    const v4h As = __builtin_bit_cast(v4h, make_uint2(as[PB][bk][arow + 32 * j] & first_k, 0u));
                     const float ca = MIN ? ac[PB][bk][MIN ? arow + 32 * j : 0] : 0.0f;
                     v16f I = __builtin_amdgcn_mfma_f32_32x32x16_f16(Wf[i][0], Af[j][0], zero16, 0, 0, 0);
                     const v16f S = __builtin_amdgcn_mfma_f32_32x32x8f16(Ws, As, zero16, 0, 0, 0);

@@ -284,3 +284,66 @@ def test_results_beyond_4_gib(g):  # noqa: F811
     del h
     y = g.moe_down(g.Q4_0, w, N, K, idx, torch.ones(T, 1, device="cuda"), h=xd.view(T, 1, K))
     assert (y.view(T // 16, 16, N).view(torch.int32) == dev(p).view(torch.int32)).all()
+
+
+# ------------------------------------------------------- values that are not finite --
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("where", ["rows", "weights"])
+@pytest.mark.parametrize("kernel,down,T,top,E,N,K", [
+    (1, 0, 2, 2, 4, 32, 288), (1, 1, 2, 2, 4, 32, 288), (4, 0, 3, 2, 3, 32, 8192 + 288), (4, 1, 2, 17, 20, 32, 288),
+    (16, 0, 70, 2, 4, 32, 288), (16, 1, 70, 2, 4, 32, 288), (64, 0, 100, 2, 2, 32, 288), (64, 1, 100, 2, 2, 32, 288),
+    (128, 0, 260, 1, 1, 32, 288), (128, 1, 260, 1, 1, 32, 288)])
+def test_values_that_are_not_finite(g, fmt, where, kernel, down, T, top, E, N, K):  # noqa: F811
+    """Infinities, NaN and magnitudes whose scale overflows fp16, in first and last blocks: as in a single product."""
+    K = K if fits(fmt, K) else -(-K // 256) * 256
+    assert g.qmv_moe_rows(fmt, down, T, top, E, N, K) in (kernel, 128 if kernel == 64 else kernel)
+    rng = np.random.default_rng(9)
+    rows = T * top if down else T
+    x = synth.activations(rows, K, 3)
+    blobs = [np.concatenate(expert_blobs(fmt, E, N, K, s)) for s in (1, 2)]
+    if where == "rows":
+        bad = [np.inf, -np.inf, np.nan, 3e7, -3e38, 0.0]
+        for r in range(0, rows, 2):
+            x[r, rng.choice([0, 31, K - 32, K - 1, K // 2])] = bad[(r // 2) % len(bad)]
+        x[1, K - 32:] = 0
+    else:
+        block, size = g.BLOCK[fmt]
+        at = size - 2 if fmt == synth.Q6_K else 0
+        for b in blobs:
+            v = b.reshape(E * N, -1, size)
+            for i, bits in enumerate((0x7C00, 0xFC00, 0x7E00, 0x7BFF)):
+                v[3 * i + 1, (0, -1)[i & 1], at:at + 2] = np.frombuffer(np.uint16(bits).tobytes(), np.uint8)
+    idx = pick(rng, T, top, E, "any")
+    w, u, xd = dev(blobs[0]), dev(blobs[1]), dev(x)
+    one = N * g.row_bytes(fmt, K)
+    pairs = idx.reshape(-1)
+    if down:
+        weight = rng.random((T, top)).astype(np.float32)
+        got = g.moe_down(fmt, w, N, K, dev(idx), dev(weight), h=xd.view(T, top, K)).cpu().numpy()
+        p = torch.stack([g.matvec(fmt, w[e * one:(e + 1) * one], N, K, x=xd[i:i + 1])[0] for i, e in enumerate(pairs)])
+        p = p.view(T, top, N).double()
+        want = torch.zeros(T, N, dtype=torch.float32, device="cuda")
+        for j in range(top):   # fma: the product is exact in 64 bits, and the sum rounded there before it is to f32
+            want = (dev(weight)[:, j, None].double() * p[:, j] + want.double()).float()
+        want = want.cpu().numpy()
+        nan = np.isnan(want)
+        assert np.array_equal(np.isnan(got), nan)
+        inf = np.isinf(want)
+        assert np.array_equal(got[inf], want[inf])
+        fin = ~(nan | inf)
+        bound = (dev(weight)[..., None].double() * p).abs().sum(1).cpu().numpy()
+        assert np.all(np.abs(got[fin].astype(np.float64) - want[fin]) <= bound[fin] * top * 2.0 ** -23)
+    else:
+        got = g.moe_gateup_swiglu(fmt, w, u, N, K, dev(idx), x=xd).view(T * top, N).cpu().numpy()
+        # (K beyond the pair's fused limit: the two products)
+        y = [torch.stack([g.matvec(fmt, m[e * one:(e + 1) * one], N, K, x=xd[i // top:i // top + 1])[0]
+                          for i, e in enumerate(pairs)]).double() for m in (w, u)]
+        want = (y[0] / (1 + torch.exp(-y[0])) * y[1]).float().cpu().numpy()
+        nan, inf = np.isnan(want), np.isinf(want)
+        assert np.array_equal(np.isnan(got), nan)
+        assert np.array_equal(got[inf], want[inf])
+        fin = ~(nan | inf)
+        # both in 64 bits, rounded once
+        assert np.all(np.abs(got[fin].astype(np.float64) - want[fin]) <= np.abs(want[fin]) * 2.0 ** -22 + 2.0 ** -148)

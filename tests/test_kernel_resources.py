@@ -64,3 +64,17 @@ def test_waves_a_simd(kernels):
         if "k_attnI" in name or "k_attn_wide" in name:
             few = "k_attnI" in name and re.search(r"ILi[1-4]E", name)
             assert k["vgpr_count"] <= (168 if few else 256), name
+
+
+def test_experts_kernels(kernels):
+    """No accumulator registers, and the waves a SIMD that each kernel counts with; only the rows kernel's variants of
+    unaligned chunks spill a little."""
+    experts = {n: k for n, k in kernels.items() if "k_moe_" in n}
+    for name, most, spills in (("k_moe_rows", 128, 32), ("k_moe_gemv", 128, 0), ("k_moe_gemm", 256, 0),
+                               ("k_moe_route", 128, 0), ("k_moe_prep", 64, 0), ("k_moe_combine", 64, 0)):
+        found = {n: k for n, k in experts.items() if name in n}
+        assert found
+        for n, k in found.items():
+            assert k["agpr_count"] == 0, n
+            assert k["vgpr_count"] <= most, (n, k["vgpr_count"])
+            assert k["vgpr_spill_count"] <= spills, (n, k["vgpr_spill_count"])
