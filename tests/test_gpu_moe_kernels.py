@@ -347,3 +347,28 @@ def test_values_that_are_not_finite(g, fmt, where, kernel, down, T, top, E, N, K
         fin = ~(nan | inf)
         # both in 64 bits, rounded once
         assert np.all(np.abs(got[fin].astype(np.float64) - want[fin]) <= np.abs(want[fin]) * 2.0 ** -22 + 2.0 ** -148)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("size", [2e-5, 1e-6, 1e6])
+@pytest.mark.parametrize("T,top,E,N,K", [(2, 2, 4, 32, 512), (70, 2, 4, 32, 512), (100, 2, 2, 32, 512),
+                                         (260, 1, 1, 32, 512)])
+def test_scales_that_are_subnormal(g, fmt, size, T, top, E, N, K):  # noqa: F811
+    """fp16 scales below 2^-14 of weights and activations: as in the documented order, bit for bit."""
+    rng = np.random.default_rng(4)
+    x = (synth.activations(T, K, 3) * np.float32(size)).astype(np.float32)
+    block, bytes_ = g.BLOCK[fmt]
+    at = bytes_ - 2 if fmt == synth.Q6_K else 0
+    blobs = [b.copy() for b in expert_blobs(fmt, E, N, K, 1)]
+    for b in blobs:
+        v = b.reshape(N, -1, bytes_)
+        bits = rng.integers(1, 0x400, v.shape[:2]).astype("<u2")
+        bits[::3] |= 0x3800                                      # of a third of the rows normal ones
+        v[:, :, at:at + 2] = bits.view(np.uint8).reshape(*v.shape[:2], 2)
+    idx = pick(rng, T, top, E, "any")
+    h = g.moe_gateup_swiglu(fmt, *[dev(np.concatenate(blobs))] * 2, N, K, dev(idx), x=dev(x)).cpu().numpy()
+    assert_bitwise(h, moe_ref.gateup(fmt, blobs, blobs, N, K, x, idx), "h")
+    one = np.ascontiguousarray(idx[:, :1])
+    y = g.moe_down(fmt, dev(np.concatenate(blobs)), N, K, dev(one), torch.ones(T, 1, device="cuda"),
+                   h=dev(x).view(T, 1, K)).cpu().numpy()
+    assert_bitwise(y, moe_ref.product(fmt, blobs, N, K, x, one[:, 0]) + np.float32(0), "y")
