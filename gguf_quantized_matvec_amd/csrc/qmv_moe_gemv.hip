@@ -1,7 +1,7 @@
 // Experts' products for single tokens and few of them, for gfx950: hardly any
 // two pairs share an expert, so the multiply is a matrix-vector product a pair,
-// bound by the bytes of the experts' weights.  Order and rounding are qmv_launch's (include/qmv.h);
-// every pair's result is bit-identical to it.
+// bound by the bytes of the experts' weights.  Order and rounding are
+// qmv_launch's (include/qmv.h); every pair's result is bit-identical to it.
 //
 // Every lane owns one 256-element chunk of one weight row: it streams the
 // chunk's bytes into registers, forms the codes of a block as int8 and takes
@@ -16,6 +16,11 @@
 // workgroup quantises its token's x itself: one launch.
 // Down: a wave takes one slot's expert and a workgroup all slots of a token for
 // the same rows, whose weighted products it adds itself.
+//
+// Measured for one token, two experts: gate and up of 14336 x 4096 in Q4_K 28.9
+// us (4.6 TB/s; a copy of 2 GiB reaches 4.9), by the kernel of 16 columns 48 for
+// the call; down of 4096 x 14336 in Q6_K 24.2 us (4.0 TB/s) behind a launch of 4
+// that quantises, the call 28.0 against 46.
 //
 // Built with -ffp-contract=off: every float operation is the one written.
 #include <hip/hip_runtime.h>
