@@ -390,18 +390,28 @@ __global__ __launch_bounds__(PAIR ? 64 * WAVES : 64 * MOST_SLOTS) void k_moe_gem
     }
 }
 
+// The launch of a call (K <= 8192 for a gate/up pair, 16384 for a down product).
+struct Grid {
+    int slots, units;   // of a workgroup: slots, and units of rows, a wave each
+    int64_t x;          // workgroups side by side
+    int threads() const { return 64 * slots * units; }
+};
+Grid grid_of(const MoeArgs& m) {
+    const int C = (int)((m.K / 32 + 7) / 8), rows = m.w2 ? 64 / C >> 1 : 64 / C;   // of a unit
+    const int waves = m.w2 ? WAVES : 8, slots = m.w2 ? 1 : m.top;
+    const int units = slots < waves ? waves / slots : 1;
+    const int64_t all = (m.N + rows - 1) / rows;
+    return {slots, units, (all + units - 1) / units};
+}
+
 template <int FMT, bool PAIR, bool LEAN>
 int launch_lean(const MoeArgs& m, GemvArgs& a, hipStream_t s) {
     using F = Fmt<FMT>;
     a.wbytes = m.E * m.N * (m.K / F::QK) * F::BB;
-    const int C = (int)((m.K / 32 + 7) / 8), G = 64 / C, GP = PAIR ? G >> 1 : G;
-    const int waves = PAIR ? WAVES : 8;
-    const int slots = PAIR ? 1 : m.top, units = slots < waves ? waves / slots : 1;   // of a workgroup
-    const int64_t all = (m.N + GP - 1) / GP;
-    const size_t lds = (size_t)slots * moe_gemv_row(m.K, has_min<FMT>()) + slots * units * 256;
-    hipLaunchKernelGGL((k_moe_gemv<FMT, PAIR, LEAN>),
-                       dim3((unsigned)((all + units - 1) / units), (unsigned)(m.P / slots)),
-                       dim3(64 * slots * units), lds, s, a);
+    const Grid g = grid_of(m);
+    const size_t lds = (size_t)g.slots * moe_gemv_row(m.K, has_min<FMT>()) + g.slots * g.units * 256;
+    hipLaunchKernelGGL((k_moe_gemv<FMT, PAIR, LEAN>), dim3((unsigned)g.x, (unsigned)(m.P / g.slots)),
+                       dim3(g.threads()), lds, s, a);
     return (int)hipGetLastError();
 }
 
@@ -432,9 +442,15 @@ bool moe_gemv_fits(const MoeArgs& m) {
     const double experts = m.top < E ? E * (1.0 - pow(1.0 - m.top / E, T)) : E;
     const double matrix = (double)(m.w2 ? 2 : 1) * m.N * row_bytes(m.type, m.K);
     if (T > 1.0 && (matrix > 16e6 || (m.P - experts) * matrix > 60e6)) return false;
-    if (m.w2) return m.K <= 8192;                       // two rows a wave at least
-    return m.K <= 16384 && m.top <= MOST_SLOTS &&
-           m.top * (moe_gemv_row(m.K, min) + 256) + 8 * 256 <= 64 * 1024;
+    if (m.w2) {
+        if (m.K > 8192) return false;                   // two rows a wave at least
+    } else if (m.K > 16384 || m.top > MOST_SLOTS ||
+               m.top * (moe_gemv_row(m.K, min) + 256) + 8 * 256 > 64 * 1024) {
+        return false;
+    }
+    // a grid's dimension ends below 2^32 threads (down: 11 million rows and more)
+    const Grid g = grid_of(m);
+    return g.x * g.threads() < (int64_t)1 << 32;
 }
 
 bool moe_gemv_quantises(const MoeArgs& m) { return m.w2 != nullptr || m.K <= 2048; }
