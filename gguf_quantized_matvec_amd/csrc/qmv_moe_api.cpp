@@ -40,6 +40,22 @@ int check_type(int type, int64_t K) {
     return QMV_EINVAL_TYPE;
 }
 
+// A buffer of a call; p NULL: one that the call does not have.
+struct Buffer {
+    const void* p;
+    int64_t bytes;
+};
+// Whether the outputs (the first `outs` of them) overlap each other or an input.
+template <int N> bool overlap(const Buffer (&b)[N], int outs) {
+    for (int i = 0; i < outs; i++)
+        for (int j = i + 1; j < N; j++) {
+            const uintptr_t u = reinterpret_cast<uintptr_t>(b[i].p), v = reinterpret_cast<uintptr_t>(b[j].p);
+            if (u && v && (u < v ? v - u < (uint64_t)b[i].bytes : u - v < (uint64_t)b[j].bytes)) return true;
+        }
+    return false;
+}
+int64_t blocks_bytes(int64_t rows, int64_t K) { return rows * (K / 32) * 34; }
+
 }  // namespace
 
 extern "C" {
@@ -55,6 +71,8 @@ int qmv_moe_route(const float* logits, int64_t T, int64_t E, int score, const fl
     if (!isfinite(scale)) return QMV_EINVAL_SHAPE;
     if (!logits || !idx || !weight || !aligned(logits, 4) || !aligned(bias, 4) ||
         !aligned(idx, 4) || !aligned(weight, 4))
+        return QMV_EINVAL_PTR;
+    if (overlap({{idx, T * top * 4}, {weight, T * top * 4}, {logits, T * E * 4}, {bias, E * 4}}, 2))
         return QMV_EINVAL_PTR;
     const int rc = check_device();
     if (rc) return rc;
@@ -77,7 +95,12 @@ int qmv_moe_gateup_swiglu(int type, const void* w_gate, const void* w_up, int64_
     if (!w_gate || !w_up || !aligned(w_gate, 16) || !aligned(w_up, 16)) return QMV_EINVAL_PTR;
     if ((x != nullptr) == (xq != nullptr) || !aligned(x, 4) || !aligned(xq, 16))
         return QMV_EINVAL_PTR;
-    if (!idx || !h || !work || !aligned(idx, 4) || !aligned(h, 4) || !aligned(work, 16) || h == x)
+    if (!idx || !h || !work || !aligned(idx, 4) || !aligned(h, 4) || !aligned(work, 16))
+        return QMV_EINVAL_PTR;
+    const int64_t w_bytes = E * N * qmv::row_bytes(type, K);
+    if (overlap({{h, T * top * N * 4}, {work, (int64_t)qmv_moe_gateup_bytes(T, top, E, N, K)},
+                 {x, T * K * 4}, {xq, blocks_bytes(T, K)}, {idx, T * top * 4},
+                 {w_gate, w_bytes}, {w_up, w_bytes}}, 2))
         return QMV_EINVAL_PTR;
     if ((rc = check_device())) return rc;
     const qmv::MoeArgs a{type, static_cast<const uint8_t*>(w_gate),
@@ -101,7 +124,11 @@ int qmv_moe_down(int type, const void* w, int64_t E, int64_t N, int64_t K, const
     if ((h != nullptr) == (hq != nullptr) || !aligned(h, 4) || !aligned(hq, 16))
         return QMV_EINVAL_PTR;
     if (!idx || !weight || !y || !work || !aligned(idx, 4) || !aligned(weight, 4) ||
-        !aligned(y, 4) || !aligned(work, 16) || y == h || y == weight)
+        !aligned(y, 4) || !aligned(work, 16))
+        return QMV_EINVAL_PTR;
+    if (overlap({{y, T * N * 4}, {work, (int64_t)qmv_moe_down_bytes(T, top, E, N, K)},
+                 {h, T * top * K * 4}, {hq, blocks_bytes(T * top, K)}, {idx, T * top * 4},
+                 {weight, T * top * 4}, {w, E * N * qmv::row_bytes(type, K)}}, 2))
         return QMV_EINVAL_PTR;
     if ((rc = check_device())) return rc;
     hipStream_t s = static_cast<hipStream_t>(stream);

@@ -535,25 +535,27 @@ enum qmv_moe_score { QMV_MOE_SOFTMAX = 0, QMV_MOE_SIGMOID = 1 };
  * not available: a logit of these has s = 0, a bias of these leaves s in the
  * softmax's sum.  Where fewer than `top` are, the slots left have idx -1 and
  * weight 0.  An infinite logit is a softmax's whole weight, shared with
- * its equals.  top <= top_groups * (E / groups); scale finite. */
+ * its equals.  top <= top_groups * (E / groups); scale finite.  idx and weight
+ * overlap neither each other nor the inputs (refused). */
 int qmv_moe_route(const float* logits, int64_t T, int64_t E, int score, const float* bias,
                   int groups, int top_groups, int group_top, int top, int renorm, float scale,
                   int32_t* idx, float* weight, void* stream);
 
 /* Bytes of workspace of the two products below (16-byte aligned, used by one
- * call at a time, need not be cleared); 0 for an invalid shape. */
+ * call at a time, need not be cleared); 0 for an invalid shape.  A product's
+ * workspace and result overlap neither each other nor its inputs (refused). */
 size_t qmv_moe_gateup_bytes(int64_t T, int top, int64_t E, int64_t N, int64_t K);
 size_t qmv_moe_down_bytes(int64_t T, int top, int64_t E, int64_t N, int64_t K);
 
 /* Gate and up products of each pair's expert with the SwiGLU:
  *   h[p] = silu(Wg[e] x[t]) * (Wu[e] x[t]),  e = idx[p], t = p / top
  * w_gate, w_up: E matrices N x K of one type; h [T * top][N] f32, 4-byte
- * aligned, overlapping nothing else.  Either x [T][K] f32 is given (4-byte
- * aligned) and quantised into the workspace, or xq (16-byte aligned), whose
- * first T * (K/32) * 34 bytes are the rows' Q8_0 blocks as quantize_act_q8_0
- * or qmv_add_rmsnorm_q8_0 leave them; the other is NULL.  Each row is
- * bit-identical to qmv_launch_gateup_swiglu on that expert's matrices with
- * B = 1, whatever the other pairs are. */
+ * aligned.  Either x [T][K] f32 is given (4-byte aligned) and quantised into
+ * the workspace, or xq (16-byte aligned), whose first T * (K/32) * 34 bytes are
+ * the rows' Q8_0 blocks as quantize_act_q8_0 or qmv_add_rmsnorm_q8_0 leave
+ * them; the other is NULL.  Each row is bit-identical to
+ * qmv_launch_gateup_swiglu on that expert's matrices with B = 1, whatever the
+ * other pairs are. */
 int qmv_moe_gateup_swiglu(int type, const void* w_gate, const void* w_up, int64_t E, int64_t N,
                           int64_t K, const int32_t* idx, int64_t T, int top, const float* x,
                           const void* xq, float* h, void* work, void* stream);
@@ -564,7 +566,7 @@ int qmv_moe_gateup_swiglu(int type, const void* w_gate, const void* w_up, int64_
  * Either h [T * top][K] f32 is given and quantised to Q8_0, or hq holds the
  * rows' Q8_0 blocks, as above.  Each product is bit-identical to qmv_launch on
  * that expert's matrix with B = 1; the sum starts at +0 and adds the slots in
- * ascending order, fma(weight, product, sum).  y overlaps nothing else. */
+ * ascending order, fma(weight, product, sum). */
 int qmv_moe_down(int type, const void* w, int64_t E, int64_t N, int64_t K, const int32_t* idx,
                  const float* weight, int64_t T, int top, const float* h, const void* hq, float* y,
                  void* work, void* stream);
