@@ -79,7 +79,11 @@ __global__ __launch_bounds__(64 * WAVES) void k_moe_route(RouteArgs a) {
         total = sum64(total);
     }
     auto score = [&](float l) -> double {
-        return a.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : part(l) / total;
+        if (!a.sigmoid) return part(l) / total;
+        // exp(-l) ends at 709.78; there the sigmoid is exp(l), a subnormal number
+        const bool low = l < -709.0f;
+        const double t = exp(low ? (double)l : -(double)l);
+        return low ? t : 1.0 / (1.0 + t);
     };
 #pragma unroll
     for (int i = 0; i < V; i++) {
