@@ -73,3 +73,12 @@ def test_outputs_over_other_buffers(entry, where):
             last = lambda n: (b[n] - 1) // 16 * 16               # noqa: E731  the last aligned place inside
             a[out] = {"same": a[other], "first in last": a[other] + last(other), "last in first": a[other] - last(out)}[where]
             assert call(entry, a) == PTR, (out, other)
+
+
+def test_the_kernels_that_other_tests_name():
+    """Both products of the shapes that tests of streams, graphs and alignment run: of 4 rows the gate/up pair is the
+    single tokens' kernel."""
+    pytest.importorskip("torch")
+    from test_gpu_moe_kernels import SOME
+    got = [tuple(g.qmv_moe_rows(g.Q5_0, down, *shape) for down in (0, 1)) for _, *shape in SOME]
+    assert got == [(1, 1), (1, 4), (16, 16), (64, 64), (128, 128)]
