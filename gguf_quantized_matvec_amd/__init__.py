@@ -897,9 +897,13 @@ def moe_route(logits, top: int, score: str = "softmax", bias=None, groups: int =
 def _experts(type, w, N, K, what):
     """(address, number) of the matrices of an expert tensor."""
     import torch
+    if type not in BLOCK:
+        raise QmvError(-1, what)
+    if N < 1 or K < 1 or K % BLOCK[type][0]:
+        raise QmvError(-2, what)
     p = _dev(w, torch.uint8, what)
     one = N * row_bytes(type, K)
-    if one <= 0 or w.numel() == 0 or w.numel() % one:
+    if w.numel() == 0 or w.numel() % one:
         raise ValueError(f"{what} must be whole {N} x {K} matrices of {one} bytes, got {w.numel()} bytes")
     return p, w.numel() // one
 

@@ -82,3 +82,15 @@ def test_the_kernels_that_other_tests_name():
     from test_gpu_moe_kernels import SOME
     got = [tuple(g.qmv_moe_rows(g.Q5_0, down, *shape) for down in (0, 1)) for _, *shape in SOME]
     assert got == [(1, 1), (1, 4), (16, 16), (64, 64), (128, 128)]
+
+
+@pytest.mark.parametrize("type,N,K,code", [(99, 16, 32, -1), (4, 16, 32, -1), (g.Q4_K, 16, 896, -2), (g.Q6_K, 16, 32, -2),
+                                           (g.Q4_0, 16, 48, -2), (g.Q4_0, 0, 32, -2), (g.Q4_0, -16, -32, -2)])
+def test_python_types_and_shapes(type, N, K, code):
+    """The library's own codes, also from the helpers, which need the bytes of a row before they call it."""
+    torch = pytest.importorskip("torch")
+    t = torch.zeros(4, 16)
+    for f, w in ((g.moe_gateup_swiglu, (t, t)), (g.moe_down, (t,))):
+        with pytest.raises(g.QmvError) as e:
+            f(type, *w, N, K, *((t,) if f is g.moe_gateup_swiglu else (t, t)), t)
+        assert e.value.code == code
