@@ -38,48 +38,17 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <type_traits>
-#include <utility>
-
 #include "qmv_moe.h"
+#include "qmv_moe_device.h"
 
 namespace qmv {
 namespace {
-
-constexpr int T_Q4_0 = 2, T_Q4_1 = 3, T_Q5_0 = 6, T_Q5_1 = 7, T_Q8_0 = 8, T_Q8_1 = 9,
-              T_Q4_K = 12, T_Q6_K = 14;
-// The block term has a second part, a minimum times the activation codes' sum.
-template <int FMT> constexpr bool has_min() {
-    return FMT == T_Q4_K || FMT == T_Q4_1 || FMT == T_Q5_1;
-}
-template <int FMT> constexpr int block_elements() { return FMT == T_Q4_K || FMT == T_Q6_K ? 256 : 32; }
-template <int FMT> constexpr int block_bytes() {
-    return FMT == T_Q8_0 ? 34 : FMT == T_Q4_0 ? 18 : FMT == T_Q5_0 ? 22 : FMT == T_Q4_1 ? 20
-         : FMT == T_Q5_1 ? 24 : FMT == T_Q8_1 ? 36 : FMT == T_Q4_K ? 144 : 210;
-}
 
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 v4h __attribute__((ext_vector_type(4)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float v16f __attribute__((ext_vector_type(16)));
-typedef __attribute__((address_space(3))) void lds_void;
-
-__device__ __forceinline__ float half_bits(uint32_t h) {
-    const uint16_t u = (uint16_t)h;
-    _Float16 f;
-    __builtin_memcpy(&f, &u, 2);
-    return (float)f;
-}
-template <class Fn, int... Is>
-__device__ __forceinline__ void each_of(Fn&& f, std::integer_sequence<int, Is...>) {
-    (f(std::integral_constant<int, Is>{}), ...);
-}
-// f(0), f(1), ... f(N - 1) with constants
-template <int N, class Fn> __device__ __forceinline__ void each(Fn&& f) {
-    each_of(f, std::make_integer_sequence<int, N>{});
-}
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // The 16 values are computed here, not later where they are used.
 __device__ __forceinline__ void pin16(float (&v)[16]) {
@@ -88,16 +57,9 @@ __device__ __forceinline__ void pin16(float (&v)[16]) {
                       "+v"(v[15]) : : "memory");
 }
 
-// silu(g) u in f64 as t = exp(-g), s = g / (1 + t), s u, rounded once.
-__device__ __forceinline__ float swiglu(float g, float u) {
-    const double gd = (double)g;
-    const double s = gd / (1.0 + exp(-gd));
-    return (float)(s * (double)u);
-}
-
 // ---------------------------------------------------------------- weights ----
 // The bytes that decode one 32-element block of a row.
-template <int FMT> struct Raw { uint32_t v[(block_bytes<FMT>() + 3) / 4]; };
+template <int FMT> struct Raw { uint32_t v[(block_bytes(FMT) + 3) / 4]; };
 template <> struct Raw<T_Q4_K> { uint32_t hdr[4], q[8]; };           // d, dmin, scales; the block's 32 nibble bytes
 template <> struct Raw<T_Q6_K> { uint32_t ql[8], qh[8], sub, d; };   // sub: the block's two sub-scales
 
@@ -116,7 +78,7 @@ __device__ __forceinline__ void fetch(const uint8_t* row, int b, Raw<FMT>& r) {
         r.sub = *reinterpret_cast<const uint16_t*>(s + 192 + 2 * j);   // not combined here: that would wait for them
         r.d = *reinterpret_cast<const uint16_t*>(s + 208);
     } else {
-        __builtin_memcpy(r.v, row + (int64_t)b * block_bytes<FMT>(), block_bytes<FMT>());
+        __builtin_memcpy(r.v, row + (int64_t)b * block_bytes(FMT), block_bytes(FMT));
     }
 }
 
@@ -132,12 +94,6 @@ __device__ __forceinline__ void codes4(uint32_t c, float bias, uint32_t* o) {
     const _Float16 k = (_Float16)(1024.0f + bias);
     o[0] = as_u32(lower(c) - h2{k, k});
     o[1] = as_u32(upper(c) - h2{k, k});
-}
-
-// Fifth bits: bit j of the nibble h at bit 4 of byte j.  h * 0x204081 holds
-// copies of h at bits 0, 7, 14 and 21, without carries.
-__device__ __forceinline__ uint32_t fifth(uint32_t h) {
-    return (__umul24(h & 15u, 0x204081u) & 0x01010101u) << 4;
 }
 
 struct Scale {
@@ -245,8 +201,8 @@ __device__ __forceinline__ void decode(const Raw<FMT>& r, int b, uint32_t (&o)[1
                 q = __builtin_amdgcn_alignbyte(r.v[QS / 4 + i + 1], r.v[QS / 4 + i], 2);
             uint32_t lo = q & 0x0F0F0F0Fu, hi = (q >> 4) & 0x0F0F0F0Fu;
             if constexpr (five) {
-                lo |= fifth(h >> (4 * i));
-                hi |= fifth(h >> (16 + 4 * i));
+                lo |= spread(h >> (4 * i)) << 4;
+                hi |= spread(h >> (16 + 4 * i)) << 4;
             }
             codes4(lo, bias, o + 2 * i);
             codes4(hi, bias, o + 8 + 2 * i);
@@ -337,7 +293,7 @@ __global__ __launch_bounds__(128 * WM, 2) void k_moe_gemm(GemmArgs a) {
         int64_t n = n0 + (PAIR ? 32 * (sr >> 6) + (sr & 31) : sr);
         if (n >= N) n = N - 1;
         const uint8_t* w = PAIR && (sr & 32) ? a.w2 : a.w;
-        wrow = w + ((int64_t)e * N + n) * (K / block_elements<FMT>() * block_bytes<FMT>());
+        wrow = w + ((int64_t)e * N + n) * (K / block_elements(FMT) * block_bytes(FMT));
     }
     const bool scales = sr < TM;
     const int64_t srow = (int64_t)(pairs[scales ? sr : 0] / a.per) * nb;

@@ -27,37 +27,12 @@
 #include <math.h>
 #include <stdint.h>
 
-#include <type_traits>
-#include <utility>
-
 #include "qmv_moe.h"
+#include "qmv_moe_device.h"
 
 namespace qmv {
 namespace {
 
-typedef __attribute__((address_space(3))) void lds_void;
-
-constexpr int T_Q4_0 = 2, T_Q4_1 = 3, T_Q5_0 = 6, T_Q5_1 = 7, T_Q8_0 = 8, T_Q8_1 = 9,
-              T_Q4_K = 12, T_Q6_K = 14;
-template <int FMT> constexpr bool has_min() {
-    return FMT == T_Q4_K || FMT == T_Q4_1 || FMT == T_Q5_1;
-}
-// QK, BB: elements and bytes of a block; CB: bytes of a chunk of 256 elements.
-template <int FMT> struct Fmt;
-template <> struct Fmt<T_Q8_0> { static constexpr int QK = 32, BB = 34, CB = 272; };
-template <> struct Fmt<T_Q4_0> { static constexpr int QK = 32, BB = 18, CB = 144; };
-template <> struct Fmt<T_Q5_0> { static constexpr int QK = 32, BB = 22, CB = 176; };
-template <> struct Fmt<T_Q4_1> { static constexpr int QK = 32, BB = 20, CB = 160; };
-template <> struct Fmt<T_Q5_1> { static constexpr int QK = 32, BB = 24, CB = 192; };
-template <> struct Fmt<T_Q8_1> { static constexpr int QK = 32, BB = 36, CB = 288; };
-template <> struct Fmt<T_Q4_K> { static constexpr int QK = 256, BB = 144, CB = 144; };
-template <> struct Fmt<T_Q6_K> { static constexpr int QK = 256, BB = 210, CB = 210; };
-// Codes with an offset are formed as a power of two times (code - offset),
-// whose int8 bits are a shift and a flipped top bit away; the power leaves
-// with the activation scale, exactly.
-template <int FMT> constexpr float scale_back() {
-    return FMT == T_Q4_0 ? 1.0f / 16 : FMT == T_Q5_0 ? 1.0f / 8 : FMT == T_Q6_K ? 1.0f / 4 : 1.0f;
-}
 // Chunks start 4-byte aligned always, or (blocks of 18, 22, 34, 210 bytes) only
 // 2-byte aligned: then one dword more is loaded, from the 4-byte aligned address
 // at or below the start, and the bytes are shifted down just before their use
@@ -68,32 +43,6 @@ template <int FMT> constexpr int dwords() { return (Fmt<FMT>::CB + 3) / 4 + (alw
 constexpr int WAVES = 4;          // of a workgroup (gate and up), at least (down)
 constexpr int MOST_SLOTS = 16;    // of a token, a wave each (down)
 constexpr int ACT_STRIDE = 272;   // bytes of a chunk in a row of activations
-
-template <class Fn, int... Is>
-__device__ __forceinline__ void each_of(Fn&& f, std::integer_sequence<int, Is...>) {
-    (f(std::integral_constant<int, Is>{}), ...);
-}
-template <int N, class Fn> __device__ __forceinline__ void each(Fn&& f) {
-    each_of(f, std::make_integer_sequence<int, N>{});
-}
-__device__ __forceinline__ float half_bits(uint32_t h) {
-    const uint16_t u = (uint16_t)h;
-    _Float16 f;
-    __builtin_memcpy(&f, &u, 2);
-    return (float)f;
-}
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ __forceinline__ void wave_sync() {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-// silu(g) u in f64 as t = exp(-g), s = g / (1 + t), s u, rounded once.
-__device__ __forceinline__ float swiglu(float g, float u) {
-    const double gd = (double)g;
-    const double s = gd / (1.0 + exp(-gd));
-    return (float)(s * (double)u);
-}
 
 // The dword (16 bits, byte) at byte O of the chunk's registers.
 template <int O, int W> __device__ __forceinline__ uint32_t dw(const uint32_t (&r)[W]) {
@@ -112,13 +61,9 @@ template <int O, int W> __device__ __forceinline__ int byte(const uint32_t (&r)[
 __device__ __forceinline__ int dot4(uint32_t a, uint32_t b, int c) {
     return __builtin_amdgcn_sdot4((int)a, (int)b, c, false);
 }
-// Bit j of the nibble h at bit 0 of byte j (h * 0x204081: copies at 0, 7, 14, 21).
-__device__ __forceinline__ uint32_t spread(uint32_t h) {
-    return __umul24(h & 15u, 0x204081u) & 0x01010101u;
-}
 
 // The sum of one chunk in the documented order.  act: its 256 activation codes;
-// da, ca: scale (times scale_back) and scale times code sum of its blocks; nbc:
+// da, ca: scale (times gemv_scale_back) and scale times code sum of its blocks; nbc:
 // how many blocks it has (the others are computed and dropped: no branch).
 template <int FMT>
 __device__ __forceinline__ float dot_chunk(const uint32_t (&r)[dwords<FMT>()], const uint8_t* act,
@@ -254,7 +199,7 @@ __device__ __forceinline__ void put_block(uint8_t* act, int C, int b, int sub, u
     *reinterpret_cast<uint32_t*>(act + (b >> 3) * ACT_STRIDE + (b & 7) * 32 + 4 * sub) = c;
     if (sub == 0) {
         float* da = reinterpret_cast<float*>(act + C * ACT_STRIDE);
-        da[b] = d * scale_back<FMT>();
+        da[b] = d * gemv_scale_back(FMT);
         if constexpr (has_min<FMT>()) da[8 * C + b] = d * (float)S;
     }
 }
@@ -281,37 +226,11 @@ __device__ __forceinline__ void stage_row(const GemvArgs& a, int64_t row, uint8_
         const bool live = b < nb;
         uint32_t c = 0;
         float d = 0.0f;
-        if (a.x) {
-            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (live) {
-                const float* x = a.x + row * a.K + 32 * b + 4 * sub;
-                if (a.a16) {
-                    const float4 f = *reinterpret_cast<const float4*>(x);
-                    v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; i++) v[i] = x[i];
-                }
-            }
-            float amax = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
-            const float q = amax / 127.0f;
-            const float r = 1.0f / q, id = __builtin_isinf(r) ? 0.0f : r;
-#pragma unroll
-            for (int i = 0; i < 4; i++) c |= ((uint32_t)(int)roundf(v[i] * id) & 0xFFu) << (8 * i);
-            d = (float)(_Float16)q;
-        } else if (live) {
-            const uint16_t* in = reinterpret_cast<const uint16_t*>(a.blocks + (row * nb + b) * 34);
-            c = (uint32_t)in[1 + 2 * sub] | ((uint32_t)in[2 + 2 * sub] << 16);
-            d = half_bits(in[0]);
-        }
-        int S = 0;
-        if constexpr (has_min<FMT>()) {
-            S = dot4(c, 0x01010101u, 0);
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) S += __shfl_xor(S, o);
-        }
+        if (a.x)
+            d = quantise_block(a.x + row * a.K + 32 * b + 4 * sub, live, a.a16, c);
+        else if (live)
+            d = read_block(a.blocks + (row * nb + b) * 34, sub, c);
+        const int S = has_min<FMT>() ? block_sum(c) : 0;
         if (live) put_block<FMT>(act, C, b, sub, c, d, S);
     }
 }
@@ -426,7 +345,6 @@ template <int FMT> int launch_fmt(const MoeArgs& m, GemvArgs& a, hipStream_t s) 
 }  // namespace
 
 bool moe_gemv_fits(const MoeArgs& m) {
-    const bool min = m.type == T_Q4_K || m.type == T_Q4_1 || m.type == T_Q5_1;
     // Every pair reads its expert's weights here, once a pair; there once an
     // expert, behind a second launch.  So by the bytes that repeated experts
     // would read again, as far as the experts of different tokens are
@@ -445,7 +363,7 @@ bool moe_gemv_fits(const MoeArgs& m) {
     if (m.w2) {
         if (m.K > 8192) return false;                   // two rows a wave at least
     } else if (m.K > 16384 || m.top > MOST_SLOTS ||
-               m.top * (moe_gemv_row(m.K, min) + 256) + 8 * 256 > 64 * 1024) {
+               m.top * (moe_gemv_row(m.K, type_has_min(m.type)) + 256) + 8 * 256 > 64 * 1024) {
         return false;
     }
     // a grid's dimension ends below 2^32 threads (down: 11 million rows and more)

@@ -32,35 +32,19 @@
 #include <stdint.h>
 
 #include <atomic>
-#include <type_traits>
-#include <utility>
 
 #include "qmv_moe.h"
+#include "qmv_moe_device.h"
 
 namespace qmv {
 namespace {
 
-constexpr int T_Q4_0 = 2, T_Q4_1 = 3, T_Q5_0 = 6, T_Q5_1 = 7, T_Q8_0 = 8, T_Q8_1 = 9,
-              T_Q4_K = 12, T_Q6_K = 14;
-
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
-// QK, BB: elements and bytes of a block; CB: bytes of a chunk of 256 elements;
-// PPS: 16-byte pieces that cover a chunk at the worst alignment of its start.
-template <int FMT> struct Fmt;
-template <> struct Fmt<T_Q8_0> { static constexpr int QK = 32, BB = 34, CB = 272, PPS = 18; };
-template <> struct Fmt<T_Q4_0> { static constexpr int QK = 32, BB = 18, CB = 144, PPS = 10; };
-template <> struct Fmt<T_Q5_0> { static constexpr int QK = 32, BB = 22, CB = 176, PPS = 12; };
-template <> struct Fmt<T_Q4_1> { static constexpr int QK = 32, BB = 20, CB = 160, PPS = 11; };
-template <> struct Fmt<T_Q5_1> { static constexpr int QK = 32, BB = 24, CB = 192, PPS = 13; };
-template <> struct Fmt<T_Q8_1> { static constexpr int QK = 32, BB = 36, CB = 288, PPS = 19; };
-template <> struct Fmt<T_Q4_K> { static constexpr int QK = 256, BB = 144, CB = 144, PPS = 9; };
-template <> struct Fmt<T_Q6_K> { static constexpr int QK = 256, BB = 210, CB = 210, PPS = 14; };
-
-// The block term has a second part, a minimum times the activation codes' sum.
-template <int FMT> constexpr bool has_min() {
-    return FMT == T_Q4_K || FMT == T_Q4_1 || FMT == T_Q5_1;
+// 16-byte pieces that cover a chunk at the worst alignment of its start.
+template <int FMT> constexpr int pieces() {
+    return (16 - std::gcd(Fmt<FMT>::BB, 16) + Fmt<FMT>::CB + 15) / 16;
 }
 // Blocks of 16 bytes of nibbles: element e < 16 the low one of byte e, e + 16 the high one.
 template <int FMT> constexpr bool nibble_block() {
@@ -76,46 +60,13 @@ template <int FMT> constexpr float scale_back() {
 // the chunk a multiple of 16 bytes).  LDS rows are an odd number of pieces
 // long, so that 16 rows' same piece meets all banks.
 template <int FMT> constexpr bool can_align() { return Fmt<FMT>::CB % 16 == 0; }
-template <int FMT, bool AL> constexpr int row_pieces() { return AL ? Fmt<FMT>::CB / 16 : Fmt<FMT>::PPS; }
+template <int FMT, bool AL> constexpr int row_pieces() { return AL ? Fmt<FMT>::CB / 16 : pieces<FMT>(); }
 template <int FMT, bool AL> constexpr int row_stride() { return 16 * (row_pieces<FMT, AL>() | 1); }
 template <int FMT, bool AL> constexpr int slice() { return 16 * row_stride<FMT, AL>(); }
 
 constexpr int WAVES = 8;
 constexpr int SEG = 16;
 constexpr int ACT_STRIDE = 272;   // a row's 256 codes of a chunk, and 16 bytes so that rows differ in their banks
-
-__device__ __forceinline__ float half_bits(uint32_t h) {
-    const uint16_t u = (uint16_t)h;
-    _Float16 f;
-    __builtin_memcpy(&f, &u, 2);
-    return (float)f;
-}
-template <typename T> __device__ __forceinline__ T ld(const uint8_t* p) {
-    T v;
-    __builtin_memcpy(&v, p, sizeof(T));
-    return v;
-}
-template <class Fn, int... Is>
-__device__ __forceinline__ void each_of(Fn&& f, std::integer_sequence<int, Is...>) {
-    (f(std::integral_constant<int, Is>{}), ...);
-}
-// f(0), f(1), ... f(N - 1) with constants
-template <int N, class Fn> __device__ __forceinline__ void each(Fn&& f) {
-    each_of(f, std::make_integer_sequence<int, N>{});
-}
-__device__ __forceinline__ void wave_sync() {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-
-// silu(g) u in f64 as t = exp(-g), s = g / (1 + t), s u, rounded once.
-__device__ __forceinline__ float swiglu(float g, float u) {
-    const double gd = (double)g;
-    const double s = gd / (1.0 + exp(-gd));
-    return (float)(s * (double)u);
-}
 
 // ----------------------------------------------------------- preparation ----
 // One launch before the product: workgroups 0 .. E sort the pairs (only beyond
@@ -222,37 +173,14 @@ __global__ __launch_bounds__(PREP) void k_moe_prep(PrepArgs a) {
     const bool live = b < a.nblocks;
     uint32_t c = 0;
     _Float16 d16 = 0;
-    if (a.x) {
-        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (live) {
-            const float* xb = a.x + b * 32 + 4 * sub;
-            if (a.a16) {
-                const float4 f = *reinterpret_cast<const float4*>(xb);
-                v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; i++) v[i] = xb[i];
-            }
-        }
-        float amax = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
-        const float d = amax / 127.0f;
-        const float r = 1.0f / d, id = __builtin_isinf(r) ? 0.0f : r;
-#pragma unroll
-        for (int i = 0; i < 4; i++) c |= ((uint32_t)(int)roundf(v[i] * id) & 0xFFu) << (8 * i);
-        d16 = (_Float16)d;
-    } else if (live) {
-        const uint16_t* in = reinterpret_cast<const uint16_t*>(a.xq + b * 34);
-        c = (uint32_t)in[1 + 2 * sub] | ((uint32_t)in[2 + 2 * sub] << 16);
-        __builtin_memcpy(&d16, in, 2);
-    }
+    if (a.x)
+        d16 = quantise_block(a.x + b * 32 + 4 * sub, live, a.a16, c);
+    else if (live)
+        d16 = read_block(a.xq + b * 34, sub, c);
     uint16_t dbits;
     __builtin_memcpy(&dbits, &d16, 2);
     if (a.gemm || a.row) {
-        int S = __builtin_amdgcn_sdot4((int)c, 0x01010101, 0, false);
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) S += __shfl_xor(S, o);
+        const int S = block_sum(c);
         if (!live) return;
         if (a.row) {
             const int64_t r = b / a.nb;
@@ -401,12 +329,10 @@ __device__ __forceinline__ void chunk_rows(const Fields<AL>& rb, const uint8_t* 
                     w[0] = v & 0x0F0F0F0Fu;
                     w[1] = (v >> 4) & 0x0F0F0F0Fu;
                 } else {
-                    // fifth bits of elements 4kg .. 4kg+3 and 16 + 4kg ..: h * 0x204081 puts
-                    // bit j of a nibble h at bit 8 j (plus others, masked off), without carries
+                    // fifth bits of elements 4kg .. 4kg+3 and 16 + 4kg ..
                     rb.template get<O + (FMT == T_Q5_0 ? 2 : 4), 1>(0, one);
                     const uint32_t h = one[0] >> (4 * kg);
-                    const uint32_t l5 = __umul24(h & 15u, 0x204081u) & 0x01010101u;
-                    const uint32_t h5 = __umul24((h >> 16) & 15u, 0x204081u) & 0x01010101u;
+                    const uint32_t l5 = spread(h), h5 = spread(h >> 16);
                     if constexpr (FMT == T_Q5_0) {
                         w[0] = (((v << 3) & 0x78787878u) | (l5 << 7)) ^ 0x80808080u;
                         w[1] = (((v >> 1) & 0x78787878u) | (h5 << 7)) ^ 0x80808080u;
@@ -886,10 +812,10 @@ static int prepare(const MoeArgs& m, bool plan, bool gemm, bool gemv, hipStream_
     p.nblocks = m.x || gemm ? m.P / m.per * (m.K / 32) : 0;
     p.gemm = gemm;
     if (gemv) {
-        p.min = m.type == T_Q4_K || m.type == T_Q4_1 || m.type == T_Q5_1;
+        p.min = type_has_min(m.type);
         p.row = moe_gemv_row(m.K, p.min);
         p.nb = (int32_t)(m.K / 32);
-        p.back = m.type == T_Q4_0 ? 1.0f / 16 : m.type == T_Q5_0 ? 1.0f / 8 : m.type == T_Q6_K ? 1.0f / 4 : 1.0f;
+        p.back = gemv_scale_back(m.type);
     }
     p.idx = m.idx;
     p.P = (int32_t)m.P;
