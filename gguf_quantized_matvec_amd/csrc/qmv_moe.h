@@ -51,7 +51,10 @@ struct MoeArgs {
 //   down Q5_0, 16 of 896 x 4864           65  92 123    86  96 127   145  129  139   264  188  196
 //   down Q6_K, 8 of 4096 x 14336         321  -  305   534  -  597   979   -   760  1873   -  1228
 // (Q6_K has no tile of 64, whose decoding it would not share enough, and costs
-// the matrix products of 16 columns two dots a block.)
+// the matrix products of 16 columns two dots a block.)  One rule for all but
+// Q6_K costs the others' types where they part: at 96 pairs 64 gains for Q4_0
+// and loses 4 % to 16 rows (7 % to 128) for Q4_K and 12 % for Q5_0, at 192 it
+// loses 4 % to 128 for Q4_K.
 inline int moe_rows(int type, int64_t P, int top, int64_t E) {
     if (type == QMV_Q6_K) {
         if (P >= 48 * E) return 128;

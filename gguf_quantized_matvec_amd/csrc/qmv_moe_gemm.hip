@@ -27,9 +27,11 @@
 // 32 takes 24, 32 x 32 (16 waves) 32.  Measured at 2048 tokens, 2 of 8 experts
 // of 2 x 14336 x 4096 (4096 x 14336): Q4_0 1823 (1091) us, with 64 x 32 2047
 // (1159), with 32 x 32 2369; Q4_K 2488 (1499), 2649 (1499), 2687; Q8_0 2030,
-// 2241, 2212; Q6_K down 1528 with 64 x 32, 1561 with 64 x 64, 2319 with 32 x 32.
-// That is 315 to 530 TFLOP/s.  Matrix cores 24 to 35 % busy, vector units 45 to
-// 60 %: of a tile's block 96 cycles of MFMA, but 16 fma of 4 cycles (32 with a
+// 2241, 2212; Q6_K down 1528 with 64 x 32, 1561 with 64 x 64, 2319 with 32 x 32
+// (one run of the forms in turn; by card and inputs Q4_K's 2488 is 2490 to 2650.)
+// That is 315 to 530 TFLOP/s.  Matrix cores 36 (Q4_0), 26 (Q4_K), 21 % (Q6_K) busy,
+// vector units 56, 62, 41 %, LDS 30, 43, 24 %, a third of the waves' time waiting:
+// of a tile's block 96 cycles of MFMA, but 16 fma of 4 cycles (32 with a
 // minimum) and 15 to 20 operations of the decoding, which the tile's rows
 // share.  Without the decoding 16 waves took 1550 instead of 2369 us.  Half of
 // 8 waves decoding after they multiply instead of before gave 4 % for Q4_K and

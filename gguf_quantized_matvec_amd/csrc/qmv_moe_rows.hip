@@ -19,8 +19,8 @@
 // Few rows are bound by the weights' bytes, more by the f32 term a block and row
 // and the decoding, which only an item's rows share.  Measured (the product's
 // launch alone): 32 tokens, 8 of 64 experts of 2 x 1024 x 2048 in Q4_0 34.4 us
-// (4.4 TB/s); 16 tokens, 2 of 8 of 4096 x 14336 in Q4_K 70.9 (3.7 TB/s); 300
-// tokens, 4 of 16 of 896 x 4864 in Q5_0 63.5 (160 TFLOP/s).
+// (4.4 TB/s); 16 tokens, 2 of 8 of 4096 x 14336 in Q4_K 70.9 to 73 (3.7 TB/s); 300
+// tokens, 4 of 16 of 896 x 4864 in Q5_0 63.5 to 71 (by run; 147 to 165 TFLOP/s).
 //
 // Order inside a block does not matter (the integers are exact), so lane kg
 // takes bytes 4kg .. 4kg+3 of a 16-byte nibble block, low and high nibbles,
